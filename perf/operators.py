@@ -176,8 +176,10 @@ def prepare_adam(c, gen):
     if c["state"] == "f32":
         s["m"], s["v"] = m, [t * t for t in r]
         return s
-    s["m"], s["ms"] = map(list, zip(*[quantised(t) for t in m]))
-    s["r"], s["rs"] = map(list, zip(*[quantised(t) for t in r]))
+    s["seed"] = 77
+    bits = [dither(n, 1, 1) for n in sizes]
+    s["m"], s["ms"] = map(list, zip(*[quantised(t, x >> 12) for t, x in zip(m, bits)]))
+    s["r"], s["rs"] = map(list, zip(*[quantised(t, x & 0xFFFFF) for t, x in zip(r, bits)]))
     return s
 
 
@@ -188,12 +190,24 @@ def blocks(t):
     return torch.nn.functional.pad(t, (0, -t.numel() % BLOCK)).reshape(-1, BLOCK)
 
 
-def quantised(t):
-    """e4m3 codes of t over one float scale (the largest magnitude, at least 2^-100, / 448) per BLOCK elements."""
+def dither(n, seed, step):
+    """32 bits per element from its index, the seed and the step; m takes the upper 20, the root the lower 20."""
+    key = (seed + step * 0x9E3779B9) & 0xFFFFFFFF
+    key = (key ^ key >> 16) * 0x85EBCA77 & 0xFFFFFFFF
+    x = (torch.arange(n, device=DEV) * 0x9E3779B1 + (key ^ key >> 13)) & 0xFFFFFFFF
+    x = (x ^ x >> 15) * 0x85EBCA77 & 0xFFFFFFFF
+    return x ^ x >> 13
+
+
+def quantised(t, bits):
+    """e4m3 codes of t over one float scale (the largest magnitude, at least 2^-100, / 448) per BLOCK elements:
+    a value between two codes takes the upper one with a probability of its place between them, by 20 bits."""
     b = blocks(t)
     top = b.abs().amax(1).clamp(min=2.0 ** -100)
-    codes = (b * (448.0 / top)[:, None]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
-    return codes.reshape(-1)[:t.numel()].clone(), top * (1.0 / 448.0)
+    y = (b * (448.0 / top)[:, None]).reshape(-1)[:t.numel()]
+    low = torch.where(y.abs() < 2.0 ** -6, 2.0 ** -6, 0.0)  # there the codes are 2^-9 apart, as above 2^-6
+    z = ((y.abs().clamp(max=448.0) + low).view(torch.int32) + bits.int()) & -0x100000
+    return torch.copysign(z.view(torch.float32) - low, y).to(torch.float8_e4m3fn), top * (1.0 / 448.0)
 
 
 def dequantised(codes, scale):
@@ -271,8 +285,9 @@ def plain_adamw(s):
     if s["master"]:
         torch._foreach_copy_(s["master"], w)
     if q8:
-        m, ms = zip(*[quantised(t) for t in m])
-        r, rs = zip(*[quantised(t) for t in r])
+        bits = [dither(t.numel(), s["seed"], s["step"]) for t in m]
+        m, ms = zip(*[quantised(t, x >> 12) for t, x in zip(m, bits)])
+        r, rs = zip(*[quantised(t, x & 0xFFFFF) for t, x in zip(r, bits)])
         [a.copy_(b) for a, b in zip(s["m"] + s["ms"] + s["r"] + s["rs"], m + ms + r + rs)]
     else:
         torch._foreach_copy_(s["m"], m)
@@ -335,7 +350,7 @@ def own_adamw(s):
         s["table"] = N.adamw_tensors(s["p"], s["g"], s["m"], s["r" if q8 else "v"], s["master"] or None,
                                      s["ms"] if q8 else None, s["rs"] if q8 else None)
     N.moe_adamw(s["table"], lr=s["lr"], beta1=s["b1"], beta2=s["b2"], eps=s["eps"], weight_decay=s["wd"], step=s["step"],
-                grad_scale=s["scale"])
+                grad_scale=s["scale"], seed=s.get("seed", 0))
     return adam_outputs(s)
 
 
@@ -415,11 +430,27 @@ def exact_combine_backward(s):
     return {"dy_perm": rows, "dw": dw}
 
 
-def e4m3(y):
-    """The e4m3 values next to y: 3 bits below the leading one, a grid of 2^-9 under 2^-6, ties to even, at most 448."""
-    y = y.clamp(-448, 448)
-    grid = torch.ldexp(torch.ones_like(y), torch.frexp(y.abs().clamp(min=2.0 ** -6))[1].sub(4))
-    return torch.round(y / grid) * grid
+def random_words(n, seed, step):
+    """The dither's definition on unsigned 32-bit words, by 16-bit halves that 64 bits hold exactly."""
+    word = 1 << 32
+
+    def times(x, c):
+        return (x * (c % 65536) + (x * (c // 65536) % 65536) * 65536) % word
+
+    key = (seed + step * 2654435769) % word
+    key = (key ^ (key // 65536)) * 2246822519 % word
+    key ^= key // 8192
+    x = (times(torch.arange(n, device=DEV), 2654435761) + key) % word
+    x = times(x ^ (x // 32768), 2246822519)
+    return x ^ (x // 8192)
+
+
+def e4m3(y, place):
+    """The e4m3 value next below y, or above it where y's place between the two is past 1 - place: 3 bits below
+    the leading one, a grid of 2^-9 under 2^-6, at most 448."""
+    a = y.abs().clamp(max=448)
+    grid = torch.ldexp(torch.ones_like(a), torch.frexp(a.clamp(min=2.0 ** -6))[1].sub(4))
+    return torch.sign(y) * torch.floor(a / grid + place) * grid
 
 
 def exact_adamw(s):
@@ -445,9 +476,10 @@ def exact_adamw(s):
             out["m"].append(m)
             out["v"].append(v)
             continue
-        for name, t in (("m", m), ("r", v.sqrt())):
+        words = random_words(g.numel(), s["seed"], s["step"])
+        for name, t, bits in (("m", m, words // 4096), ("r", v.sqrt(), words % 1048576)):
             top = torch.zeros(s[name + "s"][i].numel(), dtype=torch.float64, device=DEV)
             top.scatter_reduce_(0, block, t.abs(), "amax").clamp_(min=2.0 ** -100)
-            out[name].append(e4m3(t * 448 / top[block]))
+            out[name].append(e4m3(t * 448 / top[block], bits.double() / 1048576))
             out[name + "s"].append(top / 448)
     return out
