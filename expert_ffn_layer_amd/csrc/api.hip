@@ -7,6 +7,7 @@
 #include <mutex>
 #include <string>
 
+#include "api_util.h"
 #include "common.h"
 #include "kernels.h"
 
@@ -16,12 +17,9 @@ extern "C" __attribute__((visibility("hidden"))) hipError_t moe_launch_pack(int 
                                                                          const void* scale, void* packed,
                                                                          void* packed_scale, hipStream_t stream);
 
-namespace {
+static thread_local std::string g_last_error;
 
-thread_local std::string g_last_error;
-
-moe_status fail(moe_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-moe_status fail(moe_status s, const char* fmt, ...) {
+moe_status moe::fail(moe_status s, const char* fmt, ...) {
   char buf[512];
   va_list ap;
   va_start(ap, fmt);
@@ -31,12 +29,14 @@ moe_status fail(moe_status s, const char* fmt, ...) {
   return s;
 }
 
-moe_status hip_status(hipError_t e, const char* what) {
+moe_status moe::hip_status(hipError_t e, const char* what) {
   if (e == hipSuccess) return MOE_OK;
   return fail(MOE_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-constexpr size_t ALIGN = 256;
+namespace {
+
+constexpr size_t ALIGN = WS_ALIGN;
 size_t up(size_t x, size_t a = ALIGN) { return (x + a - 1) / a * a; }
 int act_bytes(moe_dtype a) { return a == MOE_F32 ? 4 : 2; }
 int pad64(int n) { return (n + 63) / 64 * 64; }
@@ -76,7 +76,9 @@ moe_status packed_sizes(moe_dtype fmt, int count, int K, int N, size_t* bytes, s
   return MOE_OK;
 }
 
-moe_status check_shape(const moe_shape* s) {
+}  // namespace
+
+moe_status moe::check_shape(const moe_shape* s) {
   if (!s) return fail(MOE_ERR_INVALID_ARG, "shape is NULL");
   if (s->T < 0) return fail(MOE_ERR_INVALID_ARG, "T=%d < 0", s->T);
   if (s->H < 128 || s->H % 128) return fail(MOE_ERR_INVALID_ARG, "H=%d must be a positive multiple of 128", s->H);
@@ -127,6 +129,8 @@ moe_status check_shape(const moe_shape* s) {
                 "and H a multiple of 512");
   return MOE_OK;
 }
+
+namespace {
 
 // Split-K factor of the router scores: enough workgroups (about 512) to stream Wr at full rate
 // when T is small; every part keeps at least 8 packets of the reduction.

@@ -55,3 +55,90 @@ class PackedLayer:
         N.moe_layer_forward(self.shape, x, self.Wr, bias, self.routed, self.shared, y, topk_idx, topk_w,
                             self.ws, stream)
         return y
+
+
+class TrainableLayer:
+    """One layer's experts in training: forward, backward and AdamW step over row-major weights of the
+    activations' type (gate, up [E, H, I], down [E, I, H]; the shared expert's without the first axis or
+    with one of 1). The router is read only; its scores' gradient follows from backward's routing-weight
+    gradient. Allocation and marshalling only, like PackedLayer.
+
+    forward keeps what backward reads, for the last batch alone. state: "f32", or "e4m3" for 8-bit
+    optimizer states; master: fp32 master copies of bf16 weights."""
+
+    NAMES = ("gate", "up", "down")
+
+    def __init__(self, spec, Wr: torch.Tensor, routed: dict, shared: dict | None = None, T: int | None = None,
+                 state: str = "f32", master: bool = False):
+        self.H, self.I, self.E, self.k, self.act = spec.H, spec.I, spec.E, spec.k, spec.act
+        self.Wr, _ = pack(spec.act, Wr.reshape(1, spec.H, spec.E), None, spec.H, spec.E)
+        self.dtype = torch.float32 if spec.act == "f32" else torch.bfloat16
+        self.weights = [{n: routed[n] for n in self.NAMES}]
+        if shared is not None:
+            self.weights.append({n: shared[n] for n in self.NAMES})
+        self.grads = [{n: torch.zeros_like(t) for n, t in w.items()} for w in self.weights]
+        p = [w[n] for w in self.weights for n in self.NAMES]
+        g = [d[n] for d in self.grads for n in self.NAMES]
+        if state == "e4m3":
+            m, v = ([torch.zeros(t.numel(), dtype=torch.uint8, device=t.device) for t in p] for _ in range(2))
+            ms, vs = ([torch.zeros((t.numel() + 255) // 256, device=t.device) for t in p] for _ in range(2))
+        elif state == "f32":
+            m, v = ([torch.zeros(t.shape, device=t.device) for t in p] for _ in range(2))
+            ms = vs = None
+        else:
+            raise ValueError("state is f32 or e4m3")
+        copies = [t.float() for t in p] if master else None
+        self.optimizer = N.adamw_tensors(p, g, m, v, copies, ms, vs)
+        self.steps = 0
+        self.set_tokens(spec.T if T is None else T)
+
+    def _shape(self, T, E, k):
+        return N.make_shape(T, self.H, E, k, self.I, act=self.act, w_routed=self.act)
+
+    def set_tokens(self, T: int):
+        """Buffers for batches of T tokens."""
+        dev, P, act = self.Wr.device, T * self.k, dict(dtype=self.dtype, device=self.Wr.device)
+        self.T = T
+        self.shapes = [self._shape(T, self.E, self.k)] + [self._shape(T, 1, 1)] * (len(self.weights) - 1)
+        ws = max(N.moe_workspace_size(self.shapes[0]), *[N.moe_train_workspace_size(s) for s in self.shapes])
+        self.ws = torch.empty(ws, dtype=torch.uint8, device=dev)
+        self.idx, self.pair_slot = (torch.empty((T, self.k), dtype=torch.int32, device=dev) for _ in range(2))
+        self.w, self.dw = (torch.empty((T, self.k), dtype=torch.float32, device=dev) for _ in range(2))
+        self.ones = torch.ones((T, self.k), dtype=torch.float32, device=dev)
+        self.off = torch.zeros(self.E + 1, dtype=torch.int32, device=dev)
+        self.slot_token = torch.empty(P, dtype=torch.int32, device=dev)
+        rows = [P] + [T] * (len(self.weights) - 1)
+        self.pre = [[torch.empty((r, self.I), **act) for _ in range(2)] for r in rows]
+        self.y, self.dx = ([torch.empty((r, self.H), **act) for r in rows] for _ in range(2))
+        self.dy_perm = torch.empty((P, self.H), **act)
+        self.x = None
+
+    def forward(self, x, bias=None, stream=None):
+        """y [T, H]; routing as moe_route, kept in idx and w."""
+        y = torch.empty_like(x)
+        N.moe_route_permute(self.shapes[0], x, self.Wr, bias, self.idx, self.w, self.off, self.slot_token,
+                            self.pair_slot, self.ws, stream)
+        groups = [(self.off, self.slot_token), (None, None)]
+        for shape, group, w, pre, out in zip(self.shapes, groups, self.weights, self.pre, self.y):
+            N.moe_gated_ffn(shape, x, *group, w, *pre, out, self.ws, stream)
+        N.moe_combine(self.shapes[0], self.y[0], self.pair_slot, self.w, self.y[1] if len(self.y) > 1 else None, y, stream)
+        self.x = x
+        return y
+
+    def backward(self, dy, stream=None):
+        """(dx through the experts [T, H], gradient of the routing weights [T, k]); fills grads."""
+        if self.x is None:
+            raise RuntimeError("backward needs a forward pass on this batch size")
+        dx = torch.empty_like(dy)
+        N.moe_combine_backward(self.shapes[0], dy, self.y[0], self.pair_slot, self.w, self.dy_perm, self.dw, stream)
+        groups = [(self.off, self.slot_token, self.dy_perm), (None, None, dy)]
+        for shape, (off, slot, d), w, pre, out, grads in zip(self.shapes, groups, self.weights, self.pre, self.dx, self.grads):
+            N.moe_gated_ffn_backward(shape, self.x, off, slot, w, *pre, d, out, grads, self.ws, stream)
+        N.moe_combine(self.shapes[0], self.dx[0], self.pair_slot, self.ones, self.dx[1] if len(self.dx) > 1 else None, dx,
+                      stream)
+        return dx, self.dw
+
+    def step(self, lr, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.0, stream=None, **more):
+        """One AdamW step of every expert matrix by grads; more: moe_adamw's lr_dev, step_dev, grad_scale, seed."""
+        self.steps += 1
+        N.moe_adamw(self.optimizer, lr, beta1, beta2, eps, weight_decay, self.steps, stream=stream, **more)

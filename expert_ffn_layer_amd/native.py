@@ -20,7 +20,8 @@ STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
 EXPORTS = ("moe_status_string", "moe_last_error", "moe_pack_size", "moe_pack", "moe_workspace_size",
            "moe_route", "moe_route_hash", "moe_permute", "moe_route_permute", "moe_grouped_ffn", "moe_combine",
            "moe_layer_forward", "moe_layer_forward_noalloc", "moe_layer_forward_hash", "moe_layer_forward_timed",
-           "moe_quantize_mxfp8", "moe_quantize_int8", "moe_logical_workspace_size", "moe_layer_forward_logical")
+           "moe_quantize_mxfp8", "moe_quantize_int8", "moe_logical_workspace_size", "moe_layer_forward_logical",
+           "moe_train_workspace_size", "moe_gated_ffn", "moe_gated_ffn_backward", "moe_combine_backward", "moe_adamw")
 # the library's own scratch, the workspace of moe_layer_forward_noalloc
 NOALLOC_SCRATCH_BYTES = 64 << 20
 TIMED_EVENTS = 7
@@ -43,6 +44,20 @@ class MoeWeights(ctypes.Structure):
     _fields_ = [("gate", ctypes.c_void_p), ("up", ctypes.c_void_p), ("down", ctypes.c_void_p),
                 ("gate_scale", ctypes.c_void_p), ("up_scale", ctypes.c_void_p),
                 ("down_scale", ctypes.c_void_p)]
+
+
+class MoeWeightGrads(ctypes.Structure):
+    _fields_ = [("gate", ctypes.c_void_p), ("up", ctypes.c_void_p), ("down", ctypes.c_void_p)]
+
+
+class MoeAdamwTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("p", "g", "m", "v", "m_scale", "v_scale", "master")] + [("n", ctypes.c_int64)]
+
+
+class MoeAdamwConfig(ctypes.Structure):
+    _fields_ = [("p_type", ctypes.c_int), ("g_type", ctypes.c_int), ("state", ctypes.c_int)] + \
+               [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")] + \
+               [("step", ctypes.c_int64), ("seed", ctypes.c_uint32)] + [(n, ctypes.c_void_p) for n in ("lr_dev", "step_dev", "grad_scale")]
 
 
 _lib = None
@@ -79,6 +94,11 @@ def load() -> ctypes.CDLL:
         lib.moe_quantize_int8.argtypes = [P, I32, I32, P, P, P]
         lib.moe_logical_workspace_size.argtypes = [PS, ctypes.POINTER(SZ)]
         lib.moe_layer_forward_logical.argtypes = [PS, P, P, P, PW, PW, P, P, P, P, SZ, P]
+        lib.moe_train_workspace_size.argtypes = [PS, ctypes.POINTER(SZ)]
+        lib.moe_gated_ffn.argtypes = [PS, P, P, P, PW, P, P, P, P, SZ, P]
+        lib.moe_gated_ffn_backward.argtypes = [PS, P, P, P, PW, P, P, P, P, ctypes.POINTER(MoeWeightGrads), P, SZ, P]
+        lib.moe_combine_backward.argtypes = [PS, P, P, P, P, P, P, P]
+        lib.moe_adamw.argtypes = [ctypes.POINTER(MoeAdamwConfig), ctypes.POINTER(MoeAdamwTensor), I32, P]
         for name in EXPORTS[2:]:
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
@@ -98,6 +118,14 @@ def _stream(stream=None):
     import torch
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _device_of(t):
+    """The tensor's GPU as the current one, so that the call and its stream belong to it."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError("a tensor of the call is not on a GPU")
+    return torch.cuda.device(t.device)
 
 
 def make_shape(T, H, E, k, I, I_shared=0, act="bf16", w_routed="bf16", w_shared="bf16", path="auto") -> MoeShape:
@@ -235,3 +263,87 @@ def moe_quantize_int8(x, codes, scales, stream=None):
     """x bf16 [rows, K] -> codes int8 [rows, K], scales float32 [rows]."""
     rows, K = (x.shape[0], x.shape[1]) if x is not None else (0, 8)
     _check(load().moe_quantize_int8(_p(x), rows, K, _p(codes), _p(scales), _stream(stream)))
+
+
+def moe_train_workspace_size(shape: MoeShape) -> int:
+    b = ctypes.c_size_t()
+    _check(load().moe_train_workspace_size(ctypes.byref(shape), ctypes.byref(b)))
+    return b.value
+
+
+def moe_gated_ffn(shape, x, expert_offsets, slot_token, weights_: dict, gate_pre, up_pre, y_perm, ws, stream=None):
+    """Weights row-major: gate, up [E, H, I], down [E, I, H]. gate_pre and up_pre may both be None."""
+    w = weights(weights_)
+    with _device_of(ws):
+        _check(load().moe_gated_ffn(ctypes.byref(shape), _p(x), _p(expert_offsets), _p(slot_token), ctypes.byref(w),
+                                    _p(gate_pre), _p(up_pre), _p(y_perm), _p(ws), ws.numel() * ws.element_size(),
+                                    _stream(stream)))
+
+
+def moe_gated_ffn_backward(shape, x, expert_offsets, slot_token, weights_: dict, gate_pre, up_pre, dy_perm, dx_perm,
+                           grads: dict | None, ws, stream=None):
+    """grads: gate, up and down tensors that receive the weights' gradients, or None; dx_perm may be None."""
+    w = weights(weights_)
+    g = None if grads is None else MoeWeightGrads(*[grads[n].data_ptr() for n in ("gate", "up", "down")])
+    with _device_of(ws):
+        _check(load().moe_gated_ffn_backward(ctypes.byref(shape), _p(x), _p(expert_offsets), _p(slot_token),
+                                             ctypes.byref(w), _p(gate_pre), _p(up_pre), _p(dy_perm), _p(dx_perm),
+                                             None if g is None else ctypes.byref(g), _p(ws),
+                                             ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def moe_combine_backward(shape, dy, y_perm, pair_slot, topk_w, dy_perm, dtopk_w, stream=None):
+    with _device_of(dtopk_w):
+        _check(load().moe_combine_backward(ctypes.byref(shape), _p(dy), _p(y_perm), _p(pair_slot), _p(topk_w),
+                                           _p(dy_perm), _p(dtopk_w), _stream(stream)))
+
+
+class AdamwTensors:
+    """The tensor table of moe_adamw, with references that keep its tensors alive."""
+
+    def __init__(self, array, keep, p_type: str, g_type: str, state: int):
+        self.array, self.keep, self.p_type, self.g_type, self.state = array, keep, p_type, g_type, state
+
+
+def adamw_tensors(p, g, m, v, master=None, m_scale=None, v_scale=None) -> AdamwTensors:
+    """Lists of tensors, one entry per parameter; m_scale and v_scale select the E4M3 state (m and v then
+    one byte an element). Made once and used for every step on the same tensors."""
+    import torch
+    lists = [p, g, m, v, m_scale, v_scale, master]
+    if (m_scale is None) != (v_scale is None):
+        raise ValueError("m_scale and v_scale go together")
+    if any(x is not None and len(x) != len(p) for x in lists):
+        raise ValueError("every list needs one tensor per parameter")
+    q8 = m_scale is not None
+    types = {torch.float32: "f32", torch.bfloat16: "bf16"}
+    device = p[0].device if len(p) else None
+    for i, t in enumerate(p):
+        n = t.numel()
+        if t.dtype not in types or g[i].dtype not in types or t.dtype != p[0].dtype or g[i].dtype != g[0].dtype:
+            raise ValueError("parameters and gradients are float32 or bfloat16, one type each")
+        if any(x[i].element_size() != 1 if q8 else x[i].dtype != torch.float32 for x in (m, v)):
+            raise ValueError("m and v are float32, or one byte an element with scales")
+        if any(x is not None and x[i].dtype != torch.float32 for x in (master, m_scale, v_scale)):
+            raise ValueError("master copies and scales are float32")
+        if any(x is not None and x[i].numel() != n for x in (g, m, v, master)):
+            raise ValueError("tensor %d: sizes differ" % i)
+        if q8 and any(x[i].numel() != (n + 255) // 256 for x in (m_scale, v_scale)):
+            raise ValueError("tensor %d: one scale per 256 elements" % i)
+        if any(x is not None and (not x[i].is_contiguous() or not x[i].is_cuda or x[i].device != device) for x in lists):
+            raise ValueError("tensor %d: contiguous tensors of one GPU are needed" % i)
+    array = (MoeAdamwTensor * len(p))(*[
+        MoeAdamwTensor(*[None if x is None else x[i].data_ptr() for x in lists], n=t.numel()) for i, t in enumerate(p)])
+    return AdamwTensors(array, [None if x is None else list(x) for x in lists], types[p[0].dtype] if len(p) else "f32",
+                        types[g[0].dtype] if len(p) else "f32", int(q8))
+
+
+def moe_adamw(tensors: AdamwTensors, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step=1, lr_dev=None,
+              step_dev=None, grad_scale=None, seed=0, stream=None):
+    """lr_dev, grad_scale (float32) and step_dev (int64): one-element device tensors read in place of lr, 1, step.
+    seed: of the E4M3 state's random rounding."""
+    c = MoeAdamwConfig(DTYPE[tensors.p_type], DTYPE[tensors.g_type], tensors.state, lr, beta1, beta2, eps, weight_decay,
+                       step, seed & 0xFFFFFFFF, _p(lr_dev), _p(step_dev), _p(grad_scale))
+    if not len(tensors.array):
+        return
+    with _device_of(tensors.keep[0][0]):
+        _check(load().moe_adamw(ctypes.byref(c), tensors.array, len(tensors.array), _stream(stream)))

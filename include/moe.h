@@ -13,8 +13,8 @@
  *   combine  y[t] = sum_j w[t][j] Y[pair_slot[t k + j]] + Y_shared[t]    [ch6 §6.2.6, §6.4.1]
  *
  * Conventions (all functions):
- *   - Every pointer argument is device memory owned by the caller, except the moe_shape /
- *     moe_weights structs, which are host memory read during the call only.
+ *   - Every pointer argument is device memory owned by the caller, except the structs (moe_shape,
+ *     moe_weights and the training ones), which are host memory read during the call only.
  *   - Functions validate their arguments on the host, then only enqueue kernels on `stream`
  *     and return. MOE_OK means "enqueued"; results are valid in stream order (the same
  *     contract the chapter describes for collective calls, [ch6 §6.4.3]). No function
@@ -376,6 +376,128 @@ moe_status moe_quantize_mxfp8(const void* x, int32_t rows, int32_t K, uint8_t* c
  */
 moe_status moe_quantize_int8(const void* x, int32_t rows, int32_t K, int8_t* codes, float* scales,
                              moe_stream_t stream);
+
+/*
+ * Training the layer's experts. Weights and their gradients are row-major, as [ch6 §6.2.2] writes
+ * them and as moe_layer_forward_logical takes them: gate, up [E][H][I], down [E][I][H], in the
+ * activations' type (shape->w_routed == shape->act, MOE_F32 or MOE_BF16), 16-byte aligned;
+ * moe_weights' scales are not read. shape->I_shared is 0: a shared expert, or a dense block, is a
+ * call of its own with E = k = 1. shape->path is not used. Rows are moe_permute's: expert e owns
+ * rows [expert_offsets[e], expert_offsets[e+1]) of the T*k; offsets are read as clamped to
+ * [0, T*k]. Sums and activations are fp32; each tensor below is rounded once, when it is written.
+ *   expert_offsets int32[E+1]; NULL with E = 1: one group of all T rows
+ *   slot_token     int32[T*k]: row r reads x[slot_token[r]], zeros for a token outside [0, T);
+ *                  NULL: x is [T*k][H] and row r reads x[r]
+ *   ws             moe_train_workspace_size(shape) bytes, 256-byte aligned; one call's scratch: calls
+ *                  that may run at the same time (other streams, graphs replayed side by side) need
+ *                  one each, and nothing is kept in it between calls
+ */
+moe_status moe_train_workspace_size(const moe_shape* shape, size_t* bytes);
+
+/*
+ * moe_gated_ffn — the gated block of every expert on its rows, keeping what the gradient reads:
+ *   g = x Wg, u = x Wu, h = SiLU(g) (.) u, y = h Wd
+ *   gate_pre, up_pre [T*k][I] act out: g and u (both, or both NULL: not kept)
+ *   y_perm           [T*k][H] act out
+ * h is formed from the unrounded g and u and kept in `ws` in the act type. Rows from
+ * expert_offsets[E] on are not written. T == 0 enqueues nothing.
+ */
+moe_status moe_gated_ffn(const moe_shape* shape, const void* x, const int32_t* expert_offsets,
+                         const int32_t* slot_token, const moe_weights* weights, void* gate_pre,
+                         void* up_pre, void* y_perm, void* ws, size_t ws_bytes,
+                         moe_stream_t stream);
+
+/* Weight gradients, each of its weight's layout and type. */
+typedef struct {
+  void* gate;
+  void* up;
+  void* down;
+} moe_weight_grads;
+
+/*
+ * moe_gated_ffn_backward — the block's gradient at the saved g, u, for s = 1 / (1 + e^-g):
+ *   dh = dy Wd^T, du = dh g s, dg = dh u s (1 + g (1 - s))
+ *   dx_perm = dg Wg^T + du Wu^T, dWg = x^T dg, dWu = x^T du, dWd = (g s u)^T dy
+ *   gate_pre, up_pre [T*k][I] act: as moe_gated_ffn wrote them
+ *   dy_perm  [T*k][H] act; rows from expert_offsets[E] on are not read
+ *   dx_perm  [T*k][H] act out, or NULL: not computed. Rows from expert_offsets[E] on are not
+ *            written. moe_combine with weights 1 sums the rows of each token.
+ *   grads    out, or NULL: not computed. Every element is written; an expert without rows has
+ *            gradient 0 (with T == 0 all have).
+ * h, dg and du are kept in `ws` in the act type. Outputs must not overlap inputs. The same bits on
+ * every run: no atomics.
+ */
+moe_status moe_gated_ffn_backward(const moe_shape* shape, const void* x,
+                                  const int32_t* expert_offsets, const int32_t* slot_token,
+                                  const moe_weights* weights, const void* gate_pre,
+                                  const void* up_pre, const void* dy_perm, void* dx_perm,
+                                  const moe_weight_grads* grads, void* ws, size_t ws_bytes,
+                                  moe_stream_t stream);
+
+/*
+ * moe_combine_backward — the gradient of moe_combine by its rows and weights:
+ *   dy_perm[pair_slot[t*k+j]] = topk_w[t][j] * dy[t], dtopk_w[t][j] = dy[t] . y_perm[pair_slot[t*k+j]]
+ *   dy       [T][H] act (also the gradient of y_shared)
+ *   y_perm, pair_slot, topk_w   moe_combine's inputs; the slots of different pairs differ
+ *   dy_perm  [T*k][H] act out; rows that no pair names are not written. Not the memory of dy or y_perm.
+ *   dtopk_w  float[T][k] out, summed in fp32; 0 for a pair whose pair_slot is outside [0, T*k)
+ */
+moe_status moe_combine_backward(const moe_shape* shape, const void* dy, const void* y_perm,
+                                const int32_t* pair_slot, const float* topk_w, void* dy_perm,
+                                float* dtopk_w, moe_stream_t stream);
+
+/*
+ * moe_adamw — one AdamW step of `count` tensors, at most 40 a launch, in place:
+ *   g' = grad_scale g, m = beta1 m + (1 - beta1) g', v = beta2 v + (1 - beta2) g'^2
+ *   p = p - lr weight_decay p - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in fp32. State formats:
+ *   MOE_ADAM_F32   m, v float[n]
+ *   MOE_ADAM_E4M3  m, v uint8[n]: E4M3FN codes of m and of sqrt(v), value = code * scale, with
+ *                  m_scale, v_scale float[ceil(n / 256)], one per 256 consecutive elements: the
+ *                  largest magnitude in them (at least 2^-100) / 448. All-zero codes start the state.
+ *                  A value between two codes goes to the upper one when its place between them
+ *                  (0..1) plus b / 2^20 reaches 1, b from a 32-bit word x of element i: its upper 20
+ *                  bits for m, its lower 20 for sqrt(v), so slow changes are kept on average. With
+ *                  32-bit wrapping and f(z, s, t) = (z ^ (z >> s)) * 0x85EBCA77 =: w, w ^ (w >> t):
+ *                  x = f(i * 0x9E3779B1 + f(seed + step * 0x9E3779B9, 16, 13), 15, 13).
+ *                  p moves by the new m and v before they are rounded.
+ * moe_adamw_tensor: device pointers of one tensor of n >= 0 consecutive elements; p, g, m, v and
+ * master 16-byte, scales 4-byte aligned. master float[n]: the fp32 copy that is updated, p then its
+ * rounding to bf16 (p_type MOE_BF16; every tensor has one or none has). No two tensors may
+ * share memory. g is only read.
+ * moe_adamw_config: lr_dev, step_dev and grad_scale (device, each may be NULL) are read by the kernel
+ * in place of lr, step and 1, so that a captured call follows them; step_dev below 1 counts as 1.
+ * lr, eps, weight_decay >= 0; beta1, beta2 in [0, 1); step >= 1. Non-finite gradients reach p, m
+ * and v as the formulas say. count == 0 enqueues nothing; both structs are host memory read during
+ * the call.
+ */
+typedef enum { MOE_ADAM_F32 = 0, MOE_ADAM_E4M3 = 1 } moe_adam_state;
+
+typedef struct {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale; /* MOE_ADAM_E4M3 */
+  float* v_scale;
+  float* master;  /* or NULL */
+  int64_t n;
+} moe_adamw_tensor;
+
+typedef struct {
+  moe_dtype p_type; /* MOE_F32 or MOE_BF16 */
+  moe_dtype g_type; /* MOE_F32 or MOE_BF16 */
+  moe_adam_state state;
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;     /* 1 for the first */
+  uint32_t seed;    /* MOE_ADAM_E4M3: of the random rounding */
+  const float* lr_dev;
+  const int64_t* step_dev;
+  const float* grad_scale;
+} moe_adamw_config;
+
+moe_status moe_adamw(const moe_adamw_config* config, const moe_adamw_tensor* tensors,
+                     int32_t count, moe_stream_t stream);
 
 #ifdef __cplusplus
 }
