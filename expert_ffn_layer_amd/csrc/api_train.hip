@@ -27,14 +27,15 @@ moe_status check_train_shape(const moe_shape* s) {
 }
 
 struct TrainWs {
-  size_t h, dgu, total;
+  size_t h, dgu, xg, total;
 };
 TrainWs train_ws(const moe_shape& s) {
   const size_t P = (size_t)s.T * s.k, b = s.act == MOE_F32 ? 4 : 2;
   TrainWs w;
   w.h = 0;
   w.dgu = up(P * s.I * b);
-  w.total = w.dgu + up(P * s.I * 2 * b) + WS_ALIGN;
+  w.xg = w.dgu + up(P * s.I * 2 * b);
+  w.total = w.xg + (s.act == MOE_BF16 ? up(P * s.H * b) : 0) + WS_ALIGN;
   return w;
 }
 
@@ -69,11 +70,12 @@ moe_status train_args(const moe_shape* s, const void* x, const int32_t* off, con
   a->down = w->down;
   a->h = (char*)ws + l.h;
   a->dgu = (char*)ws + l.dgu;
+  a->xg = (char*)ws + l.xg;
   return MOE_OK;
 }
 
 hipError_t product(TrainForm form, int act, const TrainArgs& a, hipStream_t st) {
-  return launch_train_f32(form, act, a, st);
+  return act == MOE_F32 ? launch_train_f32(form, a, st) : launch_train_bf16(form, a, st);
 }
 
 // Two of the updated tensors share memory: both workgroups would read and write it.

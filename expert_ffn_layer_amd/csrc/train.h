@@ -24,7 +24,7 @@ struct TrainArgs {
   void *g, *u, *y;            // TF_GATE_UP / TF_DOWN outputs; g, u inputs of TF_DH
   const void* dy;
   void *dx, *dgate, *dup, *ddown;
-  void *h, *dgu;              // workspace: [P][I] and [P][2 I]
+  void *h, *dgu, *xg;         // workspace: [P][I], [P][2 I] and, for bf16, [P][H]
 };
 
 // Largest number of row tiles of bm rows that E groups of P rows in all can take.
@@ -32,7 +32,8 @@ inline long long max_row_tiles(int P, int E, int bm) {
   return E == 1 ? ((long long)P + bm - 1) / bm : P / bm + (long long)(E < P ? E : P);
 }
 
-hipError_t launch_train_f32(TrainForm form, int act, const TrainArgs& a, hipStream_t st);
+hipError_t launch_train_f32(TrainForm form, const TrainArgs& a, hipStream_t st);
+hipError_t launch_train_bf16(TrainForm form, const TrainArgs& a, hipStream_t st);
 
 hipError_t launch_combine_backward(int act, const void* dy, const void* y_perm, const int32_t* pair_slot, const float* w,
                                    void* dy_perm, float* dw, int T, int H, int k, hipStream_t st);

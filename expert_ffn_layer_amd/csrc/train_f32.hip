@@ -251,8 +251,6 @@ hipError_t launch(TrainForm form, const TrainArgs& a, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_train_f32(TrainForm form, int act, const TrainArgs& a, hipStream_t st) {
-  return act == MOE_F32 ? launch<float>(form, a, st) : launch<uint16_t>(form, a, st);
-}
+hipError_t launch_train_f32(TrainForm form, const TrainArgs& a, hipStream_t st) { return launch<float>(form, a, st); }
 
 }  // namespace moe
