@@ -8,7 +8,7 @@ namespace moe {
 
 namespace {
 
-constexpr int BK = 32;     // reduction elements per step
+constexpr int BK = 64;     // reduction elements per step: 128 bytes of a row, a whole cache line
 constexpr int THR = 256;   // 4 waves
 constexpr int NXCD = 8;
 
@@ -24,36 +24,37 @@ typedef __attribute__((ext_vector_type(16))) float f32x16;
 
 __device__ const uint4 zero_chunk = {0u, 0u, 0u, 0u};
 
-// One operand's tile in LDS: L indices x 32 reduction elements per stage, as L / 16 units of 1 KiB,
-// each moved by one wave-wide 16-byte load straight to LDS. A fragment is 32 indices x 16 reduction
-// elements (half h of the step): lane l holds index l % 32, elements 16 h + 8 (l / 32) .. + 8.
-//   KC (reduction index contiguous in memory): unit u holds indices 16 u .. + 16, 64 bytes each, whose
-//     16-byte chunks are permuted by the row, so that 8 lanes' 16-byte reads cover all banks.
+// One operand's tile in LDS: L indices x 64 reduction elements per slot, as L / 8 units of 1 KiB, each
+// moved by one wave-wide 16-byte load straight to LDS. A fragment is 32 indices x 16 reduction elements
+// (quarter h of the step): lane l holds index l % 32, elements 16 h + 8 (l / 32) .. + 8.
+//   KC (reduction index contiguous in memory): unit u holds indices 8 u .. + 8, 128 bytes each; 16-byte
+//     chunk c of row r sits at c ^ ((r >> 1) & 7), so that 16 lanes' reads cover all 64 banks.
 //   MC (own index contiguous): a row of L indices per reduction element, read 4 x 16 at a time by the
 //     transposing read; 32-byte chunk c of row r sits at c ^ swz(r), so that its 4 rows differ in bank.
 template <int L, bool KC>
 struct Tile {
-  static constexpr int UNITS = L / 16;
+  static constexpr int UNITS = L / 8;
   static constexpr int BYTES = L * BK * 2;
   static constexpr int LPR = L / 8;  // MC: lanes per row
   __device__ static constexpr int swz(int r) { return L >= 128 ? ((r & 3) << 1) : (r & 2); }
+  // unit that wave w of 4 moves as its q-th: MC: the first half of them makes the slot's first 32 rows
+  static constexpr int U = UNITS / 4;
+  __device__ static int unit(int q, int w) { return KC ? w * U + q : (q / (U / 2)) * (UNITS / 2) + w * (U / 2) + q % (U / 2); }
   // index (KC) or reduction element (MC) that lane l of unit u moves
-  __device__ static int row(int u, int l) { return KC ? u * 16 + (l >> 2) : u * (64 / LPR) + l / LPR; }
+  __device__ static int row(int u, int l) { return KC ? u * 8 + (l >> 3) : (u * 64 + l) / LPR; }
   // first of the 8 elements it moves: reduction elements (KC) or indices (MC)
   __device__ static int elem(int u, int l) {
-    if (KC) return ((l & 3) ^ ((l >> 3) & 3)) * 8;
+    if (KC) return ((l & 7) ^ ((row(u, l) >> 1) & 7)) * 8;
     const int p = l % LPR;
     return ((p >> 1) ^ swz(row(u, l))) * 16 + (p & 1) * 8;
   }
-  // byte of lane l's part of the fragment of 32 indices from 32 t, half h, is at(t, l) + half(h, l):
-  // KC: at(0, l) + 2048 t, and half(h, l) = half(0, l) ^ 32 h; MC: at(t, l) = at(0, l) ^ 64 t, half = row offset
-  __device__ static int at(int t, int l) {
-    const int i = l & 31;
-    if (KC) return t * 2048 + i * 64;
+  // Lane l's byte of the fragment of indices 32 t.. + 32, quarter h: a register for each h (KC) or t (MC)
+  // and a constant for the other
+  __device__ static int kc_at(int t0, int h, int l) { return (t0 * 32 + (l & 31)) * 128 + (((2 * h + (l >> 5)) ^ ((l >> 1) & 7)) << 4); }
+  __device__ static int mc_at(int t, int l) {
     const int r = 8 * (l >> 5) + ((l & 15) >> 2);
     return r * (L * 2) + (((2 * t + ((l >> 4) & 1)) ^ swz(r)) << 5) + (l & 3) * 8;
   }
-  __device__ static int chunk(int h, int l) { return (((2 * h + (l >> 5)) ^ ((l >> 1) & 3)) & 3) * 16; }
 };
 
 template <int L, bool KC>
@@ -68,20 +69,41 @@ __device__ __forceinline__ bf16x8 read_frag(const lds_byte* at) {
   }
 }
 
-template <int FORM, int WR, int WC, int MT, int NT, int D>
+// Which loads go behind which phase (quarter) of a step. Quarter h + 1 is read in phase h, so the first
+// half of a slot is free after phase 0 and all of it after phase 2.
+//   MC operand: phases 1, 2 of step s bring the first half of stage s + 2, phases 3 of s and 0 of s + 1 its
+//     second half.
+//   KC operand: phases 3 of step s and 0, 1 of s + 1 bring stage s + 2.
+// U loads each per wave and stage, spread evenly: bursts lengthen the wait for all of them.
+template <bool KC, int U>
+struct Share {
+  // cumulative loads before the k-th of the phases in their order: 3 0 1 2 (KC), 1 2 3 0 (MC)
+  static constexpr int cum(int k) { return KC ? (k >= 3 ? U : (U * 3 * k + 7) / 8) : U * k / 4; }
+  static constexpr int from(int ph, int past = 0) { return cum((KC ? (ph + 1) % 4 : (ph + 3) % 4) + past); }
+  static constexpr int count(int ph) { return from(ph, 1) - from(ph); }
+};
+
+template <int FORM, int WR, int WC, int MT, int NT>
 __global__ void __launch_bounds__(THR, 1) train_bf16_kernel(const TrainArgs a) {
   constexpr bool P_KC = FORM != TF_DW, Q_KC = FORM == TF_DH || FORM == TF_DX;
   constexpr int BM = WR * MT * 32, BN = WC * NT * 32;
   using TP = Tile<BM, P_KC>;
   using TQ = Tile<BN, Q_KC>;
-  constexpr int UP = TP::UNITS / 4, UQ = TQ::UNITS / 4, L = UP + UQ;  // loads per wave and stage
-  static_assert(WR * WC == 4 && TP::UNITS % 4 == 0 && TQ::UNITS % 4 == 0, "four waves share the units");
+  constexpr int UP = TP::U, UQ = TQ::U, L = UP + UQ;  // loads per wave and stage
+  static_assert(WR * WC == 4, "four waves share the units");
+  using SP = Share<P_KC, UP>;
+  using SQ = Share<Q_KC, UQ>;
+  constexpr bool KCKC = P_KC && Q_KC;
   constexpr int OUTN = FORM == TF_GATE_UP ? BN / 2 : BN;  // columns of the output (per matrix)
-  // one array per slot and operand: the compiler then sees which loads to LDS a read has to wait for
-  __shared__ __align__(1024) uint8_t lp0[TP::BYTES], lp1[TP::BYTES], lp2[D > 2 ? TP::BYTES : 16], lp3[D > 2 ? TP::BYTES : 16];
-  __shared__ __align__(1024) uint8_t lq0[TQ::BYTES], lq1[TQ::BYTES], lq2[D > 2 ? TQ::BYTES : 16], lq3[D > 2 ? TQ::BYTES : 16];
-#define P_SLOT(S) ((lds_byte*)((S) == 0 ? lp0 : (S) == 1 ? lp1 : (S) == 2 ? lp2 : lp3))
-#define Q_SLOT(S) ((lds_byte*)((S) == 0 ? lq0 : (S) == 1 ? lq1 : (S) == 2 ? lq2 : lq3))
+  // Two slots for each operand; those of a KC operand are freed and filled whole (a cache line of every
+  // row), those of a MC one by halves of 32 rows. One array for each such part: the compiler then sees which
+  // loads to LDS a read has to wait for.
+  constexpr int PK = P_KC ? TP::BYTES : 16, QK = Q_KC ? TQ::BYTES : 16;
+  constexpr int PH = P_KC ? 16 : TP::BYTES / 2, QH = Q_KC ? 16 : TQ::BYTES / 2;
+  __shared__ __align__(1024) uint8_t pk0[PK], pk1[PK], qk0[QK], qk1[QK];
+  __shared__ __align__(1024) uint8_t p0a[PH], p0b[PH], p1a[PH], p1b[PH], q0a[QH], q0b[QH], q1a[QH], q1b[QH];
+#define P_PART(SLOT, B) ((lds_byte*)(P_KC ? ((SLOT) ? pk1 : pk0) : (SLOT) == 0 ? ((B) ? p0b : p0a) : ((B) ? p1b : p1a)))
+#define Q_PART(SLOT, B) ((lds_byte*)(Q_KC ? ((SLOT) ? qk1 : qk0) : (SLOT) == 0 ? ((B) ? q0b : q0a) : ((B) ? q1b : q1a)))
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / WC, wc = wave % WC;
   const size_t H = a.H, I = a.I, HI = H * I;
@@ -134,7 +156,7 @@ __global__ void __launch_bounds__(THR, 1) train_bf16_kernel(const TrainArgs a) {
   size_t qjump = 0;                           // TF_DX: from the end of Wg's row to the start of Wu's
 #pragma unroll
   for (int u = 0; u < UP; ++u) {
-    const int un = wave * UP + u, r = TP::row(un, lane), c = TP::elem(un, lane);
+    const int un = TP::unit(u, wave), r = TP::row(un, lane), c = TP::elem(un, lane);
     if constexpr (P_KC) {
       // rows past the group's end repeat its last one: their results are not stored
       const int row = m0 + r < mend ? m0 + r : mend - 1;
@@ -159,7 +181,7 @@ __global__ void __launch_bounds__(THR, 1) train_bf16_kernel(const TrainArgs a) {
   }
 #pragma unroll
   for (int u = 0; u < UQ; ++u) {
-    const int un = wave * UQ + u, r = TQ::row(un, lane), c = TQ::elem(un, lane);
+    const int un = TQ::unit(u, wave), r = TQ::row(un, lane), c = TQ::elem(un, lane);
     if constexpr (FORM == TF_GATE_UP) {
       // 32-column chunks in the order of the waves' fragments: NT / 2 of gate, the same columns of up
       const int ch = c >> 5, t = ch % NT;
@@ -189,10 +211,10 @@ __global__ void __launch_bounds__(THR, 1) train_bf16_kernel(const TrainArgs a) {
       }
     }
   }
-  // Stage `step` (loads q of the wave) into a slot; the source moves on by one step, and stays on the last
-  // one, whose repeats nothing reads. TF_DW: rows past the group's end read zeros.
+  // One load of stage `step` to LDS; the source moves on by one step, and stays on the last one, whose
+  // repeats nothing reads. TF_DW: rows past the group's end read zeros.
   const int half_steps = (int)I / BK;
-  auto load = [&](const uint8_t*& src, lds_byte* dst, int row, size_t adv, int step) __attribute__((always_inline)) {
+  auto load_one = [&](const uint8_t*& src, lds_byte* dst, int row, size_t adv, int step) __attribute__((always_inline)) {
     const uint8_t* from = src;
     if constexpr (FORM == TF_DW) from = row < K - step * BK ? from : (const uint8_t*)&zero_chunk;
     __builtin_amdgcn_global_load_lds((const void*)from, (lds_void*)dst, 16, 0, 0);
@@ -201,12 +223,16 @@ __global__ void __launch_bounds__(THR, 1) train_bf16_kernel(const TrainArgs a) {
   };
   auto load_p = [&](int q, int step, auto slot) __attribute__((always_inline)) {
     const size_t adv = FORM == TF_DW || step + 1 < nsteps ? pstride : 0;
-    load(psrc[q], P_SLOT(decltype(slot)::value) + (wave * UP + q) * 1024, TP::row(wave * UP + q, lane), adv, step);
+    const int un = TP::unit(q, wave);
+    lds_byte* const part = P_PART(decltype(slot)::value, q >= UP / 2);
+    load_one(psrc[q], part + (P_KC ? un : un % (TP::UNITS / 2)) * 1024, TP::row(un, lane), adv, step);
   };
   auto load_q = [&](int q, int step, auto slot) __attribute__((always_inline)) {
     size_t adv = FORM == TF_DW || step + 1 < nsteps ? qstride : 0;
     if constexpr (FORM == TF_DX) adv += step + 1 == half_steps ? qjump : 0;
-    load(qsrc[q], Q_SLOT(decltype(slot)::value) + (wave * UQ + q) * 1024, TQ::row(wave * UQ + q, lane), adv, step);
+    const int un = TQ::unit(q, wave);
+    lds_byte* const part = Q_PART(decltype(slot)::value, q >= UQ / 2);
+    load_one(qsrc[q], part + (Q_KC ? un : un % (TQ::UNITS / 2)) * 1024, TQ::row(un, lane), adv, step);
   };
 
   f32x16 acc[NT][MT];
@@ -218,88 +244,111 @@ __global__ void __launch_bounds__(THR, 1) train_bf16_kernel(const TrainArgs a) {
       for (int j = 0; j < 16; ++j) acc[t][i][j] = 0.f;
 
   if (nsteps > 0) {
-    auto fill = [&](auto slot) __attribute__((always_inline)) {
-      constexpr int S = decltype(slot)::value;
-#pragma unroll
-      for (int q = 0; q < UP; ++q) load_p(q, S, slot);
-#pragma unroll
-      for (int q = 0; q < UQ; ++q) load_q(q, S, slot);
-    };
-    fill(std::integral_constant<int, 0>{});
-    fill(std::integral_constant<int, 1>{});
-    fill(std::integral_constant<int, 2>{});
-    fill(std::integral_constant<int, 3>{});
-    // LDS bytes of this wave's fragments within a slot: a register per half for a KC operand, one per
+    // LDS bytes of this wave's fragments within a slot: a register per quarter for a KC operand, one per
     // fragment for an MC one
-    int pb[P_KC ? 2 : MT], qb[Q_KC ? 2 : NT];
+    int pb[P_KC ? 4 : MT], qb[Q_KC ? 4 : NT];
 #pragma unroll
-    for (int i = 0; i < (P_KC ? 2 : MT); ++i)
-      pb[i] = P_KC ? TP::at(wr * MT, lane) + TP::chunk(i, lane) : TP::at(wr * MT + i, lane);
+    for (int i = 0; i < (P_KC ? 4 : MT); ++i) pb[i] = P_KC ? TP::kc_at(wr * MT, i, lane) : TP::mc_at(wr * MT + i, lane);
 #pragma unroll
-    for (int t = 0; t < (Q_KC ? 2 : NT); ++t)
-      qb[t] = Q_KC ? TQ::at(wc * NT, lane) + TQ::chunk(t, lane) : TQ::at(wc * NT + t, lane);
-    bf16x8 pf[2][MT], qf[2][NT];  // by half
-    auto read_p = [&](int i, auto half, auto slot) __attribute__((always_inline)) {
-      constexpr int h = decltype(half)::value;
-      pf[h][i] = read_frag<BM, P_KC>(P_SLOT(decltype(slot)::value) + (P_KC ? pb[h] + i * 2048 : pb[i] + h * 16 * (BM * 2)));
+    for (int t = 0; t < (Q_KC ? 4 : NT); ++t) qb[t] = Q_KC ? TQ::kc_at(wc * NT, t, lane) : TQ::mc_at(wc * NT + t, lane);
+    bf16x8 pf[2][MT], qf[2][NT];  // two quarters: the one multiplied and the one read
+    auto read_p = [&](int i, auto quarter, auto slot) __attribute__((always_inline)) {
+      constexpr int h = decltype(quarter)::value;
+      lds_byte* const part = P_PART(decltype(slot)::value, h >= 2);
+      pf[h & 1][i] = read_frag<BM, P_KC>(part + (P_KC ? pb[h] + i * 4096 : pb[i] + (h & 1) * 16 * (BM * 2)));
     };
-    auto read_q = [&](int t, auto half, auto slot) __attribute__((always_inline)) {
-      constexpr int h = decltype(half)::value;
-      qf[h][t] = read_frag<BN, Q_KC>(Q_SLOT(decltype(slot)::value) + (Q_KC ? qb[h] + t * 2048 : qb[t] + h * 16 * (BN * 2)));
+    auto read_q = [&](int t, auto quarter, auto slot) __attribute__((always_inline)) {
+      constexpr int h = decltype(quarter)::value;
+      lds_byte* const part = Q_PART(decltype(slot)::value, h >= 2);
+      qf[h & 1][t] = read_frag<BN, Q_KC>(part + (Q_KC ? qb[h] + t * 4096 : qb[t] + (h & 1) * 16 * (BN * 2)));
     };
-    // products of half h, with the reads of the other half and, for LOADS, stage `step` loaded into SL
-    auto phase = [&](auto half, auto rd_slot, auto slot, auto loads, int step) __attribute__((always_inline)) {
-      constexpr int h = decltype(half)::value;
-      constexpr std::integral_constant<int, h ^ 1> other{};
-      constexpr int N_MFMA = MT * NT, READS = MT + NT, LD = decltype(loads)::value ? L : 0;
+    constexpr std::integral_constant<int, 0> C0{};
+    constexpr std::integral_constant<int, 1> C1{};
+    constexpr std::integral_constant<int, 2> C2{};
+    constexpr std::integral_constant<int, 3> C3{};
+    // the n-th load of phase ph of step s, KC operands' first; slot: that of step s
+    auto load_nth = [&](auto ph_c, int n, int s, auto slot) __attribute__((always_inline)) {
+      constexpr int ph = decltype(ph_c)::value, np = SP::count(ph), nq = SQ::count(ph);
+      constexpr std::integral_constant<int, decltype(slot)::value ^ 1> other{};
+      const bool p = P_KC ? n < np : n >= nq;
+      const int at = p ? SP::from(ph) + (P_KC ? n : n - nq) : SQ::from(ph) + (P_KC ? n - np : n);
+      // phase 0, and phase 1 of a KC operand, still bring stage s + 1, into the slot that is not step s's
+      if (p) {
+        if constexpr (ph == 0 || (P_KC && ph == 1)) load_p(at, s + 1, other);
+        else load_p(at, s + 2, slot);
+      } else {
+        if constexpr (ph == 0 || (Q_KC && ph == 1)) load_q(at, s + 1, other);
+        else load_q(at, s + 2, slot);
+      }
+    };
+    // Products of quarter h, with the reads of the next quarter early behind them and the phase's loads spread
+    // over all of them.
+    auto phase = [&](auto quarter, auto rd_slot, int s, auto slot) __attribute__((always_inline)) {
+      constexpr int h = decltype(quarter)::value, LOADS = SP::count(h) + SQ::count(h);
+      constexpr std::integral_constant<int, (h + 1) % 4> next{};
+      constexpr int PRODUCTS = MT * NT, READS = MT + NT, SPAN = PRODUCTS > 4 ? PRODUCTS * 3 / 4 : PRODUCTS;
 #pragma unroll
-      for (int n = 0; n < N_MFMA; ++n) {
+      for (int n = 0; n < PRODUCTS; ++n) {
         const int t = n % NT, i = n / NT;
-        acc[t][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf[h][t], pf[h][i], acc[t][i], 0, 0, 0);
-        // reads in the order in which the next phase needs them: q, p0, then the other rows
+        acc[t][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf[h & 1][t], pf[h & 1][i], acc[t][i], 0, 0, 0);
 #pragma unroll
-        for (int r = n * READS / N_MFMA; r < (n + 1) * READS / N_MFMA; ++r) {
-          if (r < NT) read_q(r, other, rd_slot);
-          else read_p(r - NT, other, rd_slot);
+        for (int r = n * READS / SPAN; r < (n + 1) * READS / SPAN && r < READS; ++r) {
+          if (r < NT) read_q(r, next, rd_slot);
+          else read_p(r - NT, next, rd_slot);
         }
 #pragma unroll
-        for (int q = n * LD / N_MFMA; q < (n + 1) * LD / N_MFMA; ++q) {
-          if (q < UP) load_p(q, step, slot);
-          else load_q(q - UP, step, slot);
-        }
+        for (int q = n * LOADS / PRODUCTS; q < (n + 1) * LOADS / PRODUCTS; ++q) load_nth(quarter, q, s, slot);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
-    constexpr std::integral_constant<int, 0> H0{};
-    constexpr std::integral_constant<int, 1> H1{};
-    // step s in slot SL: its second half is read during the first one's products; then every wave is done
-    // with the slot, stage s + 1 is there, and stage s + D goes into the slot
+    // Loads that may still be in flight: where a MC operand's second half is wanted (after phase 0), those of
+    // one step; where the next stage is wanted (after phase 2), those since the last one of a KC operand, or
+    // of one step where there is none.
+    constexpr int FLY0 = L;
+    constexpr int FLY2 = KCKC ? 0 : !P_KC && !Q_KC ? L : (P_KC ? SQ::count(1) + SQ::count(2) : SP::count(1) + SP::count(2));
     auto body = [&](int s, auto slot) __attribute__((always_inline)) {
-      constexpr std::integral_constant<int, (decltype(slot)::value + 1) % D> next{};
+      constexpr std::integral_constant<int, decltype(slot)::value ^ 1> other{};
       // opaque in every step, so that the slot stays a constant and does not become a register per slot and
       // fragment
 #pragma unroll
       for (int i = 0; i < MT && !P_KC; ++i) asm volatile("" : "+v"(pb[i]));
 #pragma unroll
       for (int t = 0; t < NT && !Q_KC; ++t) asm volatile("" : "+v"(qb[t]));
-      phase(H0, slot, slot, std::false_type{}, 0);
+      phase(C0, slot, s, slot);
+      if constexpr (!KCKC) {
+        MOE_WAIT_LGKM0();
+        MOE_WAIT_VMCNT(FLY0);
+        __builtin_amdgcn_s_barrier();
+      }
+      phase(C1, slot, s, slot);
+      phase(C2, slot, s, slot);
       MOE_WAIT_LGKM0();
-      MOE_WAIT_VMCNT((D - 2) * L);
+      MOE_WAIT_VMCNT(FLY2);
       __builtin_amdgcn_s_barrier();
-      phase(H1, next, slot, std::true_type{}, s + D);
+      phase(C3, other, s, slot);
     };
-    MOE_WAIT_VMCNT((D - 1) * L);
+    // what the steps before the first would have loaded, stage 0 first
+#pragma unroll
+    for (int q = 0; q < UQ; ++q) load_q(q, 0, C0);
+#pragma unroll
+    for (int q = 0; q < UP; ++q) load_p(q, 0, C0);
+    constexpr int Q1 = Q_KC ? 0 : UQ / 2, P1 = P_KC ? 0 : UP / 2;  // of stage 1, before phase 3 of step -1
+#pragma unroll
+    for (int q = 0; q < Q1; ++q) load_q(q, 1, C1);
+#pragma unroll
+    for (int q = 0; q < P1; ++q) load_p(q, 1, C1);
+#pragma unroll
+    for (int n = 0; n < SP::count(3) + SQ::count(3); ++n) load_nth(C3, n, -1, C1);
+    MOE_WAIT_VMCNT(Q1 + P1 + SP::count(3) + SQ::count(3));
     __builtin_amdgcn_s_barrier();
 #pragma unroll
-    for (int t = 0; t < NT; ++t) read_q(t, H0, H0);
+    for (int t = 0; t < NT; ++t) read_q(t, C0, C0);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) read_p(i, H0, H0);
-    // whole rounds of the ring: H and I are multiples of 128, the rows of TF_DW end in zeros
-    for (int s = 0; s < nsteps; s += D) {
-      body(s, H0);
-      body(s + 1, H1);
-      body(s + 2, std::integral_constant<int, 2>{});
-      body(s + 3, std::integral_constant<int, 3>{});
+    for (int i = 0; i < MT; ++i) read_p(i, C0, C0);
+    // pairs of steps: H and I are multiples of 128, the rows of TF_DW end in zeros
+    for (int s = 0; s < nsteps; s += 2) {
+      body(s, C0);
+      body(s + 1, C1);
     }
     MOE_WAIT_VMCNT(0);  // loads in flight land before the workgroup's LDS is released
   }
@@ -398,7 +447,7 @@ hipError_t launch(const TrainArgs& a, hipStream_t st) {
   }
   if (sbs == 0) return hipSuccess;
   const unsigned grid = (unsigned)((sbs + NXCD - 1) / NXCD * NXCD * 32);
-  train_bf16_kernel<FORM, 2, 2, 4, 4, 4><<<grid, THR, 0, st>>>(a);
+  train_bf16_kernel<FORM, 2, 2, 4, 4><<<grid, THR, 0, st>>>(a);
   return hipGetLastError();
 }
 
