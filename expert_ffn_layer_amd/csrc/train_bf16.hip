@@ -57,6 +57,10 @@ struct Tile {
   }
 };
 
+__device__ __forceinline__ u32x4 pack8(const f32x4& a, const f32x4& b) {
+  return u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])};
+}
+
 template <int L, bool KC>
 __device__ __forceinline__ bf16x8 read_frag(const lds_byte* at) {
   if constexpr (KC) {
@@ -102,6 +106,7 @@ __global__ void __launch_bounds__(THR, 1) train_bf16_kernel(const TrainArgs a) {
   constexpr int PH = P_KC ? 16 : TP::BYTES / 2, QH = Q_KC ? 16 : TQ::BYTES / 2;
   __shared__ __align__(1024) uint8_t pk0[PK], pk1[PK], qk0[QK], qk1[QK];
   __shared__ __align__(1024) uint8_t p0a[PH], p0b[PH], p1a[PH], p1b[PH], q0a[QH], q0b[QH], q1a[QH], q1b[QH];
+  __shared__ __align__(1024) uint8_t out_lds[4 * 8192];
 #define P_PART(SLOT, B) ((lds_byte*)(P_KC ? ((SLOT) ? pk1 : pk0) : (SLOT) == 0 ? ((B) ? p0b : p0a) : ((B) ? p1b : p1a)))
 #define Q_PART(SLOT, B) ((lds_byte*)(Q_KC ? ((SLOT) ? qk1 : qk0) : (SLOT) == 0 ? ((B) ? q0b : q0a) : ((B) ? q1b : q1a)))
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -353,72 +358,130 @@ __global__ void __launch_bounds__(THR, 1) train_bf16_kernel(const TrainArgs a) {
     MOE_WAIT_VMCNT(0);  // loads in flight land before the workgroup's LDS is released
   }
 
-  // --- results: element 4 q + j of a tile is column 8 q + 4 (lane / 32) + j of row lane % 32
+  // --- results. Element 4 q + j of a tile is column 8 q + 4 (lane / 32) + j of row lane % 32: 16 bytes of a
+  // row per pair of lanes. Each wave passes them through 8 KiB of LDS of its own, 32 rows at a time, so that
+  // a lane reads and writes global memory 16 bytes at a time and neighbours share cache lines. 16-byte chunk c
+  // of a row sits at c ^ (row % chunks), which keeps both directions free of bank conflicts.
+  lds_byte* const ep = (lds_byte*)out_lds + wave * 8192;
+  typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+  typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+  typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+  const int wrow = m0 + wr * MT * 32, r32 = lane & 31, hi4 = lane >> 5;
+  // The lanes of a wave exchange data through ep: its LDS accesses run in the order in which they are
+  // issued, and this keeps the compiler from changing that order.
+  auto in_order = [] { __asm__ volatile("" ::: "memory"); };
+  if constexpr (FORM == TF_GATE_UP || FORM == TF_DH) {
+    // 64 fp32 columns: 32 of g beside the same 32 of u, or 64 of dh
+    constexpr int BLOCKS = NT / 2;
+    auto put = [&](int i, int blk) __attribute__((always_inline)) {
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int m = m0 + (wr * MT + i) * 32 + (lane & 31);
-    if (m >= mend) continue;
+      for (int z = 0; z < 2; ++z) {
+        const f32x16& v = acc[FORM == TF_GATE_UP ? blk + z * (NT / 2) : 2 * blk + z][i];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *(lds_f32x4*)(ep + r32 * 256 + (((z * 8 + 2 * q + hi4) ^ (r32 & 15)) << 4)) =
+              f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+      }
+    };
+    auto get = [&](int row, int c) __attribute__((always_inline)) { return *(const lds_f32x4*)(ep + row * 256 + ((c ^ (row & 15)) << 4)); };
     if constexpr (FORM == TF_GATE_UP) {
-      bool ok = true;
-      if (a.slot_token) ok = (unsigned)a.slot_token[m] < (unsigned)a.xrows;
+      const int c8 = lane & 3;
 #pragma unroll
-      for (int t = 0; t < NT / 2; ++t)
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int n = n0 + wc * (NT * 16) + t * 32 + 8 * q + 4 * (lane >> 5);
-          if (n >= N) continue;
-          float gv[4], uv[4];
+        for (int blk = 0; blk < BLOCKS; ++blk) {
+          in_order();
+          put(i, blk);
+          in_order();
+          const int n = n0 + wc * (NT * 16) + blk * 32 + c8 * 8;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            gv[j] = ok ? acc[t][i][4 * q + j] : 0.f;
-            uv[j] = ok ? acc[t + NT / 2][i][4 * q + j] : 0.f;
+          for (int it = 0; it < 2; ++it) {
+            const int row = it * 16 + (lane >> 2), m = wrow + i * 32 + row;
+            f32x4 g0 = get(row, 2 * c8), g1 = get(row, 2 * c8 + 1), u0 = get(row, 8 + 2 * c8), u1 = get(row, 9 + 2 * c8);
+            if (m >= mend || n >= N) continue;
+            if (a.slot_token && (unsigned)a.slot_token[m] >= (unsigned)a.xrows) g0 = g1 = u0 = u1 = f32x4{0.f, 0.f, 0.f, 0.f};
+            const size_t at = m * I + n;
+            if (a.g) {
+              *(u32x4*)((uint16_t*)a.g + at) = pack8(g0, g1);
+              *(u32x4*)((uint16_t*)a.u + at) = pack8(u0, u1);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              g0[j] = silu(g0[j]) * u0[j];
+              g1[j] = silu(g1[j]) * u1[j];
+            }
+            *(u32x4*)((uint16_t*)a.h + at) = pack8(g0, g1);
           }
-          const size_t at = (m * I + n) * 2;
-          if (a.g) {
-            *(u32x2*)((uint8_t*)a.g + at) = u32x2{pack_bf16x2(gv[0], gv[1]), pack_bf16x2(gv[2], gv[3])};
-            *(u32x2*)((uint8_t*)a.u + at) = u32x2{pack_bf16x2(uv[0], uv[1]), pack_bf16x2(uv[2], uv[3])};
-          }
-          *(u32x2*)((uint8_t*)a.h + at) = u32x2{pack_bf16x2(silu(gv[0]) * uv[0], silu(gv[1]) * uv[1]),
-                                                pack_bf16x2(silu(gv[2]) * uv[2], silu(gv[3]) * uv[3])};
         }
     } else {
+      // the next block's g and u are fetched before this block's results are formed
+      const int c8 = lane & 7, r8 = lane >> 3;
+      u32x4 gw[2][4], uw[2][4];
+      auto fetch = [&](int b, int set) __attribute__((always_inline)) {
+        const int i = b / BLOCKS, n = n0 + (wc * NT + b % BLOCKS * 2) * 32 + c8 * 8;
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+          const int m = wrow + i * 32 + it * 8 + r8;
+          gw[set][it] = uw[set][it] = u32x4{0u, 0u, 0u, 0u};
+          if (m < mend && n < N) {
+            gw[set][it] = *(const u32x4*)((const uint16_t*)a.g + m * I + n);
+            uw[set][it] = *(const u32x4*)((const uint16_t*)a.u + m * I + n);
+          }
+        }
+      };
+      fetch(0, 0);
+#pragma unroll
+      for (int b = 0; b < MT * BLOCKS; ++b) {
+        if (b + 1 < MT * BLOCKS) fetch(b + 1, (b + 1) & 1);
+        in_order();
+        put(b / BLOCKS, b % BLOCKS);
+        in_order();
+        const int i = b / BLOCKS, n = n0 + (wc * NT + b % BLOCKS * 2) * 32 + c8 * 8;
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+          const int row = it * 8 + r8, m = wrow + i * 32 + row;
+          const f32x4 d[2] = {get(row, 2 * c8), get(row, 2 * c8 + 1)};
+          f32x4 dg[2], du[2], hv[2];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t gj2 = gw[b & 1][it][j >> 1], uj2 = uw[b & 1][it][j >> 1];
+            const float gj = (j & 1) ? bf16hi(gj2) : bf16lo(gj2), uj = (j & 1) ? bf16hi(uj2) : bf16lo(uj2);
+            const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-gj)), si = gj * s, dh = d[j >> 2][j & 3];
+            du[j >> 2][j & 3] = dh * si;
+            dg[j >> 2][j & 3] = dh * uj * (s + si * (1.0f - s));
+            hv[j >> 2][j & 3] = si * uj;
+          }
+          if (m >= mend || n >= N) continue;
+          uint16_t* const o = (uint16_t*)a.dgu + m * (2 * I) + n;
+          *(u32x4*)o = pack8(dg[0], dg[1]);
+          *(u32x4*)(o + I) = pack8(du[0], du[1]);
+          *(u32x4*)((uint16_t*)a.h + m * I + n) = pack8(hv[0], hv[1]);
+        }
+      }
+    }
+  } else {
+    // all the wave's columns in bf16
+    constexpr int RB = NT * 64, CH = RB / 16, RPI = 1024 / RB;  // bytes and chunks of a row, rows per access
+    const size_t ld = FORM == TF_DW && mat < 2 ? I : H;
+    uint16_t* const out = FORM == TF_DW ? (uint16_t*)(mat == 0 ? a.dgate : mat == 1 ? a.dup : a.ddown) + e * HI
+                                        : (uint16_t*)(FORM == TF_DOWN ? a.y : a.dx);
+    const int c = lane % CH, n = n0 + wc * NT * 32 + c * 8;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      in_order();
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int n = n0 + (wc * NT + t) * 32 + 8 * q + 4 * (lane >> 5);
-          const f32x4 v = {acc[t][i][4 * q], acc[t][i][4 * q + 1], acc[t][i][4 * q + 2], acc[t][i][4 * q + 3]};
-          if constexpr (FORM == TF_DH) {
-            if (n >= N) continue;
-            const u32x2 gw = *(const u32x2*)((const uint8_t*)a.g + (m * I + n) * 2);
-            const u32x2 uw = *(const u32x2*)((const uint8_t*)a.u + (m * I + n) * 2);
-            float dg[4], du[4], hv[4];
+        for (int q = 0; q < 4; ++q)
+          *(lds_u32x2*)(ep + r32 * RB + (((t * 4 + q) ^ (r32 % CH)) << 4) + hi4 * 8) =
+              u32x2{pack_bf16x2(acc[t][i][4 * q], acc[t][i][4 * q + 1]), pack_bf16x2(acc[t][i][4 * q + 2], acc[t][i][4 * q + 3])};
+      in_order();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float gj = (j & 1) ? bf16hi(gw[j >> 1]) : bf16lo(gw[j >> 1]);
-              const float uj = (j & 1) ? bf16hi(uw[j >> 1]) : bf16lo(uw[j >> 1]);
-              const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-gj)), si = gj * s;
-              du[j] = v[j] * si;
-              dg[j] = v[j] * uj * (s + si * (1.0f - s));
-              hv[j] = si * uj;
-            }
-            uint8_t* const o = (uint8_t*)a.dgu + (m * (2 * I) + n) * 2;
-            *(u32x2*)o = u32x2{pack_bf16x2(dg[0], dg[1]), pack_bf16x2(dg[2], dg[3])};
-            *(u32x2*)(o + I * 2) = u32x2{pack_bf16x2(du[0], du[1]), pack_bf16x2(du[2], du[3])};
-            *(u32x2*)((uint8_t*)a.h + (m * I + n) * 2) = u32x2{pack_bf16x2(hv[0], hv[1]), pack_bf16x2(hv[2], hv[3])};
-          } else {
-            uint8_t* o;
-            if constexpr (FORM == TF_DW) {
-              const size_t ld = mat == 2 ? H : I;
-              if (n >= (int)ld) continue;
-              o = (uint8_t*)(mat == 0 ? a.dgate : mat == 1 ? a.dup : a.ddown) + (e * HI + m * ld + n) * 2;
-            } else {
-              if (n >= N) continue;
-              o = (uint8_t*)(FORM == TF_DOWN ? a.y : a.dx) + (m * H + n) * 2;
-            }
-            *(u32x2*)o = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-          }
-        }
+      for (int it = 0; it < 32 / RPI; ++it) {
+        const int row = it * RPI + lane / CH, m = wrow + i * 32 + row;
+        const u32x4 v = *(const lds_u32x4*)(ep + row * RB + ((c ^ (row % CH)) << 4));
+        if (m < mend && n < (int)ld) *(u32x4*)(out + m * ld + n) = v;
+      }
     }
   }
 }
