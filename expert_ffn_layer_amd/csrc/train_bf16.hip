@@ -1,5 +1,19 @@
-// The gated feed-forward block's products in bf16 (v_mfma_f32_16x16x32_bf16); forms as listed in
-// train.h.
+// The gated feed-forward block's products in bf16 (v_mfma_f32_32x32x16_bf16); forms as listed in train.h.
+//
+// C[m][n] = sum_k P(m, k) Q(n, k), a tile of C per workgroup of 4 waves. Both operands go from global memory
+// to LDS without passing registers (global_load_lds), through a ring of D slots of 64 reduction elements, and
+// from there to the matrix cores a quarter of a slot (16 elements) at a time: while the products of one quarter
+// run, the next one is read, and loads for a later step go out, a few behind every quarter. Weights are read
+// as they are stored: an operand whose reduction index is contiguous (dy, dg | du, and the weights in the
+// gradients of h and x) is read 16 bytes a lane; one whose own index is (the weights in the forward products,
+// everything in the weight gradients) by transposing reads (ds_read_b64_tr_b16). Q is the MFMA's first operand,
+// so that a lane ends with 4 consecutive columns of one row.
+//
+// Bound by the matrix cores under the card's power limit: at 8192 rows, H 8192, I 4096 the forms reach 1160
+// (gate/up), 1280 (down), 1180 (dh), 1300 (dx) and 1380 (weight gradients) TFLOP/s on random data, where
+// the library's products of 8192^3 reach 1240, 1540 (dh and dx's layout) and 1090 (the weight
+// gradients' layout); on zeros, which cost little power, 1540, 1850, 1290, 1480 and 1990.
+#include <algorithm>
 #include <type_traits>
 
 #include "train.h"
@@ -31,15 +45,17 @@ __device__ const uint4 zero_chunk = {0u, 0u, 0u, 0u};
 //     chunk c of row r sits at c ^ ((r >> 1) & 7), so that 16 lanes' reads cover all 64 banks.
 //   MC (own index contiguous): a row of L indices per reduction element, read 4 x 16 at a time by the
 //     transposing read; 32-byte chunk c of row r sits at c ^ swz(r), so that its 4 rows differ in bank.
-template <int L, bool KC>
+template <int L, bool KC, bool HALVES>
 struct Tile {
   static constexpr int UNITS = L / 8;
   static constexpr int BYTES = L * BK * 2;
   static constexpr int LPR = L / 8;  // MC: lanes per row
   __device__ static constexpr int swz(int r) { return L >= 128 ? ((r & 3) << 1) : (r & 2); }
-  // unit that wave w of 4 moves as its q-th: MC: the first half of them makes the slot's first 32 rows
+  // unit that wave w of 4 moves as its q-th; with HALVES the first half of them makes the slot's first 32 rows
   static constexpr int U = UNITS / 4;
-  __device__ static int unit(int q, int w) { return KC ? w * U + q : (q / (U / 2)) * (UNITS / 2) + w * (U / 2) + q % (U / 2); }
+  __device__ static int unit(int q, int w) {
+    return HALVES ? (q / (U / 2)) * (UNITS / 2) + w * (U / 2) + q % (U / 2) : w * U + q;
+  }
   // index (KC) or reduction element (MC) that lane l of unit u moves
   __device__ static int row(int u, int l) { return KC ? u * 8 + (l >> 3) : (u * 64 + l) / LPR; }
   // first of the 8 elements it moves: reduction elements (KC) or indices (MC)
@@ -73,42 +89,74 @@ __device__ __forceinline__ bf16x8 read_frag(const lds_byte* at) {
   }
 }
 
-// Which loads go behind which phase (quarter) of a step. Quarter h + 1 is read in phase h, so the first
-// half of a slot is free after phase 0 and all of it after phase 2.
-//   MC operand: phases 1, 2 of step s bring the first half of stage s + 2, phases 3 of s and 0 of s + 1 its
-//     second half.
-//   KC operand: phases 3 of step s and 0, 1 of s + 1 bring stage s + 2.
+// The weight gradients' tiles, square ones of 128 or 256: 3 E matrices of `longer` x `shorter` tiles, cut along
+// the longer side into `per` units of up to `len` x `shorter`
+struct DwUnits {
+  int longer, shorter, len, per, tiles;
+};
+__host__ __device__ __forceinline__ DwUnits dw_units(int H, int I, int E, int bm) {
+  DwUnits u;
+  const int th = (H + bm - 1) / bm, ti = (I + bm - 1) / bm;
+  u.longer = th > ti ? th : ti;
+  u.shorter = th > ti ? ti : th;
+  // units of about 4, of 1 where the XCDs would else get few and unequal numbers of them
+  const int cut = 3 * E * ((u.longer + 3) / 4) >= 64 ? (u.longer + 3) / 4 : u.longer;
+  u.len = (u.longer + cut - 1) / cut;
+  u.per = (u.longer + u.len - 1) / u.len;
+  u.tiles = u.len * u.shorter;
+  return u;
+}
+
+// Number of row tiles of bm rows that the groups take, the same for every lane of a wave
+__device__ __forceinline__ int row_tiles(const int32_t* off, int E, int P, int bm) {
+  if (!off) return (P + bm - 1) / bm;
+  const int lane = threadIdx.x & 63;
+  int n = 0;
+  for (int e = lane; e < E; e += 64) {
+    int b, z;
+    group_rows(off, e, P, b, z);
+    n += (z - b + bm - 1) / bm;
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d);
+  return __builtin_amdgcn_readfirstlane(n);
+}
+
+// Which loads go behind which phase (quarter) of a step, for a ring of D slots. Quarter h + 1 is read in phase
+// h, so the first half of a slot is free after phase 0 and all of it after phase 2.
+//   whole slots: phases 3 of step s and 0, 1 of s + 1 bring stage s + D.
+//   halves: phases 1, 2 of step s bring the first half of stage s + D, phases 3 of s and 0 of s + 1 its second
+//     half.
 // U loads each per wave and stage, spread evenly: bursts lengthen the wait for all of them.
-template <bool KC, int U>
+template <bool HALVES, int U>
 struct Share {
-  // cumulative loads before the k-th of the phases in their order: 3 0 1 2 (KC), 1 2 3 0 (MC)
-  static constexpr int cum(int k) { return KC ? (k >= 3 ? U : (U * 3 * k + 7) / 8) : U * k / 4; }
-  static constexpr int from(int ph, int past = 0) { return cum((KC ? (ph + 1) % 4 : (ph + 3) % 4) + past); }
+  // cumulative loads before the k-th of the phases in their order: 3 0 1 2 (whole), 1 2 3 0 (halves)
+  static constexpr int cum(int k) { return HALVES ? U * k / 4 : (k >= 3 ? U : (U * 3 * k + 7) / 8); }
+  static constexpr int from(int ph, int past = 0) { return cum((HALVES ? (ph + 3) % 4 : (ph + 1) % 4) + past); }
   static constexpr int count(int ph) { return from(ph, 1) - from(ph); }
 };
 
-template <int FORM, int WR, int WC, int MT, int NT>
-__global__ void __launch_bounds__(THR, 1) train_bf16_kernel(const TrainArgs a) {
+template <int FORM, int WR, int WC, int MT, int NT, int D>
+__global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) train_bf16_kernel(const TrainArgs a) {
   constexpr bool P_KC = FORM != TF_DW, Q_KC = FORM == TF_DH || FORM == TF_DX;
   constexpr int BM = WR * MT * 32, BN = WC * NT * 32;
-  using TP = Tile<BM, P_KC>;
-  using TQ = Tile<BN, Q_KC>;
+  constexpr bool P_HV = !P_KC && D == 2, Q_HV = !Q_KC && D == 2;  // slots freed and filled by halves
+  using TP = Tile<BM, P_KC, P_HV>;
+  using TQ = Tile<BN, Q_KC, Q_HV>;
   constexpr int UP = TP::U, UQ = TQ::U, L = UP + UQ;  // loads per wave and stage
   static_assert(WR * WC == 4, "four waves share the units");
-  using SP = Share<P_KC, UP>;
-  using SQ = Share<Q_KC, UQ>;
-  constexpr bool KCKC = P_KC && Q_KC;
+  using SP = Share<P_HV, UP>;
+  using SQ = Share<Q_HV, UQ>;
   constexpr int OUTN = FORM == TF_GATE_UP ? BN / 2 : BN;  // columns of the output (per matrix)
-  // Two slots for each operand; those of a KC operand are freed and filled whole (a cache line of every
-  // row), those of a MC one by halves of 32 rows. One array for each such part: the compiler then sees which
+  // D slots for each operand; with two slots those of a MC operand are freed and filled by halves of 32 rows,
+  // all others whole (a cache line of every row). One array for each such part: the compiler then sees which
   // loads to LDS a read has to wait for.
-  constexpr int PK = P_KC ? TP::BYTES : 16, QK = Q_KC ? TQ::BYTES : 16;
-  constexpr int PH = P_KC ? 16 : TP::BYTES / 2, QH = Q_KC ? 16 : TQ::BYTES / 2;
-  __shared__ __align__(1024) uint8_t pk0[PK], pk1[PK], qk0[QK], qk1[QK];
-  __shared__ __align__(1024) uint8_t p0a[PH], p0b[PH], p1a[PH], p1b[PH], q0a[QH], q0b[QH], q1a[QH], q1b[QH];
-  __shared__ __align__(1024) uint8_t out_lds[4 * 8192];
-#define P_PART(SLOT, B) ((lds_byte*)(P_KC ? ((SLOT) ? pk1 : pk0) : (SLOT) == 0 ? ((B) ? p0b : p0a) : ((B) ? p1b : p1a)))
-#define Q_PART(SLOT, B) ((lds_byte*)(Q_KC ? ((SLOT) ? qk1 : qk0) : (SLOT) == 0 ? ((B) ? q0b : q0a) : ((B) ? q1b : q1a)))
+  constexpr int PA = P_HV ? TP::BYTES / 2 : TP::BYTES, QA = Q_HV ? TQ::BYTES / 2 : TQ::BYTES;
+  constexpr int PX = P_HV || D == 4 ? PA : 16, QX = Q_HV || D == 4 ? QA : 16;
+  __shared__ __align__(1024) uint8_t p0[PA], p1[PA], p2[PX], p3[PX], q0[QA], q1[QA], q2[QX], q3[QX];
+  // part B (0 or 1, of halves) of a slot
+#define P_PART(SLOT, B) ((lds_byte*)((SLOT) + (P_HV && (B) ? 2 : 0) == 0 ? p0 : (SLOT) + (P_HV && (B) ? 2 : 0) == 1 ? p1 : (SLOT) + (P_HV && (B) ? 2 : 0) == 2 ? p2 : p3))
+#define Q_PART(SLOT, B) ((lds_byte*)((SLOT) + (Q_HV && (B) ? 2 : 0) == 0 ? q0 : (SLOT) + (Q_HV && (B) ? 2 : 0) == 1 ? q1 : (SLOT) + (Q_HV && (B) ? 2 : 0) == 2 ? q2 : q3))
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / WC, wc = wave % WC;
   const size_t H = a.H, I = a.I, HI = H * I;
@@ -117,38 +165,40 @@ __global__ void __launch_bounds__(THR, 1) train_bf16_kernel(const TrainArgs a) {
   int e = 0, m0, mend, n0, K, beg = 0, mat = 0;
   const int N = FORM == TF_DOWN || FORM == TF_DX ? a.H : a.I;
   {
-    // superblocks of 4 x 8 tiles go to the XCDs in turn, so that the tiles which one XCD runs at the
-    // same time share operands in its L2
-    const int b = blockIdx.x;
-    const int sb = (b / (32 * NXCD)) * NXCD + b % NXCD, in = (b / NXCD) % 32;
+    // Workgroup b runs on XCD b % 8. What one XCD runs at a time shares operands in its L2.
+    const int xcd = blockIdx.x % NXCD, j = blockIdx.x / NXCD;
     if constexpr (FORM == TF_DW) {
-      const int tg_m = (a.H + BM - 1) / BM, tg_n = (a.I + BN - 1) / BN, td_m = (a.I + BM - 1) / BM, td_n = (a.H + BN - 1) / BN;
-      const int sg_n = (tg_n + 7) / 8, sg = (tg_m + 3) / 4 * sg_n, sd_n = (td_n + 7) / 8, sd = (td_m + 3) / 4 * sd_n;
-      const int per = 2 * sg + sd;
-      e = sb / per;
-      if (e >= a.E) return;
-      int r = sb % per;
-      mat = r < sg ? 0 : r < 2 * sg ? 1 : 2;
-      r -= mat * sg;
-      const int sn = mat == 2 ? sd_n : sg_n;
-      const int tm = r / sn * 4 + in % 4, tn = r % sn * 8 + in / 4;
-      if (tm >= (mat == 2 ? td_m : tg_m) || tn >= (mat == 2 ? td_n : tg_n)) return;
-      m0 = tm * BM;
-      n0 = tn * BN;
+      // units of `len` tiles of the longer side x all of the shorter side go to the XCDs in turn
+      const DwUnits u = dw_units(a.H, a.I, a.E, BM);
+      const int unit = xcd + NXCD * (j / u.tiles), in = j % u.tiles;
+      if (unit >= u.per * 3 * a.E) return;
+      e = unit / (3 * u.per);
+      mat = unit / u.per % 3;
+      const int lt = unit % u.per * u.len + in % u.len, st = in / u.len;
+      if (lt >= u.longer) return;
+      // gate and up have H rows, down has them as columns; the longer side may be either
+      const bool rows_long = (a.H >= a.I) == (mat < 2);
+      m0 = (rows_long ? lt : st) * BM;
+      n0 = (rows_long ? st : lt) * BN;
       mend = mat == 2 ? a.I : a.H;
+      if (m0 >= mend || n0 >= (mat == 2 ? a.H : a.I)) return;
       int end;
       group_rows(a.off, e, a.P, beg, end);
       K = end - beg;
     } else {
-      const int tn_all = (N + OUTN - 1) / OUTN, sn = (tn_all + 7) / 8;
-      const int tm = sb / sn * 4 + in % 4, tn = sb % sn * 8 + in / 4;
-      if (tn >= tn_all) return;
+      // 4 row tiles x all columns after each other; each XCD gets an equal run of the tiles that exist
+      const int cols = (N + OUTN - 1) / OUTN, rows = row_tiles(a.off, a.E, a.P, BM);
+      const int n = rows * cols, round = j / 32, left = n - round * 32 * NXCD;
+      const int chunk = left >= 32 * NXCD ? 32 : (left + NXCD - 1) / NXCD;
+      const int id = round * 32 * NXCD + xcd * chunk + j % 32;
+      if (j % 32 >= chunk || id >= n) return;
+      const int rb = id / (4 * cols), rr = min(4, rows - 4 * rb), rem = id - rb * 4 * cols;
       RowTile t;
-      if (!find_row_tile(a.off, a.E, a.P, BM, tm, t)) return;
+      if (!find_row_tile(a.off, a.E, a.P, BM, rb * 4 + rem % rr, t)) return;
       e = t.e;
       m0 = t.row0;
       mend = t.end;
-      n0 = tn * OUTN;
+      n0 = rem / rr * OUTN;
       K = FORM == TF_GATE_UP || FORM == TF_DH ? a.H : FORM == TF_DOWN ? a.I : 2 * a.I;
     }
   }
@@ -230,14 +280,14 @@ __global__ void __launch_bounds__(THR, 1) train_bf16_kernel(const TrainArgs a) {
     const size_t adv = FORM == TF_DW || step + 1 < nsteps ? pstride : 0;
     const int un = TP::unit(q, wave);
     lds_byte* const part = P_PART(decltype(slot)::value, q >= UP / 2);
-    load_one(psrc[q], part + (P_KC ? un : un % (TP::UNITS / 2)) * 1024, TP::row(un, lane), adv, step);
+    load_one(psrc[q], part + (P_HV ? un % (TP::UNITS / 2) : un) * 1024, TP::row(un, lane), adv, step);
   };
   auto load_q = [&](int q, int step, auto slot) __attribute__((always_inline)) {
     size_t adv = FORM == TF_DW || step + 1 < nsteps ? qstride : 0;
     if constexpr (FORM == TF_DX) adv += step + 1 == half_steps ? qjump : 0;
     const int un = TQ::unit(q, wave);
     lds_byte* const part = Q_PART(decltype(slot)::value, q >= UQ / 2);
-    load_one(qsrc[q], part + (Q_KC ? un : un % (TQ::UNITS / 2)) * 1024, TQ::row(un, lane), adv, step);
+    load_one(qsrc[q], part + (Q_HV ? un % (TQ::UNITS / 2) : un) * 1024, TQ::row(un, lane), adv, step);
   };
 
   f32x16 acc[NT][MT];
@@ -260,30 +310,30 @@ __global__ void __launch_bounds__(THR, 1) train_bf16_kernel(const TrainArgs a) {
     auto read_p = [&](int i, auto quarter, auto slot) __attribute__((always_inline)) {
       constexpr int h = decltype(quarter)::value;
       lds_byte* const part = P_PART(decltype(slot)::value, h >= 2);
-      pf[h & 1][i] = read_frag<BM, P_KC>(part + (P_KC ? pb[h] + i * 4096 : pb[i] + (h & 1) * 16 * (BM * 2)));
+      pf[h & 1][i] = read_frag<BM, P_KC>(part + (P_KC ? pb[h] + i * 4096 : pb[i] + (P_HV ? h & 1 : h) * 16 * (BM * 2)));
     };
     auto read_q = [&](int t, auto quarter, auto slot) __attribute__((always_inline)) {
       constexpr int h = decltype(quarter)::value;
       lds_byte* const part = Q_PART(decltype(slot)::value, h >= 2);
-      qf[h & 1][t] = read_frag<BN, Q_KC>(part + (Q_KC ? qb[h] + t * 4096 : qb[t] + (h & 1) * 16 * (BN * 2)));
+      qf[h & 1][t] = read_frag<BN, Q_KC>(part + (Q_KC ? qb[h] + t * 4096 : qb[t] + (Q_HV ? h & 1 : h) * 16 * (BN * 2)));
     };
     constexpr std::integral_constant<int, 0> C0{};
     constexpr std::integral_constant<int, 1> C1{};
     constexpr std::integral_constant<int, 2> C2{};
     constexpr std::integral_constant<int, 3> C3{};
-    // the n-th load of phase ph of step s, KC operands' first; slot: that of step s
+    // the n-th load of phase ph of step s, those of whole slots first; slot: that of step s
     auto load_nth = [&](auto ph_c, int n, int s, auto slot) __attribute__((always_inline)) {
       constexpr int ph = decltype(ph_c)::value, np = SP::count(ph), nq = SQ::count(ph);
-      constexpr std::integral_constant<int, decltype(slot)::value ^ 1> other{};
-      const bool p = P_KC ? n < np : n >= nq;
-      const int at = p ? SP::from(ph) + (P_KC ? n : n - nq) : SQ::from(ph) + (P_KC ? n - np : n);
-      // phase 0, and phase 1 of a KC operand, still bring stage s + 1, into the slot that is not step s's
+      constexpr std::integral_constant<int, (decltype(slot)::value + D - 1) % D> before{};
+      const bool p = Q_HV ? n < np : n >= nq;
+      const int at = p ? SP::from(ph) + (Q_HV ? n : n - nq) : SQ::from(ph) + (Q_HV ? n - np : n);
+      // phase 0, and phase 1 for whole slots, still bring stage s + D - 1, into the slot of step s - 1
       if (p) {
-        if constexpr (ph == 0 || (P_KC && ph == 1)) load_p(at, s + 1, other);
-        else load_p(at, s + 2, slot);
+        if constexpr (ph == 0 || (!P_HV && ph == 1)) load_p(at, s + D - 1, before);
+        else load_p(at, s + D, slot);
       } else {
-        if constexpr (ph == 0 || (Q_KC && ph == 1)) load_q(at, s + 1, other);
-        else load_q(at, s + 2, slot);
+        if constexpr (ph == 0 || (!Q_HV && ph == 1)) load_q(at, s + D - 1, before);
+        else load_q(at, s + D, slot);
       }
     };
     // Products of quarter h, with the reads of the next quarter early behind them and the phase's loads spread
@@ -306,13 +356,13 @@ __global__ void __launch_bounds__(THR, 1) train_bf16_kernel(const TrainArgs a) {
         __builtin_amdgcn_sched_barrier(0);
       }
     };
-    // Loads that may still be in flight: where a MC operand's second half is wanted (after phase 0), those of
-    // one step; where the next stage is wanted (after phase 2), those since the last one of a KC operand, or
-    // of one step where there is none.
+    // Loads that may still be in flight: where the second half of a slot is wanted (after phase 0), those of one
+    // step; where the next stage is wanted (after phase 2), those since the last one of a whole slot of it, or of
+    // one step where there is none.
     constexpr int FLY0 = L;
-    constexpr int FLY2 = KCKC ? 0 : !P_KC && !Q_KC ? L : (P_KC ? SQ::count(1) + SQ::count(2) : SP::count(1) + SP::count(2));
+    constexpr int FLY2 = P_HV && Q_HV ? L : (D - 2) * L + (P_HV ? SP::count(1) + SP::count(2) : 0) + (Q_HV ? SQ::count(1) + SQ::count(2) : 0);
     auto body = [&](int s, auto slot) __attribute__((always_inline)) {
-      constexpr std::integral_constant<int, decltype(slot)::value ^ 1> other{};
+      constexpr std::integral_constant<int, (decltype(slot)::value + 1) % D> other{};
       // opaque in every step, so that the slot stays a constant and does not become a register per slot and
       // fragment
 #pragma unroll
@@ -320,7 +370,7 @@ __global__ void __launch_bounds__(THR, 1) train_bf16_kernel(const TrainArgs a) {
 #pragma unroll
       for (int t = 0; t < NT && !Q_KC; ++t) asm volatile("" : "+v"(qb[t]));
       phase(C0, slot, s, slot);
-      if constexpr (!KCKC) {
+      if constexpr (P_HV || Q_HV) {
         MOE_WAIT_LGKM0();
         MOE_WAIT_VMCNT(FLY0);
         __builtin_amdgcn_s_barrier();
@@ -333,25 +383,42 @@ __global__ void __launch_bounds__(THR, 1) train_bf16_kernel(const TrainArgs a) {
       phase(C3, other, s, slot);
     };
     // what the steps before the first would have loaded, stage 0 first
+    auto whole = [&](int step, auto slot) __attribute__((always_inline)) {
 #pragma unroll
-    for (int q = 0; q < UQ; ++q) load_q(q, 0, C0);
+      for (int q = 0; q < UQ; ++q) load_q(q, step, slot);
 #pragma unroll
-    for (int q = 0; q < UP; ++q) load_p(q, 0, C0);
-    constexpr int Q1 = Q_KC ? 0 : UQ / 2, P1 = P_KC ? 0 : UP / 2;  // of stage 1, before phase 3 of step -1
+      for (int q = 0; q < UP; ++q) load_p(q, step, slot);
+    };
+    whole(0, C0);
+    if constexpr (D == 4) {
+      whole(1, C1);
+      whole(2, C2);
+    }
+    constexpr int Q1 = Q_HV ? UQ / 2 : 0, P1 = P_HV ? UP / 2 : 0;  // of stage 1, before phase 3 of step -1
 #pragma unroll
     for (int q = 0; q < Q1; ++q) load_q(q, 1, C1);
 #pragma unroll
     for (int q = 0; q < P1; ++q) load_p(q, 1, C1);
+    constexpr std::integral_constant<int, D - 1> last{};
 #pragma unroll
-    for (int n = 0; n < SP::count(3) + SQ::count(3); ++n) load_nth(C3, n, -1, C1);
-    MOE_WAIT_VMCNT(Q1 + P1 + SP::count(3) + SQ::count(3));
+    for (int n = 0; n < SP::count(3) + SQ::count(3); ++n) load_nth(C3, n, -1, last);
+    MOE_WAIT_VMCNT((D - 2) * L + Q1 + P1 + SP::count(3) + SQ::count(3));
     __builtin_amdgcn_s_barrier();
 #pragma unroll
     for (int t = 0; t < NT; ++t) read_q(t, C0, C0);
 #pragma unroll
     for (int i = 0; i < MT; ++i) read_p(i, C0, C0);
     // pairs of steps: H and I are multiples of 128, the rows of TF_DW end in zeros
-    for (int s = 0; s < nsteps; s += 2) {
+    int s = 0;
+    if constexpr (D == 4) {
+      for (; s + 2 < nsteps; s += 4) {
+        body(s, C0);
+        body(s + 1, C1);
+        body(s + 2, C2);
+        body(s + 3, C3);
+      }
+    }
+    for (; s < nsteps; s += 2) {
       body(s, C0);
       body(s + 1, C1);
     }
@@ -361,8 +428,13 @@ __global__ void __launch_bounds__(THR, 1) train_bf16_kernel(const TrainArgs a) {
   // --- results. Element 4 q + j of a tile is column 8 q + 4 (lane / 32) + j of row lane % 32: 16 bytes of a
   // row per pair of lanes. Each wave passes them through 8 KiB of LDS of its own, 32 rows at a time, so that
   // a lane reads and writes global memory 16 bytes at a time and neighbours share cache lines. 16-byte chunk c
-  // of a row sits at c ^ (row % chunks), which keeps both directions free of bank conflicts.
-  lds_byte* const ep = (lds_byte*)out_lds + wave * 8192;
+  // of a row sits at c ^ (row % chunks), which keeps both directions free of bank conflicts. The parts of the
+  // ring serve for it: nothing is read or loaded there any more.
+  static_assert((Q_HV || D == 4 ? QA : QA / 2) >= 8192, "a part of the ring per wave");
+  __builtin_amdgcn_s_barrier();
+  lds_byte* ep;
+  if constexpr (Q_HV || D == 4) ep = (lds_byte*)(wave == 0 ? q0 : wave == 1 ? q1 : wave == 2 ? q2 : q3);
+  else ep = (lds_byte*)(wave & 2 ? q1 : q0) + (wave & 1) * (QA / 2);
   typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
   typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
   typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
@@ -497,31 +569,72 @@ __global__ void __launch_bounds__(THR) gather_kernel(const TrainArgs a) {
   *((u32x4*)a.xg + id) = v;
 }
 
-template <int FORM>
+template <int FORM, int WR, int WC, int MT, int NT, int D>
 hipError_t launch(const TrainArgs& a, hipStream_t st) {
-  constexpr int BM = 256, BN = 256;
-  long long sbs;
+  constexpr int BM = WR * MT * 32, BN = WC * NT * 32;
+  long long n;
   if (FORM == TF_DW) {
-    auto blocks = [](int m, int n) { return (long long)((m + BM - 1) / BM + 3) / 4 * (((n + BN - 1) / BN + 7) / 8); };
-    sbs = (2 * blocks(a.H, a.I) + blocks(a.I, a.H)) * a.E;
+    static_assert(FORM != TF_DW || BM == BN, "square tiles");
+    const DwUnits u = dw_units(a.H, a.I, a.E, BM);
+    n = ((long long)u.per * 3 * a.E + NXCD - 1) / NXCD * u.tiles;
   } else {
     const int N = FORM == TF_DOWN || FORM == TF_DX ? a.H : a.I, outn = FORM == TF_GATE_UP ? BN / 2 : BN;
-    sbs = (max_row_tiles(a.P, a.E, BM) + 3) / 4 * (((N + outn - 1) / outn + 7) / 8);
+    n = max_row_tiles(a.P, a.E, BM) * ((N + outn - 1) / outn);
+    n = n / (32 * NXCD) * 32 + (n % (32 * NXCD) + NXCD - 1) / NXCD;
   }
-  if (sbs == 0) return hipSuccess;
-  const unsigned grid = (unsigned)((sbs + NXCD - 1) / NXCD * NXCD * 32);
-  train_bf16_kernel<FORM, 2, 2, 4, 4><<<grid, THR, 0, st>>>(a);
+  if (n == 0) return hipSuccess;
+  const unsigned grid = (unsigned)(n * NXCD);
+  train_bf16_kernel<FORM, WR, WC, MT, NT, D><<<grid, THR, 0, st>>>(a);
   return hipGetLastError();
+}
+
+// Which tile. The estimates are in microseconds per step of 64 reduction elements and round of the card,
+// fitted to runs at 16 to 32768 rows, 1 to 32 groups and the V3 and Qwen3 widths (one CU takes one 256 x 256
+// or deep-ring workgroup, two 128 x 128 ones):
+//   256 x 256            1.2
+//   128 x 128            1.1 a round of 512, 0.75 where each has a CU to itself
+//   64 x 256, 4 slots    0.67     64 x 128, 4 slots    0.43
+// Large problems are bound by the matrix cores and take the tile that reads LDS least; few or thin groups
+// leave CUs empty or rows unused, and there the latency of a step counts: more and smaller tiles, more stages in
+// flight. Measured on gate/up, best of the others in brackets: 32768 rows in 32 groups 1.78 ms (2.49); one
+// group of 1027 rows, H 4096, I 1536: 43 us (79 as 256 x 256); 440 rows in 16 groups 84 us (99).
+template <int FORM>
+hipError_t choose(const TrainArgs& a, hipStream_t st) {
+  auto rounds = [](double tiles, int per) { return (double)(long long)((tiles + per - 1) / per); };
+  if constexpr (FORM == TF_DW) {
+    // per tile also its start and the writing of its results, which two workgroups on a CU hide; the 128 x 128
+    // tiles' shorter rows of results cost at least 8.6 us a round
+    const double steps = ((double)a.P / a.E + 127) / 128 * 2;
+    const auto tiles = [&](int b) { return 3.0 * a.E * ((a.H + b - 1) / b) * ((a.I + b - 1) / b); };
+    const double big = rounds(tiles(256), 256) * (steps + 12), small = rounds(tiles(128), 512) * std::max(steps + 1, 8.6);
+    return big <= small ? launch<FORM, 2, 2, 4, 4, 2>(a, st) : launch<FORM, 2, 2, 2, 2, 2>(a, st);
+  } else {
+    const int N = FORM == TF_DOWN || FORM == TF_DX ? a.H : a.I, share = FORM == TF_GATE_UP ? 2 : 1;
+    auto tiles = [&](int bm, int bn) {
+      const int groups = std::min(a.E, a.P);
+      const double rows = a.E == 1 ? (a.P + bm - 1) / bm : std::max<double>(groups, (double)a.P / bm + groups * 0.5);
+      return rows * ((N * share + bn - 1) / bn);
+    };
+    const double b = tiles(128, 128);
+    const double t[4] = {rounds(tiles(256, 256), 256) * 1.2, rounds(b, 512) * (b > 256 ? 1.1 : 0.75),
+                         rounds(tiles(64, 256), 256) * 0.67, rounds(tiles(64, 128), 256) * 0.43};
+    switch (std::min_element(t, t + 4) - t) {
+      case 0: return launch<FORM, 2, 2, 4, 4, 2>(a, st);
+      case 1: return launch<FORM, 2, 2, 2, 2, 2>(a, st);
+      case 2: return launch<FORM, 1, 4, 2, 2, 4>(a, st);
+      default: return launch<FORM, 2, 2, 1, 2, 4>(a, st);
+    }
+  }
 }
 
 }  // namespace
 
 hipError_t launch_train_bf16(TrainForm form, const TrainArgs& a, hipStream_t st) {
   switch (form) {
-    case TF_GATE_UP: return launch<TF_GATE_UP>(a, st);
-    case TF_DOWN: return launch<TF_DOWN>(a, st);
-    case TF_DH: return launch<TF_DH>(a, st);
-    case TF_DX: return launch<TF_DX>(a, st);
+    case TF_GATE_UP: return choose<TF_GATE_UP>(a, st);
+    case TF_DOWN: return choose<TF_DOWN>(a, st);
+    case TF_DH: return choose<TF_DH>(a, st);
+    case TF_DX: return choose<TF_DX>(a, st);
     case TF_DW: {
       TrainArgs b = a;
       if (a.slot_token && a.P) {
@@ -531,7 +644,7 @@ hipError_t launch_train_bf16(TrainForm form, const TrainArgs& a, hipStream_t st)
         b.x = a.xg;
         b.slot_token = nullptr;
       }
-      return launch<TF_DW>(b, st);
+      return choose<TF_DW>(b, st);
     }
   }
   return hipErrorInvalidValue;
