@@ -213,8 +213,7 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) train_bf16_kernel(co
   for (int u = 0; u < UP; ++u) {
     const int un = TP::unit(u, wave), r = TP::row(un, lane), c = TP::elem(un, lane);
     if constexpr (P_KC) {
-      // rows past the group's end repeat its last one: their results are not stored
-      const int row = m0 + r < mend ? m0 + r : mend - 1;
+      const int row = m0 + r < mend ? m0 + r : mend - 1;  // past the group's end: not read
       if constexpr (FORM == TF_GATE_UP) {
         int s = a.slot_token ? a.slot_token[row] : row;
         if ((unsigned)s >= (unsigned)a.xrows) s = 0;  // its results become zeros
@@ -267,11 +266,12 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) train_bf16_kernel(co
     }
   }
   // One load of stage `step` to LDS; the source moves on by one step, and stays on the last one, whose
-  // repeats nothing reads. TF_DW: rows past the group's end read zeros.
+  // repeats nothing reads. With left < 0 (rows past the group's end) zeros come instead: they keep other rows'
+  // values out of the sums, and where the results are not stored they save the power of a row's products
+  // (1.5 to 2% of dh and dx of the ragged V3 slice).
   const int half_steps = (int)I / BK;
-  auto load_one = [&](const uint8_t*& src, lds_byte* dst, int row, size_t adv, int step) __attribute__((always_inline)) {
-    const uint8_t* from = src;
-    if constexpr (FORM == TF_DW) from = row < K - step * BK ? from : (const uint8_t*)&zero_chunk;
+  auto load_one = [&](const uint8_t*& src, lds_byte* dst, int left, size_t adv) __attribute__((always_inline)) {
+    const uint8_t* const from = left >= 0 ? src : (const uint8_t*)&zero_chunk;
     __builtin_amdgcn_global_load_lds((const void*)from, (lds_void*)dst, 16, 0, 0);
     src += adv;
     asm volatile("" : "+v"(src));  // one running pointer a load, not one per load and slot
@@ -280,14 +280,16 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) train_bf16_kernel(co
     const size_t adv = FORM == TF_DW || step + 1 < nsteps ? pstride : 0;
     const int un = TP::unit(q, wave);
     lds_byte* const part = P_PART(decltype(slot)::value, q >= UP / 2);
-    load_one(psrc[q], part + (P_HV ? un % (TP::UNITS / 2) : un) * 1024, TP::row(un, lane), adv, step);
+    load_one(psrc[q], part + (P_HV ? un % (TP::UNITS / 2) : un) * 1024,
+             (P_KC ? mend - m0 : K - step * BK) - 1 - TP::row(un, lane), adv);
   };
   auto load_q = [&](int q, int step, auto slot) __attribute__((always_inline)) {
     size_t adv = FORM == TF_DW || step + 1 < nsteps ? qstride : 0;
     if constexpr (FORM == TF_DX) adv += step + 1 == half_steps ? qjump : 0;
     const int un = TQ::unit(q, wave);
     lds_byte* const part = Q_PART(decltype(slot)::value, q >= UQ / 2);
-    load_one(qsrc[q], part + (Q_HV ? un % (TQ::UNITS / 2) : un) * 1024, TQ::row(un, lane), adv, step);
+    load_one(qsrc[q], part + (Q_HV ? un % (TQ::UNITS / 2) : un) * 1024,
+             FORM == TF_DW ? K - step * BK - 1 - TQ::row(un, lane) : 0, adv);
   };
 
   f32x16 acc[NT][MT];

@@ -120,12 +120,22 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _device_of(t):
-    """The tensor's GPU as the current one, so that the call and its stream belong to it."""
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _run(t, stream, call):
+    """call(stream handle) with t's GPU as the current one, so that the call and its stream belong to it."""
     import torch
-    if not t.is_cuda:
+    i = t.get_device()
+    if i < 0:
         raise ValueError("a tensor of the call is not on a GPU")
-    return torch.cuda.device(t.device)
+    if i != torch.cuda.current_device():
+        with torch.cuda.device(i):
+            return _run(t, stream, call)
+    rc = call(torch._C._cuda_getCurrentRawStream(i) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc)
 
 
 def make_shape(T, H, E, k, I, I_shared=0, act="bf16", w_routed="bf16", w_shared="bf16", path="auto") -> MoeShape:
@@ -273,29 +283,25 @@ def moe_train_workspace_size(shape: MoeShape) -> int:
 
 def moe_gated_ffn(shape, x, expert_offsets, slot_token, weights_: dict, gate_pre, up_pre, y_perm, ws, stream=None):
     """Weights row-major: gate, up [E, H, I], down [E, I, H]. gate_pre and up_pre may both be None."""
-    w = weights(weights_)
-    with _device_of(ws):
-        _check(load().moe_gated_ffn(ctypes.byref(shape), _p(x), _p(expert_offsets), _p(slot_token), ctypes.byref(w),
-                                    _p(gate_pre), _p(up_pre), _p(y_perm), _p(ws), ws.numel() * ws.element_size(),
-                                    _stream(stream)))
+    w = MoeWeights(weights_["gate"].data_ptr(), weights_["up"].data_ptr(), weights_["down"].data_ptr())
+    _run(ws, stream, lambda st: load().moe_gated_ffn(
+        shape, _ptr(x), _ptr(expert_offsets), _ptr(slot_token), w, _ptr(gate_pre), _ptr(up_pre), _ptr(y_perm),
+        ws.data_ptr(), ws.nbytes, st))
 
 
 def moe_gated_ffn_backward(shape, x, expert_offsets, slot_token, weights_: dict, gate_pre, up_pre, dy_perm, dx_perm,
                            grads: dict | None, ws, stream=None):
     """grads: gate, up and down tensors that receive the weights' gradients, or None; dx_perm may be None."""
-    w = weights(weights_)
-    g = None if grads is None else MoeWeightGrads(*[grads[n].data_ptr() for n in ("gate", "up", "down")])
-    with _device_of(ws):
-        _check(load().moe_gated_ffn_backward(ctypes.byref(shape), _p(x), _p(expert_offsets), _p(slot_token),
-                                             ctypes.byref(w), _p(gate_pre), _p(up_pre), _p(dy_perm), _p(dx_perm),
-                                             None if g is None else ctypes.byref(g), _p(ws),
-                                             ws.numel() * ws.element_size(), _stream(stream)))
+    w = MoeWeights(weights_["gate"].data_ptr(), weights_["up"].data_ptr(), weights_["down"].data_ptr())
+    g = None if grads is None else MoeWeightGrads(grads["gate"].data_ptr(), grads["up"].data_ptr(), grads["down"].data_ptr())
+    _run(ws, stream, lambda st: load().moe_gated_ffn_backward(
+        shape, _ptr(x), _ptr(expert_offsets), _ptr(slot_token), w, _ptr(gate_pre), _ptr(up_pre), _ptr(dy_perm),
+        _ptr(dx_perm), g, ws.data_ptr(), ws.nbytes, st))
 
 
 def moe_combine_backward(shape, dy, y_perm, pair_slot, topk_w, dy_perm, dtopk_w, stream=None):
-    with _device_of(dtopk_w):
-        _check(load().moe_combine_backward(ctypes.byref(shape), _p(dy), _p(y_perm), _p(pair_slot), _p(topk_w),
-                                           _p(dy_perm), _p(dtopk_w), _stream(stream)))
+    _run(dtopk_w, stream, lambda st: load().moe_combine_backward(
+        shape, _ptr(dy), _ptr(y_perm), _ptr(pair_slot), _ptr(topk_w), _ptr(dy_perm), _ptr(dtopk_w), st))
 
 
 class AdamwTensors:
@@ -342,8 +348,7 @@ def moe_adamw(tensors: AdamwTensors, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, 
     """lr_dev, grad_scale (float32) and step_dev (int64): one-element device tensors read in place of lr, 1, step.
     seed: of the E4M3 state's random rounding."""
     c = MoeAdamwConfig(DTYPE[tensors.p_type], DTYPE[tensors.g_type], tensors.state, lr, beta1, beta2, eps, weight_decay,
-                       step, seed & 0xFFFFFFFF, _p(lr_dev), _p(step_dev), _p(grad_scale))
+                       step, seed & 0xFFFFFFFF, _ptr(lr_dev), _ptr(step_dev), _ptr(grad_scale))
     if not len(tensors.array):
         return
-    with _device_of(tensors.keep[0][0]):
-        _check(load().moe_adamw(ctypes.byref(c), tensors.array, len(tensors.array), _stream(stream)))
+    _run(tensors.keep[0][0], stream, lambda st: load().moe_adamw(c, tensors.array, len(tensors.array), st))
