@@ -12,7 +12,7 @@
 // they are rounded.
 //
 // Bound by memory: every array is read or written once. A workgroup takes 8192 consecutive elements
-// of one tensor, 8 a lane and pass, so 32 lanes hold one block of the 8-bit form and its maximum
+// of one tensor (2048 where that would leave CUs without work), 8 a lane and pass, so 32 lanes hold one block of the 8-bit form and its maximum
 // takes 5 lane exchanges. The tensor table travels in the kernel arguments: no copy, no table kept.
 #include "train.h"
 
@@ -22,8 +22,9 @@ namespace {
 
 constexpr int ATHR = 256;
 constexpr int AV = 8;                    // elements per lane and pass
-constexpr int APASS = 4;                 // passes per workgroup
-constexpr int ACHUNK = ATHR * AV * APASS;
+constexpr int ASTEP = ATHR * AV;         // elements of a workgroup and pass
+constexpr int APASS = 4;                 // most passes per workgroup
+constexpr int64_t SMALL = 8 << 20;       // elements in all below which a workgroup makes one pass only
 constexpr float E4M3_MAX = 448.0f;
 constexpr float MIN_TOP = 0x1p-100f;     // keeps 448 / top finite: smaller values become code 0
 
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(ATHR) adamw_kernel(const AdamArgs a) {
   const bool after = lane < a.count && block >= a.first[lane < a.count ? lane + 1 : 1];
   const int ti = __builtin_popcountll(__ballot(after));
   const AdamTensor& t = a.t[ti];
-  const int64_t n = t.n, base = (int64_t)(block - a.first[ti]) * ACHUNK + threadIdx.x * AV;
+  const int64_t n = t.n, base = (int64_t)(block - a.first[ti]) * (a.passes * ASTEP) + threadIdx.x * AV;
   PT* const p = (PT*)t.p;
   const GT* const g = (const GT*)t.g;
 
@@ -169,9 +170,8 @@ __global__ void __launch_bounds__(ATHR) adamw_kernel(const AdamArgs a) {
   const uint32_t key = Q8 ? dither_key(a.seed, (uint32_t)step) : 0u;
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
 
-#pragma unroll
-  for (int pass = 0; pass < APASS; ++pass) {
-    const int64_t at = base + (int64_t)pass * ATHR * AV;
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int64_t at = base + (int64_t)pass * ASTEP;
     // a half wave without elements leaves together, so every block's lanes stay for its maximum
     if ((at & ~(int64_t)255) >= n) return;
     float w[AV], gv[AV], m[AV], v[AV], r[AV];
@@ -226,7 +226,8 @@ __global__ void __launch_bounds__(ATHR) adamw_kernel(const AdamArgs a) {
 
 }  // namespace
 
-int adamw_chunk() { return ACHUNK; }
+int adamw_chunk(int64_t elements) { return elements < SMALL ? ASTEP : ASTEP * APASS; }
+int adamw_passes(int chunk) { return chunk / ASTEP; }
 
 hipError_t launch_adamw(int p_type, int g_type, bool master, bool q8, const AdamArgs& a, hipStream_t st) {
   const int grid = a.first[a.count];

@@ -35,7 +35,7 @@ TrainWs train_ws(const moe_shape& s) {
   w.h = 0;
   w.dgu = up(P * s.I * b);
   w.xg = w.dgu + up(P * s.I * 2 * b);
-  w.total = w.xg + (s.act == MOE_BF16 ? up(P * s.H * b) : 0) + WS_ALIGN;
+  w.total = w.xg + up(P * s.H * b) + WS_ALIGN;
   return w;
 }
 
@@ -152,7 +152,12 @@ moe_status moe_gated_ffn_backward(const moe_shape* shape, const void* x, const i
     a.dgate = grads->gate;
     a.dup = grads->up;
     a.ddown = grads->down;
-    e = product(TF_DW, shape->act, a, st);  // also without rows: the gradients are zero then
+    if (a.slot_token) {
+      e = launch_gather_rows(shape->act, a, st);
+      a.x = a.xg;
+      a.slot_token = nullptr;
+    }
+    if (e == hipSuccess) e = product(TF_DW, shape->act, a, st);  // also without rows: the gradients are zero then
   }
   return hip_status(e, "gated FFN gradient");
 }
@@ -226,7 +231,10 @@ moe_status moe_adamw(const moe_adamw_config* c, const moe_adamw_tensor* tensors,
   a.lr_dev = c->lr_dev;
   a.step_dev = c->step_dev;
   a.grad_scale = c->grad_scale;
-  const int chunk = adamw_chunk();
+  int64_t elements = 0;
+  for (int i = 0; i < count; ++i) elements += tensors[i].n;
+  const int chunk = adamw_chunk(elements);
+  a.passes = adamw_passes(chunk);
   hipError_t e = hipSuccess;
   long long groups = 0;
   auto flush = [&] {

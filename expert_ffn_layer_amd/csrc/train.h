@@ -12,7 +12,7 @@ enum TrainForm {
   TF_DOWN,     // y = h Wd
   TF_DH,       // dh = dy Wd^T; writes dg and du side by side ([row][2 I]) and h
   TF_DX,       // dx = dg Wg^T + du Wu^T
-  TF_DW        // dWg = x^T dg, dWu = x^T du, dWd = h^T dy, per expert
+  TF_DW        // dWg = x^T dg, dWu = x^T du, dWd = h^T dy, per expert; x by row (slot_token NULL)
 };
 
 struct TrainArgs {
@@ -24,7 +24,7 @@ struct TrainArgs {
   void *g, *u, *y;            // TF_GATE_UP / TF_DOWN outputs; g, u inputs of TF_DH
   const void* dy;
   void *dx, *dgate, *dup, *ddown;
-  void *h, *dgu, *xg;         // workspace: [P][I], [P][2 I] and, for bf16, [P][H]
+  void *h, *dgu, *xg;         // workspace: [P][I], [P][2 I] and [P][H]
 };
 
 // Largest number of row tiles of bm rows that E groups of P rows in all can take.
@@ -33,6 +33,8 @@ inline long long max_row_tiles(int P, int E, int bm) {
 }
 
 hipError_t launch_train_f32(TrainForm form, const TrainArgs& a, hipStream_t st);
+// xg = rows of x in the grouped order
+hipError_t launch_gather_rows(int act, const TrainArgs& a, hipStream_t st);
 hipError_t launch_train_bf16(TrainForm form, const TrainArgs& a, hipStream_t st);
 
 hipError_t launch_combine_backward(int act, const void* dy, const void* y_perm, const int32_t* pair_slot, const float* w,
@@ -51,7 +53,7 @@ struct AdamTensor {
 struct AdamArgs {
   AdamTensor t[ADAM_MAX];
   int first[ADAM_MAX + 1];  // first workgroup of each tensor
-  int count;
+  int count, passes;
   float lr, beta1, beta2, one_minus_beta1, one_minus_beta2, eps, wd;
   float bc1, inv_root_bc2;      // 1 - beta1^t and 1 / sqrt(1 - beta2^t), without step_dev
   float log_beta1, log_beta2;
@@ -62,7 +64,8 @@ struct AdamArgs {
   const float* grad_scale;
 };
 hipError_t launch_adamw(int p_type, int g_type, bool master, bool q8, const AdamArgs& a, hipStream_t st);
-int adamw_chunk();  // elements of one workgroup
+int adamw_chunk(int64_t elements);  // elements of one workgroup, for so many in all
+int adamw_passes(int chunk);
 
 #ifdef __HIPCC__
 // Place of row tile `tile` (bm rows each, groups one after the other): its group and rows. Every

@@ -560,17 +560,6 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) train_bf16_kernel(co
   }
 }
 
-// Rows of x in the grouped order, zeros for tokens outside x: TF_DW then reads its row operand by row
-__global__ void __launch_bounds__(THR) gather_kernel(const TrainArgs a) {
-  const int cpr = a.H / 8;
-  const long long id = (long long)blockIdx.x * THR + threadIdx.x;
-  if (id >= (long long)a.P * cpr) return;
-  const int r = (int)(id / cpr), c = (int)(id - (long long)r * cpr), s = a.slot_token[r];
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if ((unsigned)s < (unsigned)a.xrows) v = *((const u32x4*)a.x + (size_t)s * cpr + c);
-  *((u32x4*)a.xg + id) = v;
-}
-
 template <int FORM, int WR, int WC, int MT, int NT, int D>
 hipError_t launch(const TrainArgs& a, hipStream_t st) {
   constexpr int BM = WR * MT * 32, BN = WC * NT * 32;
@@ -637,17 +626,7 @@ hipError_t launch_train_bf16(TrainForm form, const TrainArgs& a, hipStream_t st)
     case TF_DOWN: return choose<TF_DOWN>(a, st);
     case TF_DH: return choose<TF_DH>(a, st);
     case TF_DX: return choose<TF_DX>(a, st);
-    case TF_DW: {
-      TrainArgs b = a;
-      if (a.slot_token && a.P) {
-        gather_kernel<<<(unsigned)(((long long)a.P * (a.H / 8) + THR - 1) / THR), THR, 0, st>>>(a);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        b.x = a.xg;
-        b.slot_token = nullptr;
-      }
-      return choose<TF_DW>(b, st);
-    }
+    case TF_DW: return choose<TF_DW>(a, st);  // x without slot_token here: its rows are gathered before
   }
   return hipErrorInvalidValue;
 }
