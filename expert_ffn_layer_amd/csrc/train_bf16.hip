@@ -25,6 +25,8 @@ namespace {
 constexpr int BK = 64;     // reduction elements per step: 128 bytes of a row, a whole cache line
 constexpr int THR = 256;   // 4 waves
 constexpr int NXCD = 8;
+constexpr int NON_TEMPORAL = 2;                // cache policy of a load: nt
+constexpr long long CACHE_BYTES = 256LL << 20;  // of the last-level cache
 
 typedef __attribute__((address_space(3))) uint8_t lds_byte;
 typedef __attribute__((address_space(3))) void lds_void;
@@ -136,7 +138,8 @@ struct Share {
   static constexpr int count(int ph) { return from(ph, 1) - from(ph); }
 };
 
-template <int FORM, int WR, int WC, int MT, int NT, int D>
+// STREAM: the weights are read once and come from memory, so they pass the caches without staying there
+template <int FORM, int WR, int WC, int MT, int NT, int D, bool STREAM>
 __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) train_bf16_kernel(const TrainArgs a) {
   constexpr bool P_KC = FORM != TF_DW, Q_KC = FORM == TF_DH || FORM == TF_DX;
   constexpr int BM = WR * MT * 32, BN = WC * NT * 32;
@@ -270,9 +273,10 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) train_bf16_kernel(co
   // values out of the sums, and where the results are not stored they save the power of a row's products
   // (1.5 to 2% of dh and dx of the ragged V3 slice).
   const int half_steps = (int)I / BK;
-  auto load_one = [&](const uint8_t*& src, lds_byte* dst, int left, size_t adv) __attribute__((always_inline)) {
+  auto load_one = [&](const uint8_t*& src, lds_byte* dst, int left, size_t adv, bool weights) __attribute__((always_inline)) {
     const uint8_t* const from = left >= 0 ? src : (const uint8_t*)&zero_chunk;
-    __builtin_amdgcn_global_load_lds((const void*)from, (lds_void*)dst, 16, 0, 0);
+    if (STREAM && weights) __builtin_amdgcn_global_load_lds((const void*)from, (lds_void*)dst, 16, 0, NON_TEMPORAL);
+    else __builtin_amdgcn_global_load_lds((const void*)from, (lds_void*)dst, 16, 0, 0);
     src += adv;
     asm volatile("" : "+v"(src));  // one running pointer a load, not one per load and slot
   };
@@ -281,7 +285,7 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) train_bf16_kernel(co
     const int un = TP::unit(q, wave);
     lds_byte* const part = P_PART(decltype(slot)::value, q >= UP / 2);
     load_one(psrc[q], part + (P_HV ? un % (TP::UNITS / 2) : un) * 1024,
-             (P_KC ? mend - m0 : K - step * BK) - 1 - TP::row(un, lane), adv);
+             (P_KC ? mend - m0 : K - step * BK) - 1 - TP::row(un, lane), adv, false);
   };
   auto load_q = [&](int q, int step, auto slot) __attribute__((always_inline)) {
     size_t adv = FORM == TF_DW || step + 1 < nsteps ? qstride : 0;
@@ -289,7 +293,7 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) train_bf16_kernel(co
     const int un = TQ::unit(q, wave);
     lds_byte* const part = Q_PART(decltype(slot)::value, q >= UQ / 2);
     load_one(qsrc[q], part + (Q_HV ? un % (TQ::UNITS / 2) : un) * 1024,
-             FORM == TF_DW ? K - step * BK - 1 - TQ::row(un, lane) : 0, adv);
+             FORM == TF_DW ? K - step * BK - 1 - TQ::row(un, lane) : 0, adv, true);
   };
 
   f32x16 acc[NT][MT];
@@ -560,7 +564,7 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) train_bf16_kernel(co
   }
 }
 
-template <int FORM, int WR, int WC, int MT, int NT, int D>
+template <int FORM, int WR, int WC, int MT, int NT, int D, bool STREAM = false>
 hipError_t launch(const TrainArgs& a, hipStream_t st) {
   constexpr int BM = WR * MT * 32, BN = WC * NT * 32;
   long long n;
@@ -575,7 +579,7 @@ hipError_t launch(const TrainArgs& a, hipStream_t st) {
   }
   if (n == 0) return hipSuccess;
   const unsigned grid = (unsigned)(n * NXCD);
-  train_bf16_kernel<FORM, WR, WC, MT, NT, D><<<grid, THR, 0, st>>>(a);
+  train_bf16_kernel<FORM, WR, WC, MT, NT, D, STREAM><<<grid, THR, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -588,7 +592,7 @@ hipError_t launch(const TrainArgs& a, hipStream_t st) {
 // Large problems are bound by the matrix cores and take the tile that reads LDS least; few or thin groups
 // leave CUs empty or rows unused, and there the latency of a step counts: more and smaller tiles, more stages in
 // flight. Measured on gate/up, best of the others in brackets: 32768 rows in 32 groups 1.78 ms (2.49); one
-// group of 1027 rows, H 4096, I 1536: 43 us (79 as 256 x 256); 440 rows in 16 groups 84 us (99).
+// group of 1027 rows, H 4096, I 1536: 43 us (79 as 256 x 256); 440 rows in 16 groups 76 us (88).
 template <int FORM>
 hipError_t choose(const TrainArgs& a, hipStream_t st) {
   auto rounds = [](double tiles, int per) { return (double)(long long)((tiles + per - 1) / per); };
@@ -609,11 +613,15 @@ hipError_t choose(const TrainArgs& a, hipStream_t st) {
     const double b = tiles(128, 128);
     const double t[4] = {rounds(tiles(256, 256), 256) * 1.2, rounds(b, 512) * (b > 256 ? 1.1 : 0.75),
                          rounds(tiles(64, 256), 256) * 0.67, rounds(tiles(64, 128), 256) * 0.43};
+    // The layer's weights go through once, no second row tile reads them and the last-level cache could not hold
+    // them from before: 440 rows, H 4096, I 1536, 16 groups, gate/up 89 us with the default policy, 78 so; 100
+    // rows in 8 groups, whose 200 MB were in the cache, 41 and 66.
+    const bool stream = a.P <= 64LL * a.E && 6LL * a.E * a.H * a.I > CACHE_BYTES;
     switch (std::min_element(t, t + 4) - t) {
       case 0: return launch<FORM, 2, 2, 4, 4, 2>(a, st);
       case 1: return launch<FORM, 2, 2, 2, 2, 2>(a, st);
-      case 2: return launch<FORM, 1, 4, 2, 2, 4>(a, st);
-      default: return launch<FORM, 2, 2, 1, 2, 4>(a, st);
+      case 2: return stream ? launch<FORM, 1, 4, 2, 2, 4, true>(a, st) : launch<FORM, 1, 4, 2, 2, 4>(a, st);
+      default: return stream ? launch<FORM, 2, 2, 1, 2, 4, true>(a, st) : launch<FORM, 2, 2, 1, 2, 4>(a, st);
     }
   }
 }
