@@ -138,6 +138,29 @@ def test_wide_sizes(act):
     c.verify(c.backward(), "backward", range(0, 200, 7))
 
 
+# Rows per group, H and I that take every tile shape of every product in bf16 (256 x 256, 128 x 128, 64 x 256 and
+# 64 x 128, the last two also with the weights streamed) and both of fp32, with H and I odd multiples of 128 and
+# groups that end inside and at the end of a tile
+TILES = {
+    "thin": ([2, 5, 2, 6, 8, 4, 4, 2, 0, 3, 9, 1], 1664, 2688),
+    "thin-many": ([1, 3, 19, 9, 16, 4, 2, 66, 1, 3, 20, 13, 4, 0, 2, 1, 10, 2, 0, 5], 2176, 2176),
+    "mixed": ([64, 149, 0, 1200, 589, 256, 405, 1200, 736, 129, 173, 412], 384, 384),
+    "many-rows": ([1125, 452, 204, 0, 831, 398, 53, 75, 2400, 512, 257, 87, 2400, 476, 128, 690, 1, 255, 968, 368], 384, 384),
+    "wide": ([978, 408, 0, 598, 1281, 291, 242, 298, 616], 1664, 384),
+    "deep": ([86, 282, 96, 18, 33, 300, 300, 42, 131, 40, 58, 173, 1, 14, 0, 274, 15, 51, 129, 222], 384, 2688),
+}
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("name", TILES)
+def test_tile_shapes(name, act):
+    counts, H, I = TILES[name]
+    b = Block(counts, H, I, act, seed=21)
+    say("tiles", name, act, b.T, b.k, H, I)
+    say("forward worst", b.verify(b.forward(), "forward"))
+    say("backward worst", b.verify(b.backward(), "backward"))
+
+
 @pytest.mark.parametrize("act", ["f32", "bf16"])
 def test_rows_in_order_and_partial_outputs(act):
     """slot_token NULL reads x by row; pre-activations, dx and the weight gradients may be left out."""
