@@ -78,21 +78,29 @@ hipError_t product(TrainForm form, int act, const TrainArgs& a, hipStream_t st) 
   return act == MOE_F32 ? launch_train_f32(form, a, st) : launch_train_bf16(form, a, st);
 }
 
-// Two of the updated tensors share memory: both workgroups would read and write it.
-moe_status check_apart(const moe_adamw_tensor* t, int count, size_t size) {
+// No two of the updated arrays share memory: two workgroups would read and write it.
+moe_status check_apart(const moe_adamw_tensor* t, int count, size_t p_bytes, size_t state_bytes) {
   struct Range {
     uintptr_t at, end;
   };
-  Range* r = new (std::nothrow) Range[count];
+  Range* r = new (std::nothrow) Range[4 * (size_t)count];
   if (!r) return fail(MOE_ERR_INVALID_ARG, "no host memory to check %d tensors", count);
-  int n = 0;
-  for (int i = 0; i < count; ++i)
-    if (t[i].n) r[n++] = Range{(uintptr_t)t[i].p, (uintptr_t)t[i].p + (size_t)t[i].n * size};
+  size_t n = 0;
+  auto add = [&](const void* p, size_t bytes) {
+    if (p) r[n++] = Range{(uintptr_t)p, (uintptr_t)p + bytes};
+  };
+  for (int i = 0; i < count; ++i) {
+    if (!t[i].n) continue;
+    add(t[i].p, (size_t)t[i].n * p_bytes);
+    add(t[i].m, (size_t)t[i].n * state_bytes);
+    add(t[i].v, (size_t)t[i].n * state_bytes);
+    add(t[i].master, (size_t)t[i].n * 4);
+  }
   std::sort(r, r + n, [](const Range& x, const Range& y) { return x.at < y.at; });
   bool apart = true;
-  for (int i = 1; i < n; ++i) apart = apart && r[i - 1].end <= r[i].at;
+  for (size_t i = 1; i < n; ++i) apart = apart && r[i - 1].end <= r[i].at;
   delete[] r;
-  return apart ? MOE_OK : fail(MOE_ERR_INVALID_ARG, "two parameter tensors overlap");
+  return apart ? MOE_OK : fail(MOE_ERR_INVALID_ARG, "parameters, states or master copies overlap");
 }
 
 }  // namespace
@@ -209,7 +217,7 @@ moe_status moe_adamw(const moe_adamw_config* c, const moe_adamw_tensor* tensors,
   }
   if (master < 0) return MOE_OK;  // only empty tensors
   if (master && c->p_type == MOE_F32) return fail(MOE_ERR_INVALID_ARG, "F32 parameters take no master copy");
-  const moe_status s = check_apart(tensors, count, c->p_type == MOE_F32 ? 4 : 2);
+  const moe_status s = check_apart(tensors, count, c->p_type == MOE_F32 ? 4 : 2, q8 ? 1 : 4);
   if (s != MOE_OK) return s;
 
   AdamArgs a{};

@@ -57,13 +57,26 @@ class PackedLayer:
         return y
 
 
+def _need(name: str, t: torch.Tensor, dtype, *shapes):
+    if tuple(t.shape) not in shapes or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError("%s: a contiguous %s tensor of %s is needed" % (name, dtype, " or ".join(map(str, shapes))))
+
+
+def _result(like: torch.Tensor, stream):
+    t = torch.empty_like(like)
+    if stream is not None:
+        t.record_stream(stream)  # its memory is not handed on before this stream's work on it has ended
+    return t
+
+
 class TrainableLayer:
     """One layer's experts in training: forward, backward and AdamW step over row-major weights of the
     activations' type (gate, up [E, H, I], down [E, I, H]; the shared expert's without the first axis or
     with one of 1). The router is read only; its scores' gradient follows from backward's routing-weight
     gradient. Allocation and marshalling only, like PackedLayer.
 
-    forward keeps what backward reads, for the last batch alone. state: "f32", or "e4m3" for 8-bit
+    forward keeps what backward reads (x itself, not a copy), for the last batch alone. Calls and set_tokens on one
+    stream follow each other; from another stream they have to wait for the former ones. state: "f32", or "e4m3" for 8-bit
     optimizer states; master: fp32 master copies of bf16 weights."""
 
     NAMES = ("gate", "up", "down")
@@ -71,12 +84,16 @@ class TrainableLayer:
     def __init__(self, spec, Wr: torch.Tensor, routed: dict, shared: dict | None = None, T: int | None = None,
                  state: str = "f32", master: bool = False):
         self.H, self.I, self.E, self.k, self.act = spec.H, spec.I, spec.E, spec.k, spec.act
-        self.Wr, _ = pack(spec.act, Wr.reshape(1, spec.H, spec.E), None, spec.H, spec.E)
         self.dtype = torch.float32 if spec.act == "f32" else torch.bfloat16
+        for d, lead in ((routed, [(spec.E,)]), (shared, [(), (1,)])):
+            for n in self.NAMES if d is not None else ():
+                size = (spec.I, spec.H) if n == "down" else (spec.H, spec.I)
+                _need(n, d[n], self.dtype, *[a + size for a in lead])
         self.weights = [{n: routed[n] for n in self.NAMES}]
         if shared is not None:
             self.weights.append({n: shared[n] for n in self.NAMES})
         self.grads = [{n: torch.zeros_like(t) for n, t in w.items()} for w in self.weights]
+        self.Wr, _ = pack(spec.act, Wr.reshape(1, spec.H, spec.E), None, spec.H, spec.E)
         p = [w[n] for w in self.weights for n in self.NAMES]
         g = [d[n] for d in self.grads for n in self.NAMES]
         if state == "e4m3":
@@ -115,7 +132,8 @@ class TrainableLayer:
 
     def forward(self, x, bias=None, stream=None):
         """y [T, H]; routing as moe_route, kept in idx and w."""
-        y = torch.empty_like(x)
+        _need("x", x, self.dtype, (self.T, self.H))
+        y = _result(x, stream)
         N.moe_route_permute(self.shapes[0], x, self.Wr, bias, self.idx, self.w, self.off, self.slot_token,
                             self.pair_slot, self.ws, stream)
         groups = [(self.off, self.slot_token), (None, None)]
@@ -129,7 +147,8 @@ class TrainableLayer:
         """(dx through the experts [T, H], gradient of the routing weights [T, k]); fills grads."""
         if self.x is None:
             raise RuntimeError("backward needs a forward pass on this batch size")
-        dx = torch.empty_like(dy)
+        _need("dy", dy, self.dtype, (self.T, self.H))
+        dx = _result(dy, stream)
         N.moe_combine_backward(self.shapes[0], dy, self.y[0], self.pair_slot, self.w, self.dy_perm, self.dw, stream)
         groups = [(self.off, self.slot_token, self.dy_perm), (None, None, dy)]
         for shape, (off, slot, d), w, pre, out, grads in zip(self.shapes, groups, self.weights, self.pre, self.dx, self.grads):

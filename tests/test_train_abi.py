@@ -4,7 +4,7 @@ import ctypes
 import pytest
 import torch
 
-from expert_ffn_layer_amd import native as N
+from expert_ffn_layer_amd import layer, native as N
 
 P = ctypes.c_void_p
 OK, M8, M2 = P(0x10000), P(0x10008), P(0x10002)  # aligned, 8 off a 16-byte boundary, 2 off; never read
@@ -113,6 +113,9 @@ def test_adamw_refuses():
     assert adamw(config(), tensor(), tensor()) == 1  # the same tensor twice
     assert "overlap" in N.load().moe_last_error().decode()
     assert adamw(config(), tensor(), tensor(p=0x10040)) == 1  # inside the first one's 128 bytes
+    assert adamw(config(), tensor(m=0x40000)) == 1  # m is v
+    assert adamw(config(), tensor(), tensor(p=0x50000, m=0x60000, v=0x300C0)) == 1  # v inside the first one's m
+    assert adamw(config(), tensor(master=0x40080)) == 1  # a master copy inside v
     assert adamw(config(), tensor(), count=-1) == 1
     assert adamw(config(), count=0) == 0 and adamw(config(), tensor(n=0, p=None)) == 0
     assert N.load().moe_adamw(None, None, 0, None) == 1 and N.load().moe_adamw(ctypes.byref(config()), None, 1, None) == 1
@@ -126,3 +129,29 @@ def test_adamw_table_refuses_mismatched_lists():
         with pytest.raises(ValueError):
             N.adamw_tensors(*args)
     assert len(N.adamw_tensors([], [], [], []).array) == 0
+
+
+def test_binding_refuses_tensors_off_the_gpu():
+    """A host tensor's address never reaches a kernel."""
+    b, i = torch.zeros(8, 256, dtype=torch.bfloat16), torch.zeros(16, dtype=torch.int32)
+    w = {n: b for n in ("gate", "up", "down")}
+    with pytest.raises(ValueError):
+        N.moe_gated_ffn(shape(), b, i, i, w, b, b, b, torch.zeros(1 << 20, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        N.moe_gated_ffn_backward(shape(), b, i, i, w, b, b, b, b, w, torch.zeros(1 << 20, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        N.moe_combine_backward(shape(), b, b, i, b, b, b)
+    f = torch.zeros(8)
+    table = N.AdamwTensors((N.MoeAdamwTensor * 1)(tensor()), [[f]], "f32", "f32", 0)
+    for kw in ({}, dict(lr_dev=f.double()), dict(step_dev=f), dict(grad_scale=f[:0])):
+        with pytest.raises(ValueError):
+            N.moe_adamw(table, **kw)
+
+
+def test_layer_refuses_other_sizes_types_and_strides():
+    t = torch.zeros(4, 8)
+    layer._need("x", t, torch.float32, (4, 8))
+    layer._need("x", t, torch.float32, (8, 4), (4, 8))
+    for bad in (t[:3], t.double(), torch.zeros(8, 4).T, t[None]):
+        with pytest.raises(ValueError):
+            layer._need("x", bad, torch.float32, (4, 8))

@@ -652,3 +652,70 @@ def test_training_steps_of_a_layer(spec, state, master):
         lay.backward(dy)
     x = normal(gen, (T // 2 + 1, H), dtype)
     assert torch.isfinite(lay.forward(x).float()).all()
+
+
+@pytest.mark.parametrize("spec", LAYERS, ids=[s.name for s in LAYERS])
+def test_captured_training_step_of_a_layer(spec):
+    """Routing, forward, backward and AdamW in one graph, replayed between eager steps of a second layer with the
+    same weights: the same bits in every weight after every step."""
+    say("captured layer", spec.name)
+    dtype = DT[spec.act]
+    H, I, E, T = spec.H, spec.I, spec.E, spec.T
+
+    def build():
+        gen = gen_of(spec.seed)
+
+        def mats(*lead):
+            return {"gate": normal(gen, (*lead, H, I), dtype, H ** -0.5), "up": normal(gen, (*lead, H, I), dtype, H ** -0.5),
+                    "down": normal(gen, (*lead, I, H), dtype, I ** -0.5)}
+        Wr = normal(gen, (H, E), dtype, H ** -0.5)
+        return TrainableLayer(spec, Wr, mats(E), mats() if spec.shared else None, state="e4m3")
+    a, b = build(), build()
+    gen = gen_of(3)
+    x, dy = normal(gen, (T, H), dtype), normal(gen, (T, H), dtype)
+    step = torch.ones(1, dtype=torch.int64, device=DEV)
+
+    def run(lay):
+        y = lay.forward(x)
+        dx, _ = lay.backward(dy)
+        lay.step(1e-3, weight_decay=0.1, step_dev=step)
+        return y, dx
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            out = run(a)
+    for t in range(1, 5):
+        step.fill_(t)
+        x.copy_(normal(gen, (T, H), dtype))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = run(b)
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(out, want)), t
+        assert all(torch.equal(p, q) for p, q in zip(a.optimizer.keep[0], b.optimizer.keep[0])), t
+
+
+def test_layer_on_another_stream_and_without_tokens():
+    spec = LAYERS[1]
+    gen, dtype = gen_of(1), DT[spec.act]
+    H, I, E = spec.H, spec.I, spec.E
+    routed = {"gate": normal(gen, (E, H, I), dtype, H ** -0.5), "up": normal(gen, (E, H, I), dtype, H ** -0.5),
+              "down": normal(gen, (E, I, H), dtype, I ** -0.5)}
+    with pytest.raises(ValueError):
+        TrainableLayer(spec, normal(gen, (H, E), dtype), routed | {"up": routed["down"]})
+    lay = TrainableLayer(spec, normal(gen, (H, E), dtype, H ** -0.5), routed)
+    x, dy = normal(gen, (spec.T, H), dtype), normal(gen, (spec.T, H), dtype)
+    with pytest.raises(ValueError):
+        lay.forward(x[:-1])
+    want = lay.forward(x), *lay.backward(dy)
+    want = [t.clone() for t in want]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = lay.forward(x, stream=side), *lay.backward(dy, stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    lay.set_tokens(0)
+    assert lay.forward(x[:0]).shape == (0, H)
+    dx, dw = lay.backward(dy[:0])
+    assert dx.shape == (0, H) and all((t == 0).all() for t in lay.grads[0].values())
