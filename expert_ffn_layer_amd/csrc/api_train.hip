@@ -35,7 +35,7 @@ TrainWs train_ws(const moe_shape& s) {
   w.h = 0;
   w.dgu = up(P * s.I * b);
   w.xg = w.dgu + up(P * s.I * 2 * b);
-  w.total = w.xg + up(P * s.H * b) + WS_ALIGN;
+  w.total = w.xg + (s.act == MOE_BF16 ? up(P * s.H * b) : 0) + WS_ALIGN;
   return w;
 }
 
@@ -153,19 +153,24 @@ moe_status moe_gated_ffn_backward(const moe_shape* shape, const void* x, const i
   a.dy = dy_perm;
   a.dx = dx_perm;
   const hipStream_t st = (hipStream_t)stream;
-  hipError_t e = hipSuccess;
-  if (a.P) e = product(TF_DH, shape->act, a, st);
-  if (e == hipSuccess && a.P && dx_perm) e = product(TF_DX, shape->act, a, st);
-  if (e == hipSuccess && grads) {
+  if (grads) {
     a.dgate = grads->gate;
     a.dup = grads->up;
     a.ddown = grads->down;
-    if (a.slot_token) {
-      e = launch_gather_rows(shape->act, a, st);
+  }
+  hipError_t e = hipSuccess;
+  if (a.P) e = product(TF_DH, shape->act, a, st);
+  const bool dx = a.P && dx_perm;
+  if (e == hipSuccess && dx && grads && shape->act == MOE_F32) {
+    e = launch_gradients_f32(a, st);
+  } else {
+    if (e == hipSuccess && dx) e = product(TF_DX, shape->act, a, st);
+    if (e == hipSuccess && grads && a.slot_token && shape->act == MOE_BF16) {
+      e = launch_gather_rows(a, st);
       a.x = a.xg;
       a.slot_token = nullptr;
     }
-    if (e == hipSuccess) e = product(TF_DW, shape->act, a, st);  // also without rows: the gradients are zero then
+    if (e == hipSuccess && grads) e = product(TF_DW, shape->act, a, st);  // also without rows: the gradients are zero then
   }
   return hip_status(e, "gated FFN gradient");
 }

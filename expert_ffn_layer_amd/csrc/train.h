@@ -12,7 +12,7 @@ enum TrainForm {
   TF_DOWN,     // y = h Wd
   TF_DH,       // dh = dy Wd^T; writes dg and du side by side ([row][2 I]) and h
   TF_DX,       // dx = dg Wg^T + du Wu^T
-  TF_DW        // dWg = x^T dg, dWu = x^T du, dWd = h^T dy, per expert; x by row (slot_token NULL)
+  TF_DW        // dWg = x^T dg, dWu = x^T du, dWd = h^T dy, per expert; in bf16 x by row (slot_token NULL)
 };
 
 struct TrainArgs {
@@ -24,7 +24,7 @@ struct TrainArgs {
   void *g, *u, *y;            // TF_GATE_UP / TF_DOWN outputs; g, u inputs of TF_DH
   const void* dy;
   void *dx, *dgate, *dup, *ddown;
-  void *h, *dgu, *xg;         // workspace: [P][I], [P][2 I] and [P][H]
+  void *h, *dgu, *xg;         // workspace: [P][I], [P][2 I] and, for bf16, [P][H]
 };
 
 // Largest number of row tiles of bm rows that E groups of P rows in all can take.
@@ -33,8 +33,8 @@ inline long long max_row_tiles(int P, int E, int bm) {
 }
 
 hipError_t launch_train_f32(TrainForm form, const TrainArgs& a, hipStream_t st);
-// xg = rows of x in the grouped order
-hipError_t launch_gather_rows(int act, const TrainArgs& a, hipStream_t st);
+hipError_t launch_gradients_f32(const TrainArgs& a, hipStream_t st);  // TF_DX and TF_DW
+hipError_t launch_gather_rows(const TrainArgs& a, hipStream_t st);     // xg = rows of x in the grouped order, bf16
 hipError_t launch_train_bf16(TrainForm form, const TrainArgs& a, hipStream_t st);
 
 hipError_t launch_combine_backward(int act, const void* dy, const void* y_perm, const int32_t* pair_slot, const float* w,

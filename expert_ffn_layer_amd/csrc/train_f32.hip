@@ -11,7 +11,8 @@
 //
 // Bound by the matrix instructions where there are tiles enough (8192 rows, H 2048, I 4096, 8 groups: 112,
 // 118, 112, 105 and 108 TFLOP/s for the five forms in order, the card's fp32 library product 140), by a chain of
-// load, LDS and product per step below (16 tokens, H 256, I 128: 7.4 us and 5.1 us for the forward's two).
+// load, LDS and product per step below (16 tokens, H 256, I 128: 7.4 us and 5.1 us for the forward's two). The rows
+// of x that the weight gradients reduce over are found by tokens fetched as many steps before them again.
 #include "train.h"
 
 namespace moe {
@@ -31,14 +32,19 @@ __device__ const uint4 zero_chunk = {0u, 0u, 0u, 0u};
 __device__ __forceinline__ fvec4 load4(const float* p) { return *(const __attribute__((address_space(1))) fvec4*)p; }
 __device__ __forceinline__ void store4(float* p, fvec4 v) { *(fvec4*)p = v; }
 
+constexpr int LDS_FLOATS = 2 * 64 * LDK;  // both operands of the largest tile
+
+// One tile: x is its row tile (TF_DW: tile of the matrix), y its tile of columns (expert), z of TF_DW the matrix
 template <int FORM, int TM>
-__global__ void __launch_bounds__(TTHR) train_f32_kernel(const TrainArgs a) {
+__device__ __forceinline__ void tile(const TrainArgs& a, int bx, int by, int bz, float* lds) {
   constexpr int RT = TM / 32;                                // MFMA tiles of rows a wave has
   constexpr int LDP = TM + 4;                                // floats per row of a [k][index] row operand
   constexpr bool P_KC = FORM != TF_DW;                       // row operand contiguous along k
   constexpr bool Q_KC = FORM == TF_DH || FORM == TF_DX;      // column operand contiguous along k
-  __shared__ __align__(16) float lp[P_KC ? TM * LDK : TK * LDP];
-  __shared__ __align__(16) float lq[Q_KC ? TN * LDK : TK * LDM];
+  constexpr int PF = P_KC ? TM * LDK : TK * LDP, QF = Q_KC ? TN * LDK : TK * LDM;
+  static_assert(PF + QF <= LDS_FLOATS && PF % 4 == 0, "operands fit the workgroup's LDS");
+  float* const lp = lds;
+  float* const lq = lds + PF;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wr = wave >> 1, wc = wave & 1, l16 = lane & 15, g = lane >> 4;
   const size_t H = a.H, I = a.I, HI = H * I;
@@ -47,23 +53,23 @@ __global__ void __launch_bounds__(TTHR) train_f32_kernel(const TrainArgs a) {
   int e, m0, mend, n0, K, beg = 0;
   int mat = 0;  // TF_DW: 0 gate, 1 up, 2 down
   if constexpr (FORM == TF_DW) {
-    const int tm = (int)((blockIdx.z == 2 ? I : H) / TM), tn = (int)((blockIdx.z == 2 ? H : I) / TN);
-    mat = blockIdx.z;
-    e = blockIdx.y;
-    if ((int)blockIdx.x >= tm * tn) return;
-    m0 = (int)(blockIdx.x / tn) * TM;
-    n0 = (int)(blockIdx.x % tn) * TN;
+    const int tm = (int)((bz == 2 ? I : H) / TM), tn = (int)((bz == 2 ? H : I) / TN);
+    mat = bz;
+    e = by;
+    if (bx >= tm * tn) return;
+    m0 = bx / tn * TM;
+    n0 = bx % tn * TN;
     mend = mat == 2 ? a.I : a.H;
     int end;
     group_rows(a.off, e, a.P, beg, end);
     K = end - beg;
   } else {
     RowTile t;
-    if (!find_row_tile(a.off, a.E, a.P, TM, blockIdx.x, t)) return;
+    if (!find_row_tile(a.off, a.E, a.P, TM, bx, t)) return;
     e = t.e;
     m0 = t.row0;
     mend = t.end;
-    n0 = blockIdx.y * (FORM == TF_GATE_UP ? TN / 2 : TN);
+    n0 = by * (FORM == TF_GATE_UP ? TN / 2 : TN);
     K = FORM == TF_GATE_UP || FORM == TF_DH ? a.H : FORM == TF_DOWN ? a.I : 2 * a.I;
   }
 
@@ -79,10 +85,12 @@ __global__ void __launch_bounds__(TTHR) train_f32_kernel(const TrainArgs a) {
       if ((unsigned)tok[u] >= (unsigned)a.xrows) tok[u] = -1;
     }
   }
-  auto at_p = [&](int i, int k) -> const float* {
+  auto at_p = [&](int i, int k, int token) -> const float* {
     if constexpr (FORM == TF_DW) {
       if (k >= K) return zeros;
-      return mat == 2 ? (const float*)a.h + (beg + k) * I + m0 + i : (const float*)a.x + (beg + k) * H + m0 + i;
+      if (mat == 2) return (const float*)a.h + (beg + k) * I + m0 + i;
+      const int r = a.slot_token ? token : beg + k;
+      return (unsigned)r < (unsigned)a.xrows ? (const float*)a.x + r * H + m0 + i : zeros;
     } else {
       const int r = m0 + i;
       if (r >= mend) return zeros;
@@ -127,6 +135,18 @@ __global__ void __launch_bounds__(TTHR) train_f32_kernel(const TrainArgs a) {
   // AHEAD steps' chunks wait in registers: about 1.7 us of products, more than a load takes
   constexpr int AHEAD = 4;
   fvec4 rp[AHEAD][RT], rq[AHEAD][2];
+  // TF_DW: the token of reduction element k, fetched AHEAD steps before its row of x
+  int tokens[AHEAD][2] = {};
+  const int32_t* const token_at = FORM == TF_DW && a.slot_token && mat < 2 && K > 0 ? a.slot_token + beg : (const int32_t*)zeros;
+  const int token_last = FORM == TF_DW && a.slot_token && mat < 2 ? K - 1 : 0;
+  auto fetch_tokens = [&](int k0, int set) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < RT && FORM == TF_DW; ++u) {
+      int i, k;
+      chunk(P_KC, TM, u, i, k);
+      tokens[set][u] = *(const __attribute__((address_space(1))) int32_t*)(token_at + min(k0 + k, token_last));
+    }
+  };
   auto fetch = [&](int k0, int set) __attribute__((always_inline)) {
     if (FORM != TF_DW) k0 = min(k0, K - TK);  // past the end the last step again, which nothing uses
 #pragma unroll
@@ -134,11 +154,12 @@ __global__ void __launch_bounds__(TTHR) train_f32_kernel(const TrainArgs a) {
       int i, k;
       if (u < RT) {
         chunk(P_KC, TM, u, i, k);
-        rp[set][u] = load4(at_p(i, k0 + k));
+        rp[set][u] = load4(at_p(i, k0 + k, tokens[set][u]));
       }
       chunk(Q_KC, TN, u, i, k);
       rq[set][u] = load4(at_q(i, k0 + k));
     }
+    fetch_tokens(k0 + AHEAD * TK, set);
   };
 
   f32x4 acc[2][RT];
@@ -197,6 +218,8 @@ __global__ void __launch_bounds__(TTHR) train_f32_kernel(const TrainArgs a) {
   // rounds of AHEAD steps: H and I are multiples of 128, the rows of TF_DW end anywhere and go on in zeros
   if (K > 0) {
 #pragma unroll
+    for (int u = 0; u < AHEAD; ++u) fetch_tokens(u * TK, u);
+#pragma unroll
     for (int u = 0; u < AHEAD; ++u) fetch(u * TK, u);
   }
   for (int k0 = 0; k0 < K; k0 += AHEAD * TK) {
@@ -251,38 +274,75 @@ __global__ void __launch_bounds__(TTHR) train_f32_kernel(const TrainArgs a) {
 }
 
 template <int FORM, int TM>
-void launch(const TrainArgs& a, long long columns, hipStream_t st) {
-  train_f32_kernel<FORM, TM><<<dim3((unsigned)max_row_tiles(a.P, a.E, TM), (unsigned)columns), TTHR, 0, st>>>(a);
+__global__ void __launch_bounds__(TTHR) train_f32_kernel(const TrainArgs a) {
+  __shared__ __align__(16) float lds[LDS_FLOATS];
+  tile<FORM, TM>(a, blockIdx.x, blockIdx.y, blockIdx.z, lds);
+}
+
+// dx and the weight gradients, which both follow dh and do not need each other, in one launch: the tiles of dx
+// first, each the longer chain of steps
+template <int TM>
+__global__ void __launch_bounds__(TTHR) train_f32_gradients_kernel(const TrainArgs a, unsigned rows, unsigned dx_tiles) {
+  __shared__ __align__(16) float lds[LDS_FLOATS];
+  unsigned b = blockIdx.x;
+  if (b < dx_tiles) {
+    tile<TF_DX, TM>(a, b % rows, b / rows, 0, lds);
+    return;
+  }
+  b -= dx_tiles;
+  const unsigned per = (unsigned)(a.H / 64) * (unsigned)(a.I / TN);
+  tile<TF_DW, 64>(a, b % per, b / per % a.E, b / per / a.E, lds);
 }
 
 // Rows of a tile: 64, or 32 where tiles of 64 would not give every CU one, or where groups have at most 32 rows on
 // average, so that most of 64 would be empty. 512 rows by H 1024 by I 1024, down: 29.2 us in 128 tiles of 64, 21.0 in
 // 256 of 32; 1024 rows: 31.2 and 32.9; 8192 rows, H 2048, I 4096, 8 groups: 1209 and 1311; 333 rows in 16 groups,
 // H 4096, I 1024: 99 and 69.
+int tile_rows(const TrainArgs& a, long long columns) {
+  const long long tiles = (a.P / 64 + (a.E + 1) / 2) * columns;
+  return tiles < CUS || a.P <= 32LL * a.E ? 32 : 64;
+}
+
 template <int FORM>
-hipError_t choose(const TrainArgs& a, int tile_columns, int n, hipStream_t st) {
-  if (a.P == 0) return hipSuccess;
-  const long long columns = n / tile_columns, tiles = (a.P / 64 + (a.E + 1) / 2) * columns;
-  if (tiles < CUS || a.P <= 32LL * a.E)
-    launch<FORM, 32>(a, columns, st);
-  else
-    launch<FORM, 64>(a, columns, st);
+hipError_t launch(const TrainArgs& a, int tile_columns, int n, hipStream_t st) {
+  const unsigned columns = (unsigned)(n / tile_columns), tm = tile_rows(a, columns);
+  const dim3 grid((unsigned)max_row_tiles(a.P, a.E, tm), columns);
+  if (grid.x == 0) return hipSuccess;
+  if (tm == 32) train_f32_kernel<FORM, 32><<<grid, TTHR, 0, st>>>(a);
+  else train_f32_kernel<FORM, 64><<<grid, TTHR, 0, st>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_train_f32(TrainForm form, const TrainArgs& a, hipStream_t st) {
+  const unsigned weight_tiles = (unsigned)(a.H / 64) * (unsigned)(a.I / TN);
   switch (form) {
-    case TF_GATE_UP: return choose<TF_GATE_UP>(a, TN / 2, a.I, st);
-    case TF_DOWN: return choose<TF_DOWN>(a, TN, a.H, st);
-    case TF_DH: return choose<TF_DH>(a, TN, a.I, st);
-    case TF_DX: return choose<TF_DX>(a, TN, a.H, st);
-    case TF_DW:  // x without slot_token here: its rows are gathered before
-      train_f32_kernel<TF_DW, 64><<<dim3((unsigned)(a.H / 64 * (a.I / TN)), (unsigned)a.E, 3), TTHR, 0, st>>>(a);
+    case TF_GATE_UP: return launch<TF_GATE_UP>(a, TN / 2, a.I, st);
+    case TF_DOWN: return launch<TF_DOWN>(a, TN, a.H, st);
+    case TF_DH: return launch<TF_DH>(a, TN, a.I, st);
+    case TF_DX: return launch<TF_DX>(a, TN, a.H, st);
+    case TF_DW:
+      train_f32_kernel<TF_DW, 64><<<dim3(weight_tiles, (unsigned)a.E, 3), TTHR, 0, st>>>(a);
       return hipGetLastError();
   }
   return hipErrorInvalidValue;
+}
+
+// One launch fills the CUs that few tiles leave idle: 666 rows in 5 groups, H 1024, I 384, 45 us, and 23 + 29 in two
+// (with dx's tiles of 32 rows, which are the same 45 here). Past 2^16 tiles there is nothing to fill, and the grid
+// stays far from 2^32 threads.
+hipError_t launch_gradients_f32(const TrainArgs& a, hipStream_t st) {
+  const unsigned columns = (unsigned)(a.H / TN), tm = a.P <= 32LL * a.E ? 32 : 64;
+  const long long rows = max_row_tiles(a.P, a.E, tm), weights = 3LL * a.E * (a.H / 64) * (a.I / TN), n = rows * columns + weights;
+  if (n > 1 << 16) {
+    const hipError_t e = launch_train_f32(TF_DX, a, st);
+    return e == hipSuccess ? launch_train_f32(TF_DW, a, st) : e;
+  }
+  const unsigned dx_tiles = (unsigned)(rows * columns);
+  if (tm == 32) train_f32_gradients_kernel<32><<<(unsigned)n, TTHR, 0, st>>>(a, (unsigned)rows, dx_tiles);
+  else train_f32_gradients_kernel<64><<<(unsigned)n, TTHR, 0, st>>>(a, (unsigned)rows, dx_tiles);
+  return hipGetLastError();
 }
 
 }  // namespace moe

@@ -1,4 +1,4 @@
-// Rows of x in the grouped order, zeros for tokens outside x, for the weight gradients: there the rows are
+// Rows of x in the grouped order, zeros for tokens outside x, for the weight gradients in bf16: there the rows are
 // the reduction index, and a row named by a token would take a dependent load in every step. One thread per
 // 16 bytes; bound by memory: 32768 rows of H 7168 in bf16 take 135 us, 3.5 TB/s read (from cache, a token's rows
 // after its first) and written, 2% of the gradient they serve.
@@ -18,8 +18,8 @@ __global__ void __launch_bounds__(GTHR) gather_rows_kernel(const u32x4* __restri
   out[id] = v;
 }
 
-hipError_t launch_gather_rows(int act, const TrainArgs& a, hipStream_t st) {
-  const int cpr = a.H / (act == MOE_F32 ? 4 : 8);
+hipError_t launch_gather_rows(const TrainArgs& a, hipStream_t st) {
+  const int cpr = a.H / 8;
   if (a.P == 0) return hipSuccess;
   const unsigned grid = (unsigned)(((long long)a.P * cpr + GTHR - 1) / GTHR);
   gather_rows_kernel<<<grid, GTHR, 0, st>>>((const u32x4*)a.x, a.slot_token, (u32x4*)a.xg, a.P, a.xrows, cpr);

@@ -120,21 +120,24 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
 def _run(tensors, stream, call):
-    """call(stream handle) with the tensors' GPU as the current one, so that the call and its stream belong to it."""
+    """call(device pointers of tensors, stream handle) with their GPU as the current one, so that the call and its
+    stream belong to it. The first tensor is not None."""
     import torch
     i = tensors[0].get_device()
+    at = []
     for t in tensors:
-        if t is not None and t.get_device() != i or i < 0:
+        if t is None:
+            at.append(None)
+        elif t.get_device() != i or i < 0:
             raise ValueError("the tensors of a call are on one GPU")
+        else:
+            at.append(t.data_ptr())
     if i != torch.cuda.current_device():
         with torch.cuda.device(i):
-            return _run(tensors, stream, call)
-    rc = call(torch._C._cuda_getCurrentRawStream(i) if stream is None else stream.cuda_stream)
+            rc = call(at, torch._C._cuda_getCurrentRawStream(i) if stream is None else stream.cuda_stream)
+    else:
+        rc = call(at, torch._C._cuda_getCurrentRawStream(i) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc)
 
@@ -284,26 +287,24 @@ def moe_train_workspace_size(shape: MoeShape) -> int:
 
 def moe_gated_ffn(shape, x, expert_offsets, slot_token, weights_: dict, gate_pre, up_pre, y_perm, ws, stream=None):
     """Weights row-major: gate, up [E, H, I], down [E, I, H]. gate_pre and up_pre may both be None."""
-    w = MoeWeights(weights_["gate"].data_ptr(), weights_["up"].data_ptr(), weights_["down"].data_ptr())
-    _run((ws, x, expert_offsets, slot_token, *weights_.values(), gate_pre, up_pre, y_perm), stream, lambda st: load().moe_gated_ffn(
-        shape, _ptr(x), _ptr(expert_offsets), _ptr(slot_token), w, _ptr(gate_pre), _ptr(up_pre), _ptr(y_perm),
-        ws.data_ptr(), ws.nbytes, st))
+    tensors = (ws, x, expert_offsets, slot_token, gate_pre, up_pre, y_perm, weights_["gate"], weights_["up"], weights_["down"])
+    _run(tensors, stream, lambda at, st: load().moe_gated_ffn(shape, *at[1:4], MoeWeights(*at[7:]), *at[4:7], at[0], ws.nbytes, st))
 
 
 def moe_gated_ffn_backward(shape, x, expert_offsets, slot_token, weights_: dict, gate_pre, up_pre, dy_perm, dx_perm,
                            grads: dict | None, ws, stream=None):
     """grads: gate, up and down tensors that receive the weights' gradients, or None; dx_perm may be None."""
-    w = MoeWeights(weights_["gate"].data_ptr(), weights_["up"].data_ptr(), weights_["down"].data_ptr())
-    g = None if grads is None else MoeWeightGrads(grads["gate"].data_ptr(), grads["up"].data_ptr(), grads["down"].data_ptr())
-    tensors = (ws, x, expert_offsets, slot_token, *weights_.values(), gate_pre, up_pre, dy_perm, dx_perm)
-    _run(tensors if grads is None else tensors + tuple(grads.values()), stream, lambda st: load().moe_gated_ffn_backward(
-        shape, _ptr(x), _ptr(expert_offsets), _ptr(slot_token), w, _ptr(gate_pre), _ptr(up_pre), _ptr(dy_perm),
-        _ptr(dx_perm), g, ws.data_ptr(), ws.nbytes, st))
+    tensors = (ws, x, expert_offsets, slot_token, gate_pre, up_pre, dy_perm, dx_perm,
+               weights_["gate"], weights_["up"], weights_["down"])
+    if grads is not None:
+        tensors += (grads["gate"], grads["up"], grads["down"])
+    _run(tensors, stream, lambda at, st: load().moe_gated_ffn_backward(
+        shape, *at[1:4], MoeWeights(*at[8:11]), *at[4:8], MoeWeightGrads(*at[11:]) if len(at) > 11 else None, at[0], ws.nbytes, st))
 
 
 def moe_combine_backward(shape, dy, y_perm, pair_slot, topk_w, dy_perm, dtopk_w, stream=None):
-    _run((dtopk_w, dy, y_perm, pair_slot, topk_w, dy_perm), stream, lambda st: load().moe_combine_backward(
-        shape, _ptr(dy), _ptr(y_perm), _ptr(pair_slot), _ptr(topk_w), _ptr(dy_perm), _ptr(dtopk_w), st))
+    _run((dy, y_perm, pair_slot, topk_w, dy_perm, dtopk_w), stream,
+         lambda at, st: load().moe_combine_backward(shape, *at, st))
 
 
 class AdamwTensors:
@@ -350,11 +351,15 @@ def moe_adamw(tensors: AdamwTensors, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, 
     """lr_dev, grad_scale (float32) and step_dev (int64): one-element device tensors read in place of lr, 1, step.
     seed: of the E4M3 state's random rounding."""
     c = MoeAdamwConfig(DTYPE[tensors.p_type], DTYPE[tensors.g_type], tensors.state, lr, beta1, beta2, eps, weight_decay,
-                       step, seed & 0xFFFFFFFF, _ptr(lr_dev), _ptr(step_dev), _ptr(grad_scale))
+                       step, seed & 0xFFFFFFFF)
     if not len(tensors.array):
         return
     import torch
     for t, dtype in ((lr_dev, torch.float32), (step_dev, torch.int64), (grad_scale, torch.float32)):
         if t is not None and (t.dtype != dtype or not t.numel()):
             raise ValueError("lr_dev and grad_scale hold a float32, step_dev an int64")
-    _run((tensors.keep[0][0], lr_dev, step_dev, grad_scale), stream, lambda st: load().moe_adamw(c, tensors.array, len(tensors.array), st))
+
+    def call(at, st):
+        c.lr_dev, c.step_dev, c.grad_scale = at[1:]
+        return load().moe_adamw(c, tensors.array, len(tensors.array), st)
+    _run((tensors.keep[0][0], lr_dev, step_dev, grad_scale), stream, call)

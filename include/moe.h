@@ -385,6 +385,7 @@ moe_status moe_quantize_int8(const void* x, int32_t rows, int32_t K, int8_t* cod
  * call of its own with E = k = 1. shape->path is not used. Rows are moe_permute's: expert e owns
  * rows [expert_offsets[e], expert_offsets[e+1]) of the T*k; offsets are read as clamped to
  * [0, T*k]. Sums and activations are fp32; each tensor below is rounded once, when it is written.
+ * The bits of a row's results depend on the row and its expert's weights alone, not on the other rows.
  *   expert_offsets int32[E+1]; NULL with E = 1: one group of all T rows
  *   slot_token     int32[T*k]: row r reads x[slot_token[r]], zeros for a token outside [0, T);
  *                  NULL: x is [T*k][H] and row r reads x[r]

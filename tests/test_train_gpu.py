@@ -162,6 +162,24 @@ def test_tile_shapes(name, act):
 
 
 @pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_a_row_does_not_depend_on_the_others(act):
+    """The first rows of each group alone give the bits they give among all, in other tile shapes."""
+    counts, H, I = [1300, 0, 2047, 600], 2432, 640
+    b = Block(counts, H, I, act, seed=22, gather=False)
+    say("row alone", act)
+    full = b.forward() | b.backward(grads=False)
+    few = [33, 0, 70, 1]
+    c = Block(few, H, I, act, seed=23, gather=False)
+    c.w = b.w
+    pick = torch.cat([torch.arange(b.rows(e)[0], b.rows(e)[0] + n, device=DEV) for e, n in enumerate(few)])
+    for name in ("x", "g", "u", "dy"):
+        getattr(c, name)[:c.n] = getattr(b, name)[pick]
+    part = c.forward() | c.backward(grads=False)
+    for name in ("g", "u", "y", "dx"):
+        assert torch.equal(part[name][:c.n], full[name][pick]), name
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
 def test_rows_in_order_and_partial_outputs(act):
     """slot_token NULL reads x by row; pre-activations, dx and the weight gradients may be left out."""
     b = Block([40, 0, 90], 256, 128, act, seed=8, gather=False)
