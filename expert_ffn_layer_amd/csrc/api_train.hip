@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <new>
 
 #include "api_util.h"
@@ -74,6 +75,11 @@ moe_status train_args(const moe_shape* s, const void* x, const int32_t* off, con
   return MOE_OK;
 }
 
+// Whether p is one of the others (NULL is nobody's)
+bool among(const void* p, std::initializer_list<const void*> others) {
+  return p && std::find(others.begin(), others.end(), p) != others.end();
+}
+
 hipError_t product(TrainForm form, int act, const TrainArgs& a, hipStream_t st) {
   return act == MOE_F32 ? launch_train_f32(form, a, st) : launch_train_bf16(form, a, st);
 }
@@ -126,6 +132,8 @@ moe_status moe_gated_ffn(const moe_shape* shape, const void* x, const int32_t* e
     return fail(MOE_ERR_INVALID_ARG, "gate_pre, up_pre and y_perm must be 16-byte aligned");
   if (a.P == 0) return MOE_OK;
   if (!y_perm) return fail(MOE_ERR_INVALID_ARG, "y_perm is NULL");
+  if (among(gate_pre, {up_pre, y_perm, x}) || among(up_pre, {y_perm, x}) || y_perm == x)
+    return fail(MOE_ERR_INVALID_ARG, "an output is an input's or another output's memory");
   a.g = gate_pre;
   a.u = up_pre;
   a.y = y_perm;
@@ -148,6 +156,12 @@ moe_status moe_gated_ffn_backward(const moe_shape* shape, const void* x, const i
   if (!al16(gate_pre) || !al16(up_pre) || !al16(dy_perm) || !al16(dx_perm) ||
       (grads && (!al16(grads->gate) || !al16(grads->up) || !al16(grads->down))))
     return fail(MOE_ERR_INVALID_ARG, "pre-activations and gradients must be 16-byte aligned");
+  const std::initializer_list<const void*> inputs = {x, gate_pre, up_pre, dy_perm, weights->gate, weights->up, weights->down};
+  if (among(dx_perm, inputs) ||
+      (grads && (among(grads->gate, inputs) || among(grads->up, inputs) || among(grads->down, inputs) ||
+                 among(grads->gate, {grads->up, grads->down, dx_perm}) || among(grads->up, {grads->down, dx_perm}) ||
+                 grads->down == dx_perm)))
+    return fail(MOE_ERR_INVALID_ARG, "an output is an input's or another output's memory");
   a.g = const_cast<void*>(gate_pre);
   a.u = const_cast<void*>(up_pre);
   a.dy = dy_perm;

@@ -9,8 +9,8 @@
 // a lane at the same k. Row strides of N + 4 floats make both reads free of bank conflicts. The column
 // operand is the MFMA's A, so a lane ends with 4 consecutive columns of one row.
 //
-// Bound by the matrix instructions where there are tiles enough (8192 rows, H 2048, I 4096, 8 groups: 112,
-// 118, 112, 105 and 108 TFLOP/s for the five forms in order, the card's fp32 library product 140), by a chain of
+// Bound by the matrix instructions where there are tiles enough (8192 rows, H 2048, I 4096, 8 groups: 113,
+// 119, 116, 113 and 106 TFLOP/s for the five forms in order, the card's fp32 library product 140), by a chain of
 // load, LDS and product per step below (16 tokens, H 256, I 128: 7.4 us and 5.1 us for the forward's two). The rows
 // of x that the weight gradients reduce over are found by tokens fetched as many steps before them again.
 #include "train.h"

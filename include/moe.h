@@ -401,7 +401,8 @@ moe_status moe_train_workspace_size(const moe_shape* shape, size_t* bytes);
  *   gate_pre, up_pre [T*k][I] act out: g and u (both, or both NULL: not kept)
  *   y_perm           [T*k][H] act out
  * h is formed from the unrounded g and u and kept in `ws` in the act type. Rows from
- * expert_offsets[E] on are not written. T == 0 enqueues nothing.
+ * expert_offsets[E] on are not written. T == 0 enqueues nothing. Outputs must not overlap x or each
+ * other.
  */
 moe_status moe_gated_ffn(const moe_shape* shape, const void* x, const int32_t* expert_offsets,
                          const int32_t* slot_token, const moe_weights* weights, void* gate_pre,
@@ -425,7 +426,7 @@ typedef struct {
  *            written. moe_combine with weights 1 sums the rows of each token.
  *   grads    out, or NULL: not computed. Every element is written; an expert without rows has
  *            gradient 0 (with T == 0 all have).
- * h, dg and du are kept in `ws` in the act type. Outputs must not overlap inputs. The same bits on
+ * h, dg and du are kept in `ws` in the act type. Outputs must not overlap inputs or each other. The same bits on
  * every run: no atomics.
  */
 moe_status moe_gated_ffn_backward(const moe_shape* shape, const void* x,

@@ -63,6 +63,15 @@ def test_block_refuses():
     assert ffn_backward(s, dx=None, grads=None) == 1
     assert ffn_backward(s, grads=(0x10000, None, 0x10000)) == 1 and ffn_backward(s, grads=(0x10000, 0x10000, 0x10008)) == 1
     assert ffn(shape(T=0), x=None, y=None, g=None, u=None) == 0  # nothing to do
+    apart = dict(x=P(0x20000), g=P(0x30000), u=P(0x40000), y=P(0x50000))
+    for a, b in (("g", "u"), ("g", "y"), ("u", "y"), ("y", "x"), ("g", "x")):
+        assert ffn(s, **apart | {a: apart[b]}) == 1 and "memory" in N.load().moe_last_error().decode()
+    apart = dict(x=P(0x20000), g=P(0x30000), u=P(0x40000), dy=P(0x50000), dx=P(0x60000), grads=(0x70000, 0x80000, 0x90000))
+    for name in ("x", "g", "u", "dy"):
+        assert ffn_backward(s, **apart | {"dx": apart[name]}) == 1 and "memory" in N.load().moe_last_error().decode()
+        assert ffn_backward(s, **apart | {"grads": (0x70000, apart[name].value, 0x90000)}) == 1
+    for grads in ((0x70000, 0x70000, 0x90000), (0x70000, 0x80000, 0x60000), (0x10000, 0x80000, 0x90000)):
+        assert ffn_backward(s, **apart | {"grads": grads}) == 1 and "memory" in N.load().moe_last_error().decode()
     lib = N.load()
     assert lib.moe_gated_ffn(None, OK, OK, OK, ctypes.byref(weights()), OK, OK, OK, OK, BIG, None) == 1
     assert lib.moe_gated_ffn(ctypes.byref(s), OK, OK, OK, None, OK, OK, OK, OK, BIG, None) == 1
