@@ -10,7 +10,7 @@
 // operand is the MFMA's A, so a lane ends with 4 consecutive columns of one row.
 //
 // Bound by the matrix instructions where there are tiles enough (8192 rows, H 2048, I 4096, 8 groups: 113,
-// 119, 116, 113 and 106 TFLOP/s for the five forms in order, the card's fp32 library product 140), by a chain of
+// 120, 111, 111 and 106 TFLOP/s for the five forms in order, the card's fp32 library product 140), by a chain of
 // load, LDS and product per step below (16 tokens, H 256, I 128: 7.4 us and 5.1 us for the forward's two). The rows
 // of x that the weight gradients reduce over are found by tokens fetched as many steps before them again.
 #include "train.h"
@@ -162,11 +162,13 @@ __device__ __forceinline__ void tile(const TrainArgs& a, int bx, int by, int bz,
     fetch_tokens(k0 + AHEAD * TK, set);
   };
 
-  f32x4 acc[2][RT];
+  // A round's sums are added to the total at its end: the error of a product stays at that of a chain of 128
+  // additions (3.6 2^-24 of its norm at K = 2048 and at 640)
+  f32x4 acc[2][RT], total[2][RT];
 #pragma unroll
   for (int t = 0; t < 2; ++t)
 #pragma unroll
-    for (int j = 0; j < RT; ++j) acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < RT; ++j) acc[t][j] = total[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   auto qcol = [&](int t) { return FORM == TF_GATE_UP ? t * 32 + wc * 16 : wc * 32 + t * 16; };
   auto step = [&](int k0, int set) __attribute__((always_inline)) {
@@ -228,6 +230,13 @@ __device__ __forceinline__ void tile(const TrainArgs& a, int bx, int by, int bz,
       if (FORM == TF_DW && k0 + u * TK >= K) break;
       step(k0 + u * TK, u);
     }
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        total[t][r] += acc[t][r];
+        acc[t][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
   }
 
   // lane: columns qcol(t) + 4 g + [0, 4) of row wr * TM / 2 + r * 16 + l16
@@ -239,10 +248,10 @@ __device__ __forceinline__ void tile(const TrainArgs& a, int bx, int by, int bz,
       const size_t at = m * I + n0 + wc * 16 + 4 * g;
       fvec4 hv;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) hv[i] = silu(acc[0][r][i]) * acc[1][r][i];
+      for (int i = 0; i < 4; ++i) hv[i] = silu(total[0][r][i]) * total[1][r][i];
       if (a.g) {
-        store4((float*)a.g + at, acc[0][r]);
-        store4((float*)a.u + at, acc[1][r]);
+        store4((float*)a.g + at, total[0][r]);
+        store4((float*)a.u + at, total[1][r]);
       }
       store4((float*)a.h + at, hv);
       continue;
@@ -255,7 +264,7 @@ __device__ __forceinline__ void tile(const TrainArgs& a, int bx, int by, int bz,
         fvec4 dg, du, hv;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float s = 1.0f / (1.0f + __expf(-gv[i])), si = gv[i] * s, dh = acc[t][r][i];
+          const float s = 1.0f / (1.0f + __expf(-gv[i])), si = gv[i] * s, dh = total[t][r][i];
           du[i] = dh * si;
           dg[i] = dh * uv[i] * (s + si * (1.0f - s));
           hv[i] = si * uv[i];
@@ -265,16 +274,17 @@ __device__ __forceinline__ void tile(const TrainArgs& a, int bx, int by, int bz,
         store4((float*)a.h + m * I + n, hv);
       } else if constexpr (FORM == TF_DW) {
         float* o = (float*)(mat == 0 ? a.dgate : mat == 1 ? a.dup : a.ddown) + e * HI;
-        store4(o + m * (mat == 2 ? H : I) + n, acc[t][r]);
+        store4(o + m * (mat == 2 ? H : I) + n, total[t][r]);
       } else {
-        store4((float*)(FORM == TF_DOWN ? a.y : a.dx) + m * H + n, acc[t][r]);
+        store4((float*)(FORM == TF_DOWN ? a.y : a.dx) + m * H + n, total[t][r]);
       }
     }
   }
 }
 
+// 4 waves a SIMD, so 128 registers at most: 1 to 5% faster than 3 waves with some more registers
 template <int FORM, int TM>
-__global__ void __launch_bounds__(TTHR) train_f32_kernel(const TrainArgs a) {
+__global__ void __launch_bounds__(TTHR, 4) train_f32_kernel(const TrainArgs a) {
   __shared__ __align__(16) float lds[LDS_FLOATS];
   tile<FORM, TM>(a, blockIdx.x, blockIdx.y, blockIdx.z, lds);
 }
@@ -282,7 +292,7 @@ __global__ void __launch_bounds__(TTHR) train_f32_kernel(const TrainArgs a) {
 // dx and the weight gradients, which both follow dh and do not need each other, in one launch: the tiles of dx
 // first, each the longer chain of steps
 template <int TM>
-__global__ void __launch_bounds__(TTHR) train_f32_gradients_kernel(const TrainArgs a, unsigned rows, unsigned dx_tiles) {
+__global__ void __launch_bounds__(TTHR, 4) train_f32_gradients_kernel(const TrainArgs a, unsigned rows, unsigned dx_tiles) {
   __shared__ __align__(16) float lds[LDS_FLOATS];
   unsigned b = blockIdx.x;
   if (b < dx_tiles) {
