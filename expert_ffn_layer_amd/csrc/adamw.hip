@@ -123,13 +123,24 @@ __device__ __forceinline__ float to_e4m3(float y, uint32_t bits) {
   const float z = __uint_as_float((__float_as_uint(a + low) + bits) & 0xFFF00000u) - low;
   return __builtin_copysignf(z, y);
 }
-// codes of the lane's 8 values over their block's scale, which the block's 32 lanes agree on
-__device__ __forceinline__ u32x2 encode(const float (&v)[AV], const uint32_t (&bits)[AV], float& scale) {
+// largest magnitude in the block of the lane's 8 values and its 31 neighbours'; a NaN does not count
+__device__ __forceinline__ float block_top(const float (&v)[AV]) {
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < AV; ++i) top = __builtin_fmaxf(top, __builtin_fabsf(v[i]));
 #pragma unroll
   for (int s = 1; s < 32; s <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, s));
+  return top;
+}
+// codes of the lane's 8 values over their block's scale, which the block's 32 lanes agree on
+__device__ __forceinline__ u32x2 encode(float (&v)[AV], const uint32_t (&bits)[AV], float& scale) {
+  float top = block_top(v);
+  if (top == __builtin_inff()) {
+    // an infinity becomes NaN, which has a code, and does not reach the scale and the block's other elements
+#pragma unroll
+    for (int i = 0; i < AV; ++i) v[i] = __builtin_fabsf(v[i]) == __builtin_inff() ? __builtin_nanf("") : v[i];
+    top = block_top(v);
+  }
   top = __builtin_fmaxf(top, MIN_TOP);
   const float inv = E4M3_MAX * (1.0f / top);
   scale = top * (1.0f / E4M3_MAX);

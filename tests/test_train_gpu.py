@@ -502,6 +502,10 @@ def test_adamw_non_finite_gradients_stay_in_their_elements():
         N.moe_adamw(c["table"], lr=1e-3, step=2)
         bad = ~torch.isfinite(c["p"][0].float())
         assert bad[3] and bad[700] and bad.sum() == 2
+        c["g"][0].fill_(1e-3)  # nor do the states carry them to other elements of a block
+        N.moe_adamw(c["table"], lr=1e-3, step=3)
+        bad = ~torch.isfinite(c["p"][0].float())
+        assert bad[3] and bad[700] and bad.sum() == 2
 
 
 def test_adamw_captured_step_follows_device_values():
