@@ -583,12 +583,10 @@ hipError_t launch(const TrainArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Which tile. The estimates are in microseconds per step of 64 reduction elements and round of the card,
-// fitted to runs at 16 to 32768 rows, 1 to 32 groups and the V3 and Qwen3 widths (one CU takes one 256 x 256
-// or deep-ring workgroup, two 128 x 128 ones):
-//   256 x 256            1.2
-//   128 x 128            1.1 a round of 512, 0.75 where each has a CU to itself
-//   64 x 256, 4 slots    0.67     64 x 128, 4 slots    0.43
+// Which tile, by the time it would take: rounds of the card times the time of a tile, steps of 64 reduction elements
+// at so many microseconds each and what does not depend on them. Fitted to runs of 110 random sizes (8 to 32768 rows,
+// 1 to 48 groups, H to 7168, I to 2048), where the tile taken is 0.3% slower than the best of the four on average,
+// 0.2% for the weight gradients (one CU takes one 256 x 256 or four-slot workgroup, two 128 x 128 ones).
 // Large problems are bound by the matrix cores and take the tile that reads LDS least; few or thin groups
 // leave CUs empty or rows unused, and there the latency of a step counts: more and smaller tiles, more stages in
 // flight. Measured on gate/up, best of the others in brackets: 32768 rows in 32 groups 1.78 ms (2.49); one
@@ -597,11 +595,10 @@ template <int FORM>
 hipError_t choose(const TrainArgs& a, hipStream_t st) {
   auto rounds = [](double tiles, int per) { return (double)(long long)((tiles + per - 1) / per); };
   if constexpr (FORM == TF_DW) {
-    // per tile also its start and the writing of its results, which two workgroups on a CU hide; the 128 x 128
-    // tiles' shorter rows of results cost at least 8.6 us a round
+    // the 128 x 128 tiles' shorter rows of results cost at least 5.4 us a round
     const double steps = ((double)a.P / a.E + 127) / 128 * 2;
     const auto tiles = [&](int b) { return 3.0 * a.E * ((a.H + b - 1) / b) * ((a.I + b - 1) / b); };
-    const double big = rounds(tiles(256), 256) * (steps + 12), small = rounds(tiles(128), 512) * std::max(steps + 1, 8.6);
+    const double big = rounds(tiles(256), 256) * (1.24 * steps + 12), small = rounds(tiles(128), 512) * std::max(0.8 * steps + 4.2, 5.4);
     return big <= small ? launch<FORM, 2, 2, 4, 4, 2>(a, st) : launch<FORM, 2, 2, 2, 2, 2>(a, st);
   } else {
     const int N = FORM == TF_DOWN || FORM == TF_DX ? a.H : a.I, share = FORM == TF_GATE_UP ? 2 : 1;
@@ -610,9 +607,11 @@ hipError_t choose(const TrainArgs& a, hipStream_t st) {
       const double rows = a.E == 1 ? (a.P + bm - 1) / bm : std::max<double>(groups, (double)a.P / bm + groups * 0.5);
       return rows * ((N * share + bn - 1) / bn);
     };
-    const double b = tiles(128, 128);
-    const double t[4] = {rounds(tiles(256, 256), 256) * 1.2, rounds(b, 512) * (b > 256 ? 1.1 : 0.75),
-                         rounds(tiles(64, 256), 256) * 0.67, rounds(tiles(64, 128), 256) * 0.43};
+    const double steps = (FORM == TF_GATE_UP || FORM == TF_DH ? a.H : FORM == TF_DOWN ? a.I : 2 * a.I) / BK, b = tiles(128, 128);
+    const double t[4] = {rounds(tiles(256, 256), 256) * (1.1 * steps + 11),
+                         b > 256 ? rounds(b, 512) * (1.0 * steps + 3.8) + 3.7 : 0.52 * steps + 6.4,
+                         rounds(tiles(64, 256), 256) * (0.47 * steps + 6.4) + 1.1,
+                         rounds(tiles(64, 128), 256) * (0.31 * steps + 3.9) + 2.7};
     // The layer's weights go through once, no second row tile reads them and the last-level cache could not hold
     // them from before: 440 rows, H 4096, I 1536, 16 groups, gate/up 89 us with the default policy, 78 so; 100
     // rows in 8 groups, whose 200 MB were in the cache, 41 and 66.

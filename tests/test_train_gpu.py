@@ -147,6 +147,8 @@ TILES = {
     "mixed": ([64, 149, 0, 1200, 589, 256, 405, 1200, 736, 129, 173, 412], 384, 384),
     "many-rows": ([1125, 452, 204, 0, 831, 398, 53, 75, 2400, 512, 257, 87, 2400, 476, 128, 690, 1, 255, 968, 368], 384, 384),
     "wide": ([978, 408, 0, 598, 1281, 291, 242, 298, 616], 1664, 384),
+    "uneven": ([90, 67, 35, 80, 27, 0, 58, 143, 107, 68, 150, 0, 15, 10, 24, 150, 12, 44, 70, 102], 1664, 1152),
+    "two-rows": ([1, 1], 7040, 3968),
     "deep": ([86, 282, 96, 18, 33, 300, 300, 42, 131, 40, 58, 173, 1, 14, 0, 274, 15, 51, 129, 222], 384, 2688),
 }
 
