@@ -14,9 +14,11 @@
 // Bound by memory: every array is read or written once. A workgroup takes 8192 consecutive elements
 // of one tensor, 8 a lane and pass, so 32 lanes hold one block of the 8-bit form and its maximum takes
 // 5 lane exchanges; 2048 where that would leave CUs without work (five tensors of 0.8 M elements: 10.1
-// us by 8192, 6.8 by 2048; twelve of 14.7 M 5.2 TB/s with fp32 states and master copies, ten 4.8 TB/s with
+// us by 8192, 6.8 by 2048; twelve of 14.7 M 5.3 TB/s with fp32 states and master copies, ten 5.0 TB/s with
 // 8-bit ones, where a large copy reaches 4.9). The tensor table travels in the kernel arguments: no copy,
 // no table kept.
+#include <type_traits>
+
 #include "train.h"
 
 namespace moe {
@@ -53,19 +55,19 @@ __device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = (uint16_t)pack_bf16x2(v, 0.f); }
 
-// the lane's elements at, at + 1, ... below n; the others read as zero
-template <typename T>
+// the lane's elements at, at + 1, ... below n; the others read as zero. FULL: all 8 are below n
+template <bool FULL, typename T>
 __device__ __forceinline__ void load_some(const T* p, int64_t at, int64_t n, float (&v)[AV]) {
-  if (at + AV <= n) {
+  if (FULL || at + AV <= n) {
     load8(p + at, v);
     return;
   }
 #pragma unroll
   for (int i = 0; i < AV; ++i) v[i] = at + i < n ? load1(p + at + i) : 0.f;
 }
-template <typename T>
+template <bool FULL, typename T>
 __device__ __forceinline__ void store_some(T* p, int64_t at, int64_t n, const float (&v)[AV]) {
-  if (at + AV <= n) {
+  if (FULL || at + AV <= n) {
     store8(p + at, v);
     return;
   }
@@ -74,16 +76,18 @@ __device__ __forceinline__ void store_some(T* p, int64_t at, int64_t n, const fl
     if (at + i < n) store1(p + at + i, v[i]);
 }
 
+template <bool FULL>
 __device__ __forceinline__ u32x2 load_codes(const uint8_t* p, int64_t at, int64_t n) {
-  if (at + AV <= n) return *(const u32x2*)(p + at);
+  if (FULL || at + AV <= n) return *(const u32x2*)(p + at);
   u32x2 c = {0u, 0u};
 #pragma unroll
   for (int i = 0; i < AV; ++i)
     if (at + i < n) c[i >> 2] |= (uint32_t)p[at + i] << (8 * (i & 3));
   return c;
 }
+template <bool FULL>
 __device__ __forceinline__ void store_codes(uint8_t* p, int64_t at, int64_t n, u32x2 c) {
-  if (at + AV <= n) {
+  if (FULL || at + AV <= n) {
     *(u32x2*)(p + at) = c;
     return;
   }
@@ -123,24 +127,13 @@ __device__ __forceinline__ float to_e4m3(float y, uint32_t bits) {
   const float z = __uint_as_float((__float_as_uint(a + low) + bits) & 0xFFF00000u) - low;
   return __builtin_copysignf(z, y);
 }
-// largest magnitude in the block of the lane's 8 values and its 31 neighbours'; a NaN does not count
-__device__ __forceinline__ float block_top(const float (&v)[AV]) {
+// codes of the lane's 8 values over their block's scale, which the block's 32 lanes agree on
+__device__ __forceinline__ u32x2 encode(const float (&v)[AV], const uint32_t (&bits)[AV], float& scale) {
   float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < AV; ++i) top = __builtin_fmaxf(top, __builtin_fabsf(v[i]));
+  for (int i = 0; i < AV; ++i) top = __builtin_fmaxf(top, __builtin_fabsf(v[i]));  // a NaN does not count
 #pragma unroll
   for (int s = 1; s < 32; s <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, s));
-  return top;
-}
-// codes of the lane's 8 values over their block's scale, which the block's 32 lanes agree on
-__device__ __forceinline__ u32x2 encode(float (&v)[AV], const uint32_t (&bits)[AV], float& scale) {
-  float top = block_top(v);
-  if (top == __builtin_inff()) {
-    // an infinity becomes NaN, which has a code, and does not reach the scale and the block's other elements
-#pragma unroll
-    for (int i = 0; i < AV; ++i) v[i] = __builtin_fabsf(v[i]) == __builtin_inff() ? __builtin_nanf("") : v[i];
-    top = block_top(v);
-  }
   top = __builtin_fmaxf(top, MIN_TOP);
   const float inv = E4M3_MAX * (1.0f / top);
   scale = top * (1.0f / E4M3_MAX);
@@ -156,6 +149,15 @@ __device__ __forceinline__ u32x2 encode(float (&v)[AV], const uint32_t (&bits)[A
   return c;
 }
 
+// Square root by one Newton step on v * rsq(v) with an exact residual: correctly rounded but for rare halfway cases, 6
+// operations where the compiler's takes 17 (the 8-bit form has 76 an element: 149 M elements take 299 us so and 308
+// with that one). 0 and NaN stay, and an infinity becomes NaN: that has a code and does not reach the scale of its
+// block. Under 2^-126, where v itself has lost its digits, the root comes out too small.
+__device__ __forceinline__ float root(float v) {
+  const float y = __builtin_amdgcn_rsqf(__builtin_fmaxf(v, 0x1p-126f)), s = v * y;
+  return __builtin_fmaf(__builtin_fmaf(-s, s, v), 0.5f * y, s);
+}
+
 template <typename PT, typename GT, bool MASTER, bool Q8>
 __global__ void __launch_bounds__(ATHR) adamw_kernel(const AdamArgs a) {
   // every product and sum rounds by itself, so the 8-bit codes are the same whatever the compiler would fuse
@@ -166,6 +168,7 @@ __global__ void __launch_bounds__(ATHR) adamw_kernel(const AdamArgs a) {
   const int ti = __builtin_popcountll(__ballot(after));
   const AdamTensor& t = a.t[ti];
   const int64_t n = t.n, base = (int64_t)(block - a.first[ti]) * (a.passes * ASTEP) + threadIdx.x * AV;
+  const int64_t wave_end = (int64_t)(block - a.first[ti]) * (a.passes * ASTEP) + (__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + 1) * 64 * AV;
   PT* const p = (PT*)t.p;
   const GT* const g = (const GT*)t.g;
 
@@ -184,37 +187,35 @@ __global__ void __launch_bounds__(ATHR) adamw_kernel(const AdamArgs a) {
   const uint32_t key = Q8 ? dither_key(a.seed, (uint32_t)step) : 0u;
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
 
-  for (int pass = 0; pass < a.passes; ++pass) {
-    const int64_t at = base + (int64_t)pass * ASTEP;
-    // a half wave without elements leaves together, so every block's lanes stay for its maximum
-    if ((at & ~(int64_t)255) >= n) return;
+  auto pass_at = [&](int64_t at, auto full) __attribute__((always_inline)) {
+    constexpr bool FULL = decltype(full)::value;
     float w[AV], gv[AV], m[AV], v[AV], r[AV];
-    if constexpr (MASTER) load_some(t.master, at, n, w);
-    else load_some((const PT*)p, at, n, w);
-    load_some(g, at, n, gv);
+    if constexpr (MASTER) load_some<FULL>(t.master, at, n, w);
+    else load_some<FULL>((const PT*)p, at, n, w);
+    load_some<FULL>(g, at, n, gv);
     if constexpr (Q8) {
       const int64_t b = at >> 8;
-      const u32x2 cm = load_codes((const uint8_t*)t.m, at, n), cr = load_codes((const uint8_t*)t.v, at, n);
+      const u32x2 cm = load_codes<FULL>((const uint8_t*)t.m, at, n), cr = load_codes<FULL>((const uint8_t*)t.v, at, n);
       decode(cm, t.ms[b], m);
       decode(cr, t.vs[b], r);
 #pragma unroll
       for (int i = 0; i < AV; ++i) v[i] = r[i] * r[i];
     } else {
-      load_some((const float*)t.m, at, n, m);
-      load_some((const float*)t.v, at, n, v);
+      load_some<FULL>((const float*)t.m, at, n, m);
+      load_some<FULL>((const float*)t.v, at, n, v);
     }
 #pragma unroll
     for (int i = 0; i < AV; ++i) {
       const float gi = gv[i] * gs;
       m[i] = a.beta1 * m[i] + a.one_minus_beta1 * gi;
       v[i] = a.beta2 * v[i] + a.one_minus_beta2 * (gi * gi);
-      r[i] = __builtin_sqrtf(v[i]);
+      r[i] = Q8 ? root(v[i]) : __builtin_sqrtf(v[i]);
       // hardware reciprocal, about 1 ulp of an update that is itself about lr
       const float low = __builtin_fmaf(r[i], inv_root_bc2, a.eps);
       w[i] -= __builtin_fmaf(lrwd, w[i], step_size * (m[i] * __builtin_amdgcn_rcpf(low)));
     }
-    if constexpr (MASTER) store_some(t.master, at, n, w);
-    store_some(p, at, n, w);
+    if constexpr (MASTER) store_some<FULL>(t.master, at, n, w);
+    store_some<FULL>(p, at, n, w);
     if constexpr (Q8) {
       float sm, sr;
       uint32_t bm[AV], br[AV];
@@ -223,17 +224,31 @@ __global__ void __launch_bounds__(ATHR) adamw_kernel(const AdamArgs a) {
         const uint32_t x = dither((uint32_t)at + i, key);
         bm[i] = x >> 12;
         br[i] = x & 0xFFFFFu;
+        m[i] = __builtin_fmaf(0.f, r[i], m[i]);  // NaN where the root is
       }
       const u32x2 cm = encode(m, bm, sm), cr = encode(r, br, sr);
-      store_codes((uint8_t*)t.m, at, n, cm);
-      store_codes((uint8_t*)t.v, at, n, cr);
+      store_codes<FULL>((uint8_t*)t.m, at, n, cm);
+      store_codes<FULL>((uint8_t*)t.v, at, n, cr);
       if ((lane & 31) == 0) {
         t.ms[at >> 8] = sm;
         t.vs[at >> 8] = sr;
       }
     } else {
-      store_some((float*)t.m, at, n, m);
-      store_some((float*)t.v, at, n, v);
+      store_some<FULL>((float*)t.m, at, n, m);
+      store_some<FULL>((float*)t.v, at, n, v);
+    }
+  };
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int64_t at = base + (int64_t)pass * ASTEP;
+    // A wave whose elements are all there takes a path without conditions, whose loads leave together (fp32 states
+    // with master copies 945 us, 957 by the other path); the 8-bit form, with more to compute between its loads, is
+    // faster without it (299 and 320 us). In the other path a half wave without elements leaves together, so every
+    // block's lanes stay for its maximum.
+    if (!Q8 && wave_end + (int64_t)pass * ASTEP <= n) {
+      pass_at(at, std::true_type{});
+    } else {
+      if ((at & ~(int64_t)255) >= n) return;
+      pass_at(at, std::false_type{});
     }
   }
 }

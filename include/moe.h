@@ -470,8 +470,8 @@ moe_status moe_combine_backward(const moe_shape* shape, const void* dy, const vo
  * moe_adamw_config: lr_dev, step_dev and grad_scale (device, each may be NULL) are read by the kernel
  * in place of lr, step and 1, so that a captured call follows them; step_dev below 1 counts as 1.
  * lr, eps, weight_decay >= 0; beta1, beta2 in [0, 1); step >= 1. Non-finite gradients reach p, m
- * and v as the formulas say; in the E4M3 form m and sqrt(v) hold NaN for an infinity, and the other
- * elements of its 256 are not affected. count == 0 enqueues nothing; both structs are host memory
+ * and v as the formulas say; in the E4M3 form p, m and sqrt(v) become NaN where v is infinite, and the
+ * other elements of its 256 are not affected. count == 0 enqueues nothing; both structs are host memory
  * read during the call.
  */
 typedef enum { MOE_ADAM_F32 = 0, MOE_ADAM_E4M3 = 1 } moe_adam_state;
