@@ -586,7 +586,7 @@ hipError_t launch(const TrainArgs& a, hipStream_t st) {
 // Which tile, by the time it would take: rounds of the card times the time of a tile, steps of 64 reduction elements
 // at so many microseconds each and what does not depend on them. Fitted to runs of 110 random sizes (8 to 32768 rows,
 // 1 to 48 groups, H to 7168, I to 2048), where the tile taken is 0.3% slower than the best of the four on average,
-// 0.2% for the weight gradients (one CU takes one 256 x 256 or four-slot workgroup, two 128 x 128 ones).
+// 0.6% for the weight gradients (one CU takes one 256 x 256 or four-slot workgroup, two 128 x 128 ones).
 // Large problems are bound by the matrix cores and take the tile that reads LDS least; few or thin groups
 // leave CUs empty or rows unused, and there the latency of a step counts: more and smaller tiles, more stages in
 // flight. Measured on gate/up, best of the others in brackets: 32768 rows in 32 groups 1.78 ms (2.49); one
