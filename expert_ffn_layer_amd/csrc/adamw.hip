@@ -14,7 +14,7 @@
 // Bound by memory: every array is read or written once. A workgroup takes 8192 consecutive elements
 // of one tensor, 8 a lane and pass, so 32 lanes hold one block of the 8-bit form and its maximum takes
 // 5 lane exchanges; 2048 where that would leave CUs without work (five tensors of 0.8 M elements: 10.1
-// us by 8192, 6.8 by 2048; twelve of 14.7 M 5.3 TB/s with fp32 states and master copies, ten 5.0 TB/s with
+// us by 8192, 6.8 by 2048; twelve of 14.7 M 5.3 TB/s with fp32 states and master copies, ten 4.9 TB/s with
 // 8-bit ones, where a large copy reaches 4.9). The tensor table travels in the kernel arguments: no copy,
 // no table kept.
 #include <type_traits>
@@ -149,13 +149,15 @@ __device__ __forceinline__ u32x2 encode(const float (&v)[AV], const uint32_t (&b
   return c;
 }
 
-// Square root by one Newton step on v * rsq(v) with an exact residual: correctly rounded but for rare halfway cases, 6
-// operations where the compiler's takes 17 (the 8-bit form has 76 an element: 149 M elements take 299 us so and 308
-// with that one). 0 and NaN stay, and an infinity becomes NaN: that has a code and does not reach the scale of its
-// block. Under 2^-126, where v itself has lost its digits, the root comes out too small.
+// Square root by one Newton step on v * rsq(v) with an exact residual: correctly rounded but for rare halfway cases.
+// Values below 2^-96 go through 2^24 times them, for the hardware's rsq takes no denormals. 11 operations where the
+// compiler's takes 17, of 76 an element of the 8-bit form. 0 and NaN stay, and an infinity becomes NaN: that has a code
+// and does not reach the scale of its block.
 __device__ __forceinline__ float root(float v) {
-  const float y = __builtin_amdgcn_rsqf(__builtin_fmaxf(v, 0x1p-126f)), s = v * y;
-  return __builtin_fmaf(__builtin_fmaf(-s, s, v), 0.5f * y, s);
+  const bool low = v < 0x1p-96f;
+  const float x = v * (low ? 0x1p24f : 1.0f);
+  const float y = __builtin_amdgcn_rsqf(__builtin_fmaxf(x, 0x1p-126f)), s = x * y;
+  return __builtin_fmaf(__builtin_fmaf(-s, s, x), 0.5f * y, s) * (low ? 0x1p-12f : 1.0f);
 }
 
 template <typename PT, typename GT, bool MASTER, bool Q8>
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(ATHR) adamw_kernel(const AdamArgs a) {
     const int64_t at = base + (int64_t)pass * ASTEP;
     // A wave whose elements are all there takes a path without conditions, whose loads leave together (fp32 states
     // with master copies 945 us, 957 by the other path); the 8-bit form, with more to compute between its loads, is
-    // faster without it (299 and 320 us). In the other path a half wave without elements leaves together, so every
+    // 7% slower by it. In the other path a half wave without elements leaves together, so every
     // block's lanes stay for its maximum.
     if (!Q8 && wave_end + (int64_t)pass * ASTEP <= n) {
       pass_at(at, std::true_type{});

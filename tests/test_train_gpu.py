@@ -496,6 +496,20 @@ def test_adamw_zero_state_and_zero_gradients():
         assert torch.equal(c["p"][0][768:], before[768:])
 
 
+def test_adamw_tiny_gradients_without_eps():
+    """v = 1e-41 is a denormal number of 7136 steps: the first update is lr within 2^-12 of it, in both formats."""
+    for state in ("f32", "e4m3"):
+        c = adam_case([700], "f32", "f32", False, state, seed=14)
+        for name in ("m", "v", "ms", "rs"):
+            if c[name] is not None:
+                c[name][0].zero_()
+        c["p"][0].zero_()
+        c["g"][0].fill_(-1e-20)
+        N.moe_adamw(c["table"], lr=1e-2, beta1=0.9, beta2=0.9, eps=0.0, step=1)
+        # g^2 and v are rounded to 2^-149: 2^-17 and 2^-13.8 of them, half of that in the root
+        assert ((c["p"][0] - 1e-2).abs() <= 1e-2 * 2.0 ** -12).all(), state
+
+
 def test_adamw_non_finite_gradients_stay_in_their_elements():
     for state in ("f32", "e4m3"):
         c = adam_case([2000], "bf16", "bf16", False, state, seed=5)
