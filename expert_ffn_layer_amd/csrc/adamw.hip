@@ -119,13 +119,13 @@ __device__ __forceinline__ uint32_t dither(uint32_t index, uint32_t key) {
 }
 // y (at most about 448 in magnitude) to an e4m3 value: adding 20 random bits below the 3 kept
 // mantissa bits and cutting carries with the probability wanted. Under 2^-6 the codes are 2^-9
-// apart, which adding 2^-6 turns into the same cut.
+// apart, which adding 2^-6 turns into the same cut. A NaN's word could carry into the sign, so the
+// minimum makes a number of it first and 0 y brings it back: no more operations than a compare and select.
 __device__ __forceinline__ float to_e4m3(float y, uint32_t bits) {
-  float a = __builtin_fabsf(y);
-  a = a > E4M3_MAX ? E4M3_MAX : a;  // a NaN stays
+  const float a = __builtin_fminf(__builtin_fabsf(y), E4M3_MAX);
   const float low = a < 0x1p-6f ? 0x1p-6f : 0.0f;
   const float z = __uint_as_float((__float_as_uint(a + low) + bits) & 0xFFF00000u) - low;
-  return __builtin_copysignf(z, y);
+  return __builtin_copysignf(__builtin_fmaf(0.0f, y, z), y);
 }
 // codes of the lane's 8 values over their block's scale, which the block's 32 lanes agree on
 __device__ __forceinline__ u32x2 encode(const float (&v)[AV], const uint32_t (&bits)[AV], float& scale) {

@@ -1,0 +1,49 @@
+"""What include/moe.h and TrainableLayer promise about training beside the formulas, on the GPU."""
+import pytest
+import torch
+
+from expert_ffn_layer_amd import native as N
+
+from _gpu import say
+from _train import DT
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+
+
+def gen_of(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def normal(gen, shape, dtype, std=1.0):
+    return (torch.randn(shape, generator=gen, device=DEV) * std).to(dtype)
+
+
+# ------------------------------------------------------------------------------------------------
+# AdamW
+
+def is_nan_code(codes):
+    return (codes & 0x7F) == 0x7F
+
+
+@pytest.mark.parametrize("g,word", [("bf16", 0x7FFF), ("bf16", 0xFFFF), ("bf16", 0x7FC0), ("bf16", 0x7F80), ("bf16", 0xFF80),
+                                    ("f32", 0x7FFFFFFF), ("f32", 0xFFFFFFFF), ("f32", 0x7FC00001), ("f32", 0x7F800000)])
+def test_adamw_8_bit_states_keep_every_nan(g, word):
+    """m and sqrt(v) become NaN exactly where the gradient is NaN or infinite, whatever the NaN's payload, and stay so."""
+    say("nan codes", g, hex(word))
+    n = 20_000
+    gen = gen_of(word)
+    p, grad = normal(gen, (n,), torch.bfloat16, 0.05), normal(gen, (n,), DT[g], 1e-3)
+    at = torch.rand(n, generator=gen, device=DEV) < 0.1
+    bits = grad.view(torch.int16 if g == "bf16" else torch.int32)
+    bits[at] = word - (1 << 16) if g == "bf16" and word >> 15 else word - (1 << 32) if word >> 31 else word
+    m, v = (torch.zeros(n, dtype=torch.uint8, device=DEV) for _ in range(2))
+    ms, vs = (torch.zeros((n + 255) // 256, device=DEV) for _ in range(2))
+    table = N.adamw_tensors([p], [grad], [m], [v], None, [ms], [vs])
+    for step in range(1, 9):
+        N.moe_adamw(table, lr=1e-3, step=step, seed=1000 * step)
+        if step == 4:
+            grad.fill_(1e-3)
+        assert torch.equal(is_nan_code(m), at) and torch.equal(is_nan_code(v), at), step
+        assert torch.equal(torch.isnan(p), at), step
+        assert torch.isfinite(ms).all() and torch.isfinite(vs).all()
