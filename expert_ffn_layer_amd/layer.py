@@ -120,7 +120,7 @@ class TrainableLayer:
         ws = max(N.moe_workspace_size(self.shapes[0]), *[N.moe_train_workspace_size(s) for s in self.shapes])
         self.ws = torch.empty(ws, dtype=torch.uint8, device=dev)
         self.idx, self.pair_slot = (torch.empty((T, self.k), dtype=torch.int32, device=dev) for _ in range(2))
-        self.w, self.dw = (torch.empty((T, self.k), dtype=torch.float32, device=dev) for _ in range(2))
+        self.w = torch.empty((T, self.k), dtype=torch.float32, device=dev)
         self.ones = torch.ones((T, self.k), dtype=torch.float32, device=dev)
         self.off = torch.zeros(self.E + 1, dtype=torch.int32, device=dev)
         self.slot_token = torch.empty(P, dtype=torch.int32, device=dev)
@@ -144,18 +144,18 @@ class TrainableLayer:
         return y
 
     def backward(self, dy, stream=None):
-        """(dx through the experts [T, H], gradient of the routing weights [T, k]); fills grads."""
+        """(dx through the experts [T, H], gradient of the routing weights [T, k]), both new tensors; fills grads."""
         if self.x is None:
             raise RuntimeError("backward needs a forward pass on this batch size")
         _need("dy", dy, self.dtype, (self.T, self.H))
-        dx = _result(dy, stream)
-        N.moe_combine_backward(self.shapes[0], dy, self.y[0], self.pair_slot, self.w, self.dy_perm, self.dw, stream)
+        dx, dw = _result(dy, stream), _result(self.w, stream)
+        N.moe_combine_backward(self.shapes[0], dy, self.y[0], self.pair_slot, self.w, self.dy_perm, dw, stream)
         groups = [(self.off, self.slot_token, self.dy_perm), (None, None, dy)]
         for shape, (off, slot, d), w, pre, out, grads in zip(self.shapes, groups, self.weights, self.pre, self.dx, self.grads):
             N.moe_gated_ffn_backward(shape, self.x, off, slot, w, *pre, d, out, grads, self.ws, stream)
         N.moe_combine(self.shapes[0], self.dx[0], self.pair_slot, self.ones, self.dx[1] if len(self.dx) > 1 else None, dx,
                       stream)
-        return dx, self.dw
+        return dx, dw
 
     def step(self, lr, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.0, stream=None, **more):
         """One AdamW step of every expert matrix by grads; more: moe_adamw's lr_dev, step_dev, grad_scale, seed."""

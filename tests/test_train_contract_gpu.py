@@ -3,6 +3,8 @@ import pytest
 import torch
 
 from expert_ffn_layer_amd import native as N
+from expert_ffn_layer_amd.layer import TrainableLayer
+from inputgen import layers as L
 
 from _gpu import say
 from _train import DT
@@ -47,3 +49,39 @@ def test_adamw_8_bit_states_keep_every_nan(g, word):
         assert torch.equal(is_nan_code(m), at) and torch.equal(is_nan_code(v), at), step
         assert torch.equal(torch.isnan(p), at), step
         assert torch.isfinite(ms).all() and torch.isfinite(vs).all()
+
+
+# ------------------------------------------------------------------------------------------------
+# the layer
+
+SPEC = L.LayerSpec("train-contract", T=100, H=512, E=8, k=3, I=256, shared=True, seed=62)
+
+
+def build_layer(spec=SPEC, seed=1, **kw):
+    gen, dtype = gen_of(seed), DT[spec.act]
+    H, I, E = spec.H, spec.I, spec.E
+
+    def mats(*lead):
+        return {"gate": normal(gen, (*lead, H, I), dtype, H ** -0.5), "up": normal(gen, (*lead, H, I), dtype, H ** -0.5),
+                "down": normal(gen, (*lead, I, H), dtype, I ** -0.5)}
+    Wr = normal(gen, (H, E), dtype, H ** -0.5)
+    return TrainableLayer(spec, Wr, mats(E), mats() if spec.shared else None, **kw)
+
+
+def batch(spec, seed, T=None):
+    gen = gen_of(seed)
+    return [normal(gen, (spec.T if T is None else T, spec.H), DT[spec.act]) for _ in range(2)]
+
+
+def test_layer_results_outlive_the_next_batch():
+    say("results")
+    lay = build_layer()
+    kept, copies = [], []
+    for seed in range(3):
+        x, dy = batch(SPEC, seed)
+        y = lay.forward(x)
+        out = (y, *lay.backward(dy))
+        kept.append(out)
+        copies.append([t.clone() for t in out])
+    for out, want in zip(kept, copies):
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
