@@ -63,9 +63,13 @@ def _need(name: str, t: torch.Tensor, dtype, *shapes):
 
 
 def _result(like: torch.Tensor, stream):
-    t = torch.empty_like(like)
-    if stream is not None:
-        t.record_stream(stream)  # its memory is not handed on before this stream's work on it has ended
+    """A tensor that `stream` writes and the current stream may go on with: memory of the one, kept until work of the
+    other on it has ended too."""
+    if stream is None:
+        return torch.empty_like(like)
+    with torch.cuda.stream(stream):
+        t = torch.empty_like(like)
+    t.record_stream(torch.cuda.current_stream(like.device))
     return t
 
 
@@ -75,9 +79,10 @@ class TrainableLayer:
     with one of 1). The router is read only; its scores' gradient follows from backward's routing-weight
     gradient. Allocation and marshalling only, like PackedLayer.
 
-    forward keeps what backward reads (x itself, not a copy), for the last batch alone. Calls and set_tokens on one
-    stream follow each other; from another stream they have to wait for the former ones. state: "f32", or "e4m3" for 8-bit
-    optimizer states; master: fp32 master copies of bf16 weights."""
+    forward keeps what backward reads (x itself, not a copy), for the last batch alone. Calls, set_tokens and the
+    constructor on one stream follow each other; a call on another stream has to wait for the former ones. No memory that a
+    call works on (arguments, the layer's own and results) is handed on before that work has ended, whatever its stream.
+    state: "f32", or "e4m3" for 8-bit optimizer states; master: fp32 master copies of bf16 weights."""
 
     NAMES = ("gate", "up", "down")
 
@@ -112,8 +117,12 @@ class TrainableLayer:
     def _shape(self, T, E, k):
         return N.make_shape(T, self.H, E, k, self.I, act=self.act, w_routed=self.act)
 
-    def set_tokens(self, T: int):
-        """Buffers for batches of T tokens."""
+    def set_tokens(self, T: int, stream=None):
+        """Buffers for batches of T tokens, made on `stream`."""
+        with torch.cuda.stream(stream):
+            self._set_tokens(T)
+
+    def _set_tokens(self, T: int):
         dev, P, act = self.Wr.device, T * self.k, dict(dtype=self.dtype, device=self.Wr.device)
         self.T = T
         self.shapes = [self._shape(T, self.E, self.k)] + [self._shape(T, 1, 1)] * (len(self.weights) - 1)
@@ -129,10 +138,24 @@ class TrainableLayer:
         self.y, self.dx = ([torch.empty((r, self.H), **act) for r in rows] for _ in range(2))
         self.dy_perm = torch.empty((P, self.H), **act)
         self.x = None
+        self.streams = set()  # those that the allocator knows to work on the layer's memory
+
+    def _work_on(self, stream, *tensors):
+        """Has the allocator keep tensors, and once per stream everything of the layer, until this call's work has ended."""
+        stream = torch.cuda.current_stream(self.Wr.device) if stream is None else stream
+        if stream.cuda_stream not in self.streams:
+            self.streams.add(stream.cuda_stream)
+            tensors += (self.Wr, self.ws, self.idx, self.pair_slot, self.w, self.ones, self.off, self.slot_token, self.dy_perm,
+                        *self.y, *self.dx, *[t for pair in self.pre for t in pair],
+                        *[t for x in self.optimizer.keep if x is not None for t in x])
+        for t in tensors:
+            if torch.is_tensor(t):
+                t.record_stream(stream)
 
     def forward(self, x, bias=None, stream=None):
         """y [T, H]; routing as moe_route, kept in idx and w."""
         _need("x", x, self.dtype, (self.T, self.H))
+        self._work_on(stream, x, bias)
         y = _result(x, stream)
         N.moe_route_permute(self.shapes[0], x, self.Wr, bias, self.idx, self.w, self.off, self.slot_token,
                             self.pair_slot, self.ws, stream)
@@ -148,6 +171,7 @@ class TrainableLayer:
         if self.x is None:
             raise RuntimeError("backward needs a forward pass on this batch size")
         _need("dy", dy, self.dtype, (self.T, self.H))
+        self._work_on(stream, self.x, dy)
         dx, dw = _result(dy, stream), _result(self.w, stream)
         N.moe_combine_backward(self.shapes[0], dy, self.y[0], self.pair_slot, self.w, self.dy_perm, dw, stream)
         groups = [(self.off, self.slot_token, self.dy_perm), (None, None, dy)]
@@ -159,5 +183,6 @@ class TrainableLayer:
 
     def step(self, lr, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.0, stream=None, **more):
         """One AdamW step of every expert matrix by grads; more: moe_adamw's lr_dev, step_dev, grad_scale, seed."""
+        self._work_on(stream, *more.values())
         self.steps += 1
         N.moe_adamw(self.optimizer, lr, beta1, beta2, eps, weight_decay, self.steps, stream=stream, **more)

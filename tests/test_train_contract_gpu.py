@@ -85,3 +85,72 @@ def test_layer_results_outlive_the_next_batch():
         copies.append([t.clone() for t in out])
     for out, want in zip(kept, copies):
         assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def busy(stream):
+    """Some 20 ms of other work on the stream, so that what follows waits behind it."""
+    a = torch.ones((8192, 8192), dtype=torch.bfloat16, device=DEV)
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        for _ in range(20):
+            b = a @ a
+    return a, b
+
+
+def overwrite(like):
+    """New tensors of the current stream in the place of freed ones of the same sizes."""
+    return [torch.full(shape, 3.0, dtype=dtype, device=DEV) for shape, dtype in like for _ in range(3)]
+
+
+@pytest.mark.parametrize("given", [True, False])
+@pytest.mark.parametrize("what", ["set_tokens", "next batch", "layer"])
+def test_memory_stays_until_its_stream_is_through(what, given):
+    """What a call on a side stream still has to read is dropped, and memory of those sizes written, without a host
+    synchronisation; given: the stream as an argument, otherwise as the current one."""
+    say("memory", what, given)
+    want_layer, lay = build_layer(), build_layer()
+    x, dy = batch(SPEC, 5)
+    want = [want_layer.forward(x), *want_layer.backward(dy)]
+    want_layer.step(1e-3)
+    want += [t.clone() for t in want_layer.optimizer.keep[0]]
+    sizes = [(t.shape, t.dtype) for t in (x, lay.ws, lay.idx, lay.w, lay.off, lay.slot_token, lay.dy_perm, *lay.y, *lay.dx,
+                                         *lay.pre[0], *lay.optimizer.keep[1], *lay.optimizer.keep[2])]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    kept = busy(side)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(None if given else side):
+        kw = dict(stream=side) if given else {}
+        got = [lay.forward(x, **kw), *lay.backward(dy, **kw)]
+        lay.step(1e-3, **kw)
+        got += lay.optimizer.keep[0]
+        if what == "next batch":
+            lay.forward(dy, **kw)
+    del x, dy
+    if what == "set_tokens":
+        lay.set_tokens(SPEC.T)
+    elif what == "layer":
+        del lay
+    new = overwrite(sizes)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all((t == 3).all() for t in new)
+    del kept
+
+
+def test_set_tokens_on_a_stream():
+    """Buffers made and filled on the stream that uses them, behind other work there."""
+    say("set_tokens on a stream")
+    want_layer, lay = build_layer(), build_layer()
+    T = 57
+    x, dy = batch(SPEC, 7, T)
+    want_layer.set_tokens(T)
+    want = [want_layer.forward(x), *want_layer.backward(dy)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    kept = busy(side)
+    lay.set_tokens(T, stream=side)
+    got = [lay.forward(x, stream=side), *lay.backward(dy, stream=side)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    del kept
