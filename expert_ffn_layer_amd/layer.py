@@ -57,9 +57,11 @@ class PackedLayer:
         return y
 
 
-def _need(name: str, t: torch.Tensor, dtype, *shapes):
+def _need(name: str, t: torch.Tensor, dtype, *shapes, device=None):
     if tuple(t.shape) not in shapes or t.dtype != dtype or not t.is_contiguous():
         raise ValueError("%s: a contiguous %s tensor of %s is needed" % (name, dtype, " or ".join(map(str, shapes))))
+    if device is not None and (t.device != device or not t.is_cuda):
+        raise ValueError("%s: a tensor on the layer's GPU is needed" % name)
 
 
 def _result(like: torch.Tensor, stream):
@@ -90,15 +92,17 @@ class TrainableLayer:
                  state: str = "f32", master: bool = False):
         self.H, self.I, self.E, self.k, self.act = spec.H, spec.I, spec.E, spec.k, spec.act
         self.dtype = torch.float32 if spec.act == "f32" else torch.bfloat16
+        H, E, dev = spec.H, spec.E, Wr.device
+        _need("Wr", Wr, self.dtype, (H, E), (1, H, E), device=dev)
         for d, lead in ((routed, [(spec.E,)]), (shared, [(), (1,)])):
             for n in self.NAMES if d is not None else ():
                 size = (spec.I, spec.H) if n == "down" else (spec.H, spec.I)
-                _need(n, d[n], self.dtype, *[a + size for a in lead])
+                _need(n, d[n], self.dtype, *[a + size for a in lead], device=dev)
         self.weights = [{n: routed[n] for n in self.NAMES}]
         if shared is not None:
             self.weights.append({n: shared[n] for n in self.NAMES})
         self.grads = [{n: torch.zeros_like(t) for n, t in w.items()} for w in self.weights]
-        self.Wr, _ = pack(spec.act, Wr.reshape(1, spec.H, spec.E), None, spec.H, spec.E)
+        self.Wr, _ = pack(spec.act, Wr.reshape(1, H, E), None, H, E)
         p = [w[n] for w in self.weights for n in self.NAMES]
         g = [d[n] for d in self.grads for n in self.NAMES]
         if state == "e4m3":
@@ -154,7 +158,9 @@ class TrainableLayer:
 
     def forward(self, x, bias=None, stream=None):
         """y [T, H]; routing as moe_route, kept in idx and w."""
-        _need("x", x, self.dtype, (self.T, self.H))
+        _need("x", x, self.dtype, (self.T, self.H), device=self.Wr.device)
+        if bias is not None:
+            _need("bias", bias, torch.float32, (self.E,), device=self.Wr.device)
         self._work_on(stream, x, bias)
         y = _result(x, stream)
         N.moe_route_permute(self.shapes[0], x, self.Wr, bias, self.idx, self.w, self.off, self.slot_token,
@@ -170,7 +176,7 @@ class TrainableLayer:
         """(dx through the experts [T, H], gradient of the routing weights [T, k]), both new tensors; fills grads."""
         if self.x is None:
             raise RuntimeError("backward needs a forward pass on this batch size")
-        _need("dy", dy, self.dtype, (self.T, self.H))
+        _need("dy", dy, self.dtype, (self.T, self.H), device=self.Wr.device)
         self._work_on(stream, self.x, dy)
         dx, dw = _result(dy, stream), _result(self.w, stream)
         N.moe_combine_backward(self.shapes[0], dy, self.y[0], self.pair_slot, self.w, self.dy_perm, dw, stream)
