@@ -34,7 +34,8 @@ class PackedLayer:
         self.spec = spec
         self.shape = N.shape_from_spec(spec, T, path)
         H, I, E = spec.H, spec.I, spec.E
-        self.Wr, _ = pack(spec.act, Wr.reshape(1, H, E), None, H, E)
+        with torch.cuda.device(dev):
+            self.Wr, _ = pack(spec.act, Wr.reshape(1, H, E), None, H, E)
         self.routed = pack_expert_set(routed, spec.w_routed, H, I)
         self.shared = pack_expert_set(shared, spec.w_shared, H, I) if spec.shared else None
         self.ws = torch.empty(N.moe_workspace_size(self.shape), dtype=torch.uint8, device=Wr.device)
@@ -102,7 +103,8 @@ class TrainableLayer:
         if shared is not None:
             self.weights.append({n: shared[n] for n in self.NAMES})
         self.grads = [{n: torch.zeros_like(t) for n, t in w.items()} for w in self.weights]
-        self.Wr, _ = pack(spec.act, Wr.reshape(1, H, E), None, H, E)
+        with torch.cuda.device(dev):
+            self.Wr, _ = pack(spec.act, Wr.reshape(1, H, E), None, H, E)
         p = [w[n] for w in self.weights for n in self.NAMES]
         g = [d[n] for d in self.grads for n in self.NAMES]
         if state == "e4m3":
@@ -147,6 +149,8 @@ class TrainableLayer:
     def _work_on(self, stream, *tensors):
         """Has the allocator keep tensors, and once per stream everything of the layer, until this call's work has ended."""
         stream = torch.cuda.current_stream(self.Wr.device) if stream is None else stream
+        if stream.device != self.Wr.device:
+            raise ValueError("stream: one of the layer's GPU is needed")
         if stream.cuda_stream not in self.streams:
             self.streams.add(stream.cuda_stream)
             tensors += (self.Wr, self.ws, self.idx, self.pair_slot, self.w, self.ones, self.off, self.slot_token, self.dy_perm,
@@ -163,12 +167,13 @@ class TrainableLayer:
             _need("bias", bias, torch.float32, (self.E,), device=self.Wr.device)
         self._work_on(stream, x, bias)
         y = _result(x, stream)
-        N.moe_route_permute(self.shapes[0], x, self.Wr, bias, self.idx, self.w, self.off, self.slot_token,
-                            self.pair_slot, self.ws, stream)
-        groups = [(self.off, self.slot_token), (None, None)]
-        for shape, group, w, pre, out in zip(self.shapes, groups, self.weights, self.pre, self.y):
-            N.moe_gated_ffn(shape, x, *group, w, *pre, out, self.ws, stream)
-        N.moe_combine(self.shapes[0], self.y[0], self.pair_slot, self.w, self.y[1] if len(self.y) > 1 else None, y, stream)
+        with torch.cuda.device(self.Wr.device):
+            N.moe_route_permute(self.shapes[0], x, self.Wr, bias, self.idx, self.w, self.off, self.slot_token,
+                                self.pair_slot, self.ws, stream)
+            groups = [(self.off, self.slot_token), (None, None)]
+            for shape, group, w, pre, out in zip(self.shapes, groups, self.weights, self.pre, self.y):
+                N.moe_gated_ffn(shape, x, *group, w, *pre, out, self.ws, stream)
+            N.moe_combine(self.shapes[0], self.y[0], self.pair_slot, self.w, self.y[1] if len(self.y) > 1 else None, y, stream)
         self.x = x
         return y
 
@@ -179,12 +184,13 @@ class TrainableLayer:
         _need("dy", dy, self.dtype, (self.T, self.H), device=self.Wr.device)
         self._work_on(stream, self.x, dy)
         dx, dw = _result(dy, stream), _result(self.w, stream)
-        N.moe_combine_backward(self.shapes[0], dy, self.y[0], self.pair_slot, self.w, self.dy_perm, dw, stream)
-        groups = [(self.off, self.slot_token, self.dy_perm), (None, None, dy)]
-        for shape, (off, slot, d), w, pre, out, grads in zip(self.shapes, groups, self.weights, self.pre, self.dx, self.grads):
-            N.moe_gated_ffn_backward(shape, self.x, off, slot, w, *pre, d, out, grads, self.ws, stream)
-        N.moe_combine(self.shapes[0], self.dx[0], self.pair_slot, self.ones, self.dx[1] if len(self.dx) > 1 else None, dx,
-                      stream)
+        with torch.cuda.device(self.Wr.device):
+            N.moe_combine_backward(self.shapes[0], dy, self.y[0], self.pair_slot, self.w, self.dy_perm, dw, stream)
+            groups = [(self.off, self.slot_token, self.dy_perm), (None, None, dy)]
+            for shape, (off, slot, d), w, pre, out, grads in zip(self.shapes, groups, self.weights, self.pre, self.dx, self.grads):
+                N.moe_gated_ffn_backward(shape, self.x, off, slot, w, *pre, d, out, grads, self.ws, stream)
+            N.moe_combine(self.shapes[0], self.dx[0], self.pair_slot, self.ones, self.dx[1] if len(self.dx) > 1 else None, dx,
+                          stream)
         return dx, dw
 
     def step(self, lr, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.0, stream=None, **more):

@@ -125,6 +125,8 @@ def _run(tensors, stream, call):
     stream belong to it. The first tensor is not None."""
     import torch
     i = tensors[0].get_device()
+    if stream is not None and stream.device.index != i:
+        raise ValueError("the stream of a call is one of its tensors' GPU")
     at = []
     for t in tensors:
         if t is None:

@@ -1,10 +1,11 @@
 """What TrainableLayer and the training entry points refuse before any launch (no GPU)."""
+import contextlib
 import types
 
 import pytest
 import torch
 
-from expert_ffn_layer_amd import layer
+from expert_ffn_layer_amd import layer, native as N
 from inputgen import layers as L
 
 SPEC = L.LayerSpec("train-refusals", T=8, H=256, E=4, k=2, I=128, act="f32", w_routed="f32", w_shared="f32", seed=1)
@@ -47,3 +48,39 @@ def test_layer_refuses_a_bias_of_another_size_or_type():
     for bad in (torch.zeros(2), torch.zeros(3, dtype=torch.bfloat16), torch.zeros(6)[::2]):
         with pytest.raises(ValueError, match="bias"):
             lay.forward(good, bad)
+
+
+def test_a_stream_of_another_gpu_is_refused():
+    tensor = types.SimpleNamespace(get_device=lambda: 0, data_ptr=lambda: 16)
+    stream = types.SimpleNamespace(device=torch.device("cuda:1"), cuda_stream=1)
+    with pytest.raises(ValueError, match="stream"):
+        N._run((tensor,), stream, lambda at, st: 0)
+    lay = layer.TrainableLayer.__new__(layer.TrainableLayer)
+    lay.Wr, lay.streams = types.SimpleNamespace(device=torch.device("cuda:0")), set()
+    with pytest.raises(ValueError, match="stream"):
+        lay._work_on(stream)
+
+
+def test_layer_calls_with_its_own_gpu_as_the_current_one(monkeypatch):
+    """Every call of the library is made under the layer's GPU, whichever one is current."""
+    current, calls = ["cuda:0"], []
+
+    @contextlib.contextmanager
+    def device(d):
+        before, current[0] = current[0], d
+        yield
+        current[0] = before
+    monkeypatch.setattr(torch.cuda, "device", device)
+    names = ("moe_route_permute", "moe_gated_ffn", "moe_combine", "moe_combine_backward", "moe_gated_ffn_backward")
+    for name in names:
+        monkeypatch.setattr(N, name, lambda *a, name=name: calls.append((name, current[0])))
+    monkeypatch.setattr(layer, "_need", lambda *a, **kw: None)
+    monkeypatch.setattr(layer, "_result", lambda *a: None)
+    lay = layer.TrainableLayer.__new__(layer.TrainableLayer)
+    for n in "T H E dtype w idx off slot_token pair_slot ws ones dy_perm".split():
+        setattr(lay, n, None)
+    lay.Wr, lay._work_on = types.SimpleNamespace(device="cuda:1"), lambda *a: None
+    lay.shapes, lay.weights, lay.y, lay.dx, lay.grads, lay.pre = [1, 2], [{}, {}], [1, 2], [1, 2], [{}, {}], [[1, 1], [2, 2]]
+    lay.forward("x")
+    lay.backward("dy")
+    assert {n for n, _ in calls} == set(names) and {d for _, d in calls} == {"cuda:1"}
