@@ -84,12 +84,14 @@ hipError_t product(TrainForm form, int act, const TrainArgs& a, hipStream_t st) 
   return act == MOE_F32 ? launch_train_f32(form, a, st) : launch_train_bf16(form, a, st);
 }
 
-// No two of the updated arrays share memory: two workgroups would read and write it.
-moe_status check_apart(const moe_adamw_tensor* t, int count, size_t p_bytes, size_t state_bytes) {
+// No two of the updated arrays share memory, and none holds an input: two workgroups would reach it in no order.
+moe_status check_apart(const moe_adamw_config* c, const moe_adamw_tensor* t, int count) {
+  const bool q8 = c->state == MOE_ADAM_E4M3;
+  const size_t p_bytes = c->p_type == MOE_F32 ? 4 : 2, g_bytes = c->g_type == MOE_F32 ? 4 : 2, state_bytes = q8 ? 1 : 4;
   struct Range {
     uintptr_t at, end;
   };
-  Range* r = new (std::nothrow) Range[4 * (size_t)count];
+  Range* r = new (std::nothrow) Range[6 * (size_t)count];
   if (!r) return fail(MOE_ERR_INVALID_ARG, "no host memory to check %d tensors", count);
   size_t n = 0;
   auto add = [&](const void* p, size_t bytes) {
@@ -97,16 +99,31 @@ moe_status check_apart(const moe_adamw_tensor* t, int count, size_t p_bytes, siz
   };
   for (int i = 0; i < count; ++i) {
     if (!t[i].n) continue;
-    add(t[i].p, (size_t)t[i].n * p_bytes);
-    add(t[i].m, (size_t)t[i].n * state_bytes);
-    add(t[i].v, (size_t)t[i].n * state_bytes);
-    add(t[i].master, (size_t)t[i].n * 4);
+    const size_t each = (size_t)t[i].n;
+    add(t[i].p, each * p_bytes);
+    add(t[i].m, each * state_bytes);
+    add(t[i].v, each * state_bytes);
+    add(t[i].master, each * 4);
+    if (q8) {
+      add(t[i].m_scale, (each + 255) / 256 * 4);
+      add(t[i].v_scale, (each + 255) / 256 * 4);
+    }
   }
   std::sort(r, r + n, [](const Range& x, const Range& y) { return x.at < y.at; });
   bool apart = true;
   for (size_t i = 1; i < n; ++i) apart = apart && r[i - 1].end <= r[i].at;
+  // whether an input is apart from all of them: the first that ends behind its start starts behind its end
+  auto outside = [&](const void* p, size_t bytes) {
+    if (!p) return true;
+    const Range* const q = std::upper_bound(r, r + n, (uintptr_t)p, [](uintptr_t at, const Range& x) { return at < x.end; });
+    return q == r + n || (uintptr_t)p + bytes <= q->at;
+  };
+  bool inputs = true;
+  for (int i = 0; apart && i < count; ++i) inputs = inputs && (!t[i].n || outside(t[i].g, (size_t)t[i].n * g_bytes));
+  if (apart) inputs = inputs && outside(c->lr_dev, 4) && outside(c->step_dev, 8) && outside(c->grad_scale, 4);
   delete[] r;
-  return apart ? MOE_OK : fail(MOE_ERR_INVALID_ARG, "parameters, states or master copies overlap");
+  if (!apart) return fail(MOE_ERR_INVALID_ARG, "parameters, states, scales or master copies overlap");
+  return inputs ? MOE_OK : fail(MOE_ERR_INVALID_ARG, "a gradient or device value overlaps an updated array");
 }
 
 }  // namespace
@@ -236,7 +253,7 @@ moe_status moe_adamw(const moe_adamw_config* c, const moe_adamw_tensor* tensors,
   }
   if (master < 0) return MOE_OK;  // only empty tensors
   if (master && c->p_type == MOE_F32) return fail(MOE_ERR_INVALID_ARG, "F32 parameters take no master copy");
-  const moe_status s = check_apart(tensors, count, c->p_type == MOE_F32 ? 4 : 2, q8 ? 1 : 4);
+  const moe_status s = check_apart(c, tensors, count);
   if (s != MOE_OK) return s;
 
   AdamArgs a{};

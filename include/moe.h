@@ -466,7 +466,8 @@ moe_status moe_combine_backward(const moe_shape* shape, const void* dy, const vo
  * moe_adamw_tensor: device pointers of one tensor of n >= 0 consecutive elements; p, g, m, v and
  * master 16-byte, scales 4-byte aligned. master float[n]: the fp32 copy that is updated, p then its
  * rounding to bf16 (p_type MOE_BF16; every tensor has one or none has). No two of all tensors' p,
- * m, v, master and scales may share memory. g is only read.
+ * m, v, master and scales may share memory. g is only read; it and the device values below must not
+ * overlap any of those, but tensors may share a g.
  * moe_adamw_config: lr_dev, step_dev and grad_scale (device, each may be NULL) are read by the kernel
  * in place of lr, step and 1, so that a captured call follows them; step_dev below 1 counts as 1.
  * lr, eps, weight_decay >= 0; beta1, beta2 in [0, 1); step >= 1. Non-finite gradients reach p, m

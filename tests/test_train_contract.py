@@ -1,5 +1,6 @@
 """What TrainableLayer and the training entry points refuse before any launch (no GPU)."""
 import contextlib
+import ctypes
 import types
 
 import pytest
@@ -84,3 +85,39 @@ def test_layer_calls_with_its_own_gpu_as_the_current_one(monkeypatch):
     lay.forward("x")
     lay.backward("dy")
     assert {n for n, _ in calls} == set(names) and {d for _, d in calls} == {"cuda:1"}
+
+
+# ------------------------------------------------------------------------------------------------
+# arrays that overlap; addresses are never read
+
+def adamw(*tensors, state=0, p_type=1, g_type=1, **kw):
+    c = N.MoeAdamwConfig(p_type=p_type, g_type=g_type, state=state, lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, step=1, **kw)
+    arr = (N.MoeAdamwTensor * len(tensors))(*[N.MoeAdamwTensor(**t) for t in tensors])
+    rc = N.load().moe_adamw(ctypes.byref(c), arr, len(tensors), None)
+    return rc, N.load().moe_last_error().decode()
+
+
+def tensor(at, n=600, q8=False, **kw):
+    t = dict(p=at, g=at + 0x1000, m=at + 0x2000, v=at + 0x3000, n=n)
+    if q8:
+        t |= dict(m_scale=at + 0x4000, v_scale=at + 0x5000)
+    return t | kw
+
+
+# 600 elements take 1200 bytes of bf16, 2400 of fp32, 600 of codes and 12 of scales
+@pytest.mark.parametrize("state,other", [
+    (1, dict(v_scale=0x24000)), (1, dict(v_scale=0x24008)), (1, dict(m_scale=0x23FF8, v_scale=0x24000)),
+    (1, dict(m_scale=0x14000)), (1, dict(v_scale=0x14008)), (1, dict(m_scale=0x15004)), (1, dict(m_scale=0x12254)),
+    (1, dict(p=0x14000)), (1, dict(m=0x15000)),
+    (0, dict(g=0x20000)), (0, dict(g=0x22000)), (0, dict(g=0x10000)), (0, dict(g=0x104A0)), (0, dict(g=0x0FFF0)),
+    (0, dict(g=0x12950)), (0, dict(g=0x13000)), (1, dict(g=0x14000)), (1, dict(g=0x14FF0))])
+def test_adamw_refuses_overlapping_arrays(state, other):
+    q8 = state == 1
+    rc, text = adamw(tensor(0x10000, q8=q8), tensor(0x20000, q8=q8, **other), state=state)
+    assert rc == 1 and "overlap" in text
+
+
+@pytest.mark.parametrize("kw", [dict(lr_dev=0x10010), dict(step_dev=0x12000), dict(grad_scale=0x12950), dict(step_dev=0x104A8)])
+def test_adamw_refuses_device_values_inside_updated_arrays(kw):
+    rc, text = adamw(tensor(0x10000), **kw)
+    assert rc == 1 and "overlap" in text

@@ -51,6 +51,34 @@ def test_adamw_8_bit_states_keep_every_nan(g, word):
         assert torch.isfinite(ms).all() and torch.isfinite(vs).all()
 
 
+@pytest.mark.parametrize("q8", [False, True])
+def test_adamw_takes_arrays_side_by_side(q8):
+    """All arrays of two tensors packed without a gap, and one gradient for both: the same bits as apart."""
+    say("packed arrays", q8)
+    n, size = 512, torch.uint8 if q8 else torch.float32
+
+    def run(packed):
+        block = torch.zeros(64 * 1024, dtype=torch.uint8, device=DEV)
+        at = [0]
+
+        def take(count, dtype):
+            b = count * torch.empty(0, dtype=dtype).element_size()
+            if not packed:
+                return torch.zeros(count, dtype=dtype, device=DEV)
+            t = block[at[0]:at[0] + b].view(dtype)
+            at[0] += b
+            return t
+        p, m, v = [take(n, torch.bfloat16) for _ in range(2)], [take(n, size) for _ in range(2)], [take(n, size) for _ in range(2)]
+        ms, vs = ([take(n // 256, torch.float32) for _ in range(2)] for _ in range(2)) if q8 else (None, None)
+        g = take(n, torch.bfloat16)
+        g.copy_(normal(gen_of(4), (n,), torch.bfloat16))
+        for i in range(2):
+            p[i].copy_(normal(gen_of(i), (n,), torch.bfloat16))
+        N.moe_adamw(N.adamw_tensors(p, [g, g], m, v, None, ms, vs), lr=1e-2, step=1)
+        return [t.clone() for t in (*p, *m, *v, *(ms or []), *(vs or []))]
+    assert all(torch.equal(a, b) for a, b in zip(run(True), run(False)))
+
+
 # ------------------------------------------------------------------------------------------------
 # the layer
 
