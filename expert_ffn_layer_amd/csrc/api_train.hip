@@ -40,6 +40,21 @@ TrainWs train_ws(const moe_shape& s) {
   return w;
 }
 
+// Bytes of the block's arguments: x, rows of H and of I, a weight matrix of every expert, the indices, the workspace
+struct Sizes {
+  size_t x, h, i, w, off, slot, ws;
+  Sizes(const moe_shape& s, int xrows) {
+    const size_t b = s.act == MOE_F32 ? 4 : 2, P = (size_t)s.T * s.k;
+    x = (size_t)xrows * s.H * b;
+    h = P * s.H * b;
+    i = P * s.I * b;
+    w = (size_t)s.E * s.H * s.I * b;
+    off = ((size_t)s.E + 1) * 4;
+    slot = P * 4;
+    ws = train_ws(s).total;
+  }
+};
+
 // Checks common to the block and its gradient, and the arguments they share.
 moe_status train_args(const moe_shape* s, const void* x, const int32_t* off, const int32_t* slot_token,
                       const moe_weights* w, void* ws, size_t ws_bytes, TrainArgs* a) {
@@ -75,9 +90,23 @@ moe_status train_args(const moe_shape* s, const void* x, const int32_t* off, con
   return MOE_OK;
 }
 
-// Whether p is one of the others (NULL is nobody's)
-bool among(const void* p, std::initializer_list<const void*> others) {
-  return p && std::find(others.begin(), others.end(), p) != others.end();
+// Memory of an argument; none where it is NULL
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  return a.p && b.p && a.bytes && b.bytes && (uintptr_t)a.p < (uintptr_t)b.p + b.bytes && (uintptr_t)b.p < (uintptr_t)a.p + a.bytes;
+}
+// No output shares memory with an input or another output, the workspace being one of them.
+moe_status check_outputs(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
+  for (const Span* o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const Span* other = o + 1; other != outputs.end(); ++other)
+      if (overlap(*o, *other)) return fail(MOE_ERR_INVALID_ARG, "two outputs, or an output and the workspace, share memory");
+    for (const Span& in : inputs)
+      if (overlap(*o, in)) return fail(MOE_ERR_INVALID_ARG, "an output or the workspace shares memory with an input");
+  }
+  return MOE_OK;
 }
 
 hipError_t product(TrainForm form, int act, const TrainArgs& a, hipStream_t st) {
@@ -142,15 +171,17 @@ moe_status moe_gated_ffn(const moe_shape* shape, const void* x, const int32_t* e
                          const moe_weights* weights, void* gate_pre, void* up_pre, void* y_perm, void* ws,
                          size_t ws_bytes, moe_stream_t stream) {
   TrainArgs a;
-  const moe_status s = train_args(shape, x, expert_offsets, slot_token, weights, ws, ws_bytes, &a);
+  moe_status s = train_args(shape, x, expert_offsets, slot_token, weights, ws, ws_bytes, &a);
   if (s != MOE_OK) return s;
   if (!gate_pre != !up_pre) return fail(MOE_ERR_INVALID_ARG, "gate_pre and up_pre are kept both or not at all");
   if (!al16(gate_pre) || !al16(up_pre) || !al16(y_perm))
     return fail(MOE_ERR_INVALID_ARG, "gate_pre, up_pre and y_perm must be 16-byte aligned");
   if (a.P == 0) return MOE_OK;
   if (!y_perm) return fail(MOE_ERR_INVALID_ARG, "y_perm is NULL");
-  if (among(gate_pre, {up_pre, y_perm, x}) || among(up_pre, {y_perm, x}) || y_perm == x)
-    return fail(MOE_ERR_INVALID_ARG, "an output is an input's or another output's memory");
+  const Sizes z(*shape, a.xrows);
+  s = check_outputs({{gate_pre, z.i}, {up_pre, z.i}, {y_perm, z.h}, {ws, z.ws}},
+                    {{x, z.x}, {expert_offsets, z.off}, {slot_token, z.slot}, {weights->gate, z.w}, {weights->up, z.w}, {weights->down, z.w}});
+  if (s != MOE_OK) return s;
   a.g = gate_pre;
   a.u = up_pre;
   a.y = y_perm;
@@ -165,7 +196,7 @@ moe_status moe_gated_ffn_backward(const moe_shape* shape, const void* x, const i
                                   const void* up_pre, const void* dy_perm, void* dx_perm, const moe_weight_grads* grads,
                                   void* ws, size_t ws_bytes, moe_stream_t stream) {
   TrainArgs a;
-  const moe_status s = train_args(shape, x, expert_offsets, slot_token, weights, ws, ws_bytes, &a);
+  moe_status s = train_args(shape, x, expert_offsets, slot_token, weights, ws, ws_bytes, &a);
   if (s != MOE_OK) return s;
   if (!dx_perm && !grads) return fail(MOE_ERR_INVALID_ARG, "neither dx_perm nor grads is asked for");
   if (grads && (!grads->gate || !grads->up || !grads->down)) return fail(MOE_ERR_INVALID_ARG, "gradient pointer is NULL");
@@ -173,12 +204,12 @@ moe_status moe_gated_ffn_backward(const moe_shape* shape, const void* x, const i
   if (!al16(gate_pre) || !al16(up_pre) || !al16(dy_perm) || !al16(dx_perm) ||
       (grads && (!al16(grads->gate) || !al16(grads->up) || !al16(grads->down))))
     return fail(MOE_ERR_INVALID_ARG, "pre-activations and gradients must be 16-byte aligned");
-  const std::initializer_list<const void*> inputs = {x, gate_pre, up_pre, dy_perm, weights->gate, weights->up, weights->down};
-  if (among(dx_perm, inputs) ||
-      (grads && (among(grads->gate, inputs) || among(grads->up, inputs) || among(grads->down, inputs) ||
-                 among(grads->gate, {grads->up, grads->down, dx_perm}) || among(grads->up, {grads->down, dx_perm}) ||
-                 grads->down == dx_perm)))
-    return fail(MOE_ERR_INVALID_ARG, "an output is an input's or another output's memory");
+  const Sizes z(*shape, a.xrows);
+  s = check_outputs({{dx_perm, z.h}, {grads ? grads->gate : nullptr, z.w}, {grads ? grads->up : nullptr, z.w},
+                     {grads ? grads->down : nullptr, z.w}, {ws, z.ws}},
+                    {{x, z.x}, {expert_offsets, z.off}, {slot_token, z.slot}, {weights->gate, z.w}, {weights->up, z.w},
+                     {weights->down, z.w}, {gate_pre, z.i}, {up_pre, z.i}, {dy_perm, z.h}});
+  if (s != MOE_OK) return s;
   a.g = const_cast<void*>(gate_pre);
   a.u = const_cast<void*>(up_pre);
   a.dy = dy_perm;
@@ -208,7 +239,7 @@ moe_status moe_gated_ffn_backward(const moe_shape* shape, const void* x, const i
 
 moe_status moe_combine_backward(const moe_shape* shape, const void* dy, const void* y_perm, const int32_t* pair_slot,
                                 const float* topk_w, void* dy_perm, float* dtopk_w, moe_stream_t stream) {
-  const moe_status s = check_shape(shape);
+  moe_status s = check_shape(shape);
   if (s != MOE_OK) return s;
   if (!al16(dy) || !al16(y_perm) || !al16(dy_perm))
     return fail(MOE_ERR_INVALID_ARG, "dy, y_perm and dy_perm must be 16-byte aligned");
@@ -216,7 +247,11 @@ moe_status moe_combine_backward(const moe_shape* shape, const void* dy, const vo
     return fail(MOE_ERR_INVALID_ARG, "index and routing-weight arrays must be 4-byte aligned");
   if (shape->T == 0) return MOE_OK;
   if (!dy || !y_perm || !pair_slot || !topk_w || !dy_perm || !dtopk_w) return fail(MOE_ERR_INVALID_ARG, "NULL pointer");
-  if (dy_perm == y_perm || dy_perm == dy) return fail(MOE_ERR_INVALID_ARG, "dy_perm must not be an input's memory");
+  const size_t P = (size_t)shape->T * shape->k, row = (size_t)shape->H * (shape->act == MOE_F32 ? 4 : 2);
+  // a pair's weight is read before its gradient is written, so the gradient may take its place
+  s = check_outputs({{dy_perm, P * row}, {dtopk_w, P * 4}},
+                    {{dy, shape->T * row}, {y_perm, P * row}, {pair_slot, P * 4}, {topk_w == dtopk_w ? nullptr : topk_w, P * 4}});
+  if (s != MOE_OK) return s;
   return hip_status(launch_combine_backward(shape->act, dy, y_perm, pair_slot, topk_w, dy_perm, dtopk_w, shape->T,
                                             shape->H, shape->k, (hipStream_t)stream),
                     "combine gradient");

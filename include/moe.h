@@ -401,8 +401,8 @@ moe_status moe_train_workspace_size(const moe_shape* shape, size_t* bytes);
  *   gate_pre, up_pre [T*k][I] act out: g and u (both, or both NULL: not kept)
  *   y_perm           [T*k][H] act out
  * h is formed from the unrounded g and u and kept in `ws` in the act type. Rows from
- * expert_offsets[E] on are not written. T == 0 enqueues nothing. Outputs must not overlap x or each
- * other.
+ * expert_offsets[E] on are not written. T == 0 enqueues nothing. Outputs and ws must not overlap inputs
+ * or each other.
  */
 moe_status moe_gated_ffn(const moe_shape* shape, const void* x, const int32_t* expert_offsets,
                          const int32_t* slot_token, const moe_weights* weights, void* gate_pre,
@@ -426,8 +426,8 @@ typedef struct {
  *            written. moe_combine with weights 1 sums the rows of each token.
  *   grads    out, or NULL: not computed. Every element is written; an expert without rows has
  *            gradient 0 (with T == 0 all have).
- * h, dg and du are kept in `ws` in the act type. Outputs must not overlap inputs or each other. The same bits on
- * every run: no atomics.
+ * h, dg and du are kept in `ws` in the act type. Outputs and ws must not overlap inputs or each other.
+ * The same bits on every run: no atomics.
  */
 moe_status moe_gated_ffn_backward(const moe_shape* shape, const void* x,
                                   const int32_t* expert_offsets, const int32_t* slot_token,
@@ -441,8 +441,9 @@ moe_status moe_gated_ffn_backward(const moe_shape* shape, const void* x,
  *   dy_perm[pair_slot[t*k+j]] = topk_w[t][j] * dy[t], dtopk_w[t][j] = dy[t] . y_perm[pair_slot[t*k+j]]
  *   dy       [T][H] act (also the gradient of y_shared)
  *   y_perm, pair_slot, topk_w   moe_combine's inputs; the slots of different pairs differ
- *   dy_perm  [T*k][H] act out; rows that no pair names are not written. Not the memory of dy or y_perm.
+ *   dy_perm  [T*k][H] act out; rows that no pair names are not written
  *   dtopk_w  float[T][k] out, summed in fp32; 0 for a pair whose pair_slot is outside [0, T*k)
+ * Outputs must not overlap inputs or each other, but dtopk_w may be topk_w.
  */
 moe_status moe_combine_backward(const moe_shape* shape, const void* dy, const void* y_perm,
                                 const int32_t* pair_slot, const float* topk_w, void* dy_perm,

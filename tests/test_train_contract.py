@@ -121,3 +121,56 @@ def test_adamw_refuses_overlapping_arrays(state, other):
 def test_adamw_refuses_device_values_inside_updated_arrays(kw):
     rc, text = adamw(tensor(0x10000), **kw)
     assert rc == 1 and "overlap" in text
+
+
+P = ctypes.c_void_p
+# T 4, k 2, E 2, H 256, I 128 in bf16: x 2048 bytes, rows of H 4096, of I 2048, a weight 131072, offsets 12, slots 32,
+# workspace under 0x10000
+BLOCK = dict(x=0x100000, off=0x110000, slot=0x120000, gate=0x200000, up=0x300000, down=0x400000, g=0x500000, u=0x510000,
+             dy=0x520000, y=0x600000, dgate=0x700000, dup=0x800000, ddown=0x900000, ws=0xA00000)
+
+
+def block(gradient, **kw):
+    a = BLOCK | kw
+    s = N.make_shape(4, 256, 2, 2, 128)
+    w = N.MoeWeights(a["gate"], a["up"], a["down"], None, None, None)
+    ws, size = P(a["ws"]), N.moe_train_workspace_size(s)
+    assert size < 0x10000
+    if gradient:
+        grads = N.MoeWeightGrads(a["dgate"], a["dup"], a["ddown"])
+        rc = N.load().moe_gated_ffn_backward(ctypes.byref(s), P(a["x"]), P(a["off"]), P(a["slot"]), ctypes.byref(w), P(a["g"]),
+                                             P(a["u"]), P(a["dy"]), P(a["y"]), ctypes.byref(grads), ws, size, None)
+    else:
+        rc = N.load().moe_gated_ffn(ctypes.byref(s), P(a["x"]), P(a["off"]), P(a["slot"]), ctypes.byref(w), P(a["g"]), P(a["u"]),
+                                    P(a["y"]), ws, size, None)
+    return rc, N.load().moe_last_error().decode()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(u=0x5007F0), dict(g=0x5107F0), dict(y=0x5007F0), dict(y=0x4FF010), dict(y=0x1007F0), dict(y=0x21FFF0), dict(y=0x300000),
+    dict(g=0x41FFF0), dict(g=0x400000), dict(y=0x10FFF0), dict(y=0x11F010), dict(y=0xA00000), dict(g=0xA00800), dict(u=0x9FF810),
+    dict(ws=0x300000), dict(ws=0x5FFF00), dict(ws=0x100700), dict(ws=0x110000)])
+def test_block_refuses_overlapping_outputs(kw):
+    rc, text = block(False, **kw)
+    assert rc == 1 and "memory" in text
+
+
+@pytest.mark.parametrize("kw", [
+    dict(y=0x520FF0), dict(y=0x51F010), dict(y=0x5007F0), dict(y=0x1007F0), dict(y=0x21FFF0), dict(dgate=0x4E0010),
+    dict(dup=0x71FFF0), dict(ddown=0x7E0010), dict(dgate=0x5FFFF0), dict(dup=0x520FF0), dict(ddown=0x3FFFF0),
+    dict(dgate=0x0E0010), dict(dup=0x110000), dict(dgate=0xA00000), dict(y=0xA00800), dict(ws=0x900000), dict(ws=0x500700),
+    dict(ws=0x120000), dict(ws=0x200000)])
+def test_block_gradient_refuses_overlapping_outputs(kw):
+    rc, text = block(True, **kw)
+    assert rc == 1 and "memory" in text
+
+
+# T 4, k 2, H 256 in bf16: dy 2048 bytes, rows 4096, slots and weights 32
+@pytest.mark.parametrize("kw", [
+    dict(rows=0x200FF0), dict(rows=0x1FF010), dict(rows=0x1007F0), dict(rows=0x2FFFF0), dict(rows=0x400010 - 0x1000), dict(dw=0x2007F0),
+    dict(dw=0x100000), dict(dw=0x300010), dict(dw=0x40001C), dict(dw=0x3FFFE4), dict(dw=0x500FF0)])
+def test_combine_gradient_refuses_overlapping_outputs(kw):
+    a = dict(dy=0x100000, y=0x200000, slot=0x300000, w=0x400000, rows=0x500000, dw=0x600000) | kw
+    s = N.make_shape(4, 256, 2, 2, 128)
+    rc = N.load().moe_combine_backward(ctypes.byref(s), *[P(v) for v in a.values()], None)
+    assert rc == 1 and "memory" in N.load().moe_last_error().decode()

@@ -182,3 +182,53 @@ def test_set_tokens_on_a_stream():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     del kept
+
+
+# ------------------------------------------------------------------------------------------------
+# arguments side by side
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_block_takes_arguments_side_by_side(act):
+    """Every argument of the block and its gradient packed without a gap: the same bits as apart; and the combine's
+    gradient with the routing weights' in their place."""
+    say("packed block", act)
+    T, H, I, E, k = 24, 256, 128, 3, 2
+    P, dtype = T * k, DT[act]
+    shape = N.make_shape(T, H, E, k, I, act=act, w_routed=act)
+    size = N.moe_train_workspace_size(shape)
+
+    def run(packed):
+        gen, at = gen_of(8), [0]
+        memory = torch.zeros(8 << 20, dtype=torch.uint8, device=DEV)
+
+        def take(*dims, dtype=dtype):
+            n = torch.Size(dims).numel()
+            b = n * torch.empty(0, dtype=dtype).element_size()
+            if not packed:
+                return torch.zeros(dims, dtype=dtype, device=DEV)
+            t = memory[at[0]:at[0] + b].view(dtype).view(dims)
+            at[0] += b
+            return t
+
+        def filled(*dims):
+            return take(*dims).copy_(normal(gen, dims, dtype))
+        ws = take(size, dtype=torch.uint8)
+        x, g, u, y = filled(T, H), take(P, I), take(P, I), take(P, H)
+        w = {"gate": filled(E, H, I), "up": filled(E, H, I), "down": filled(E, I, H)}
+        grads = {n: take(*t.shape) for n, t in w.items()}
+        dy, dx, rows = filled(T, H), take(P, H), take(P, H)
+        tw, dw = take(T, k, dtype=torch.float32), take(T, k, dtype=torch.float32)
+        tw.copy_(torch.rand((T, k), generator=gen, device=DEV))
+        slot, pair = take(P, dtype=torch.int32), take(P, dtype=torch.int32)
+        slot.copy_(torch.arange(P, device=DEV, dtype=torch.int32) % T)
+        pair.copy_(torch.randperm(P, generator=gen, device=DEV))
+        off = take(E + 1, dtype=torch.int32)
+        off.copy_(torch.tensor([0, 20, 20, P]))
+        N.moe_gated_ffn(shape, x, off, slot, w, g, u, y, ws)
+        if packed:
+            N.moe_combine_backward(shape, dy, y, pair, tw, rows, tw)
+        else:
+            N.moe_combine_backward(shape, dy, y, pair, tw, rows, dw)
+        N.moe_gated_ffn_backward(shape, x, off, slot, w, g, u, rows, dx, grads, ws)
+        return [t.clone() for t in (g, u, y, rows, tw if packed else dw, dx, *grads.values())]
+    assert all(torch.equal(a, b) for a, b in zip(run(True), run(False)))
