@@ -7,10 +7,11 @@
 namespace moe {
 
 constexpr int GTHR = 256;
+constexpr long long GRID_X = 1 << 23;  // workgroups along x: a grid's dimension ends before 2^32 threads
 
 __global__ void __launch_bounds__(GTHR) gather_rows_kernel(const u32x4* __restrict__ x, const int32_t* __restrict__ token,
                                                           u32x4* __restrict__ out, int P, int xrows, int cpr) {
-  const long long id = (long long)blockIdx.x * GTHR + threadIdx.x;
+  const long long id = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * GTHR + threadIdx.x;
   if (id >= (long long)P * cpr) return;
   const int r = (int)(id / cpr), c = (int)(id - (long long)r * cpr), s = token[r];
   u32x4 v = {0u, 0u, 0u, 0u};
@@ -21,7 +22,8 @@ __global__ void __launch_bounds__(GTHR) gather_rows_kernel(const u32x4* __restri
 hipError_t launch_gather_rows(const TrainArgs& a, hipStream_t st) {
   const int cpr = a.H / 8;
   if (a.P == 0) return hipSuccess;
-  const unsigned grid = (unsigned)(((long long)a.P * cpr + GTHR - 1) / GTHR);
+  const long long groups = ((long long)a.P * cpr + GTHR - 1) / GTHR;
+  const dim3 grid((unsigned)(groups < GRID_X ? groups : GRID_X), (unsigned)((groups + GRID_X - 1) / GRID_X));
   gather_rows_kernel<<<grid, GTHR, 0, st>>>((const u32x4*)a.x, a.slot_token, (u32x4*)a.xg, a.P, a.xrows, cpr);
   return hipGetLastError();
 }

@@ -7,7 +7,7 @@ from expert_ffn_layer_amd.layer import TrainableLayer
 from inputgen import layers as L
 
 from _gpu import say
-from _train import DT
+from _train import DT, backward, check
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
@@ -232,3 +232,44 @@ def test_block_takes_arguments_side_by_side(act):
         N.moe_gated_ffn_backward(shape, x, off, slot, w, g, u, rows, dx, grads, ws)
         return [t.clone() for t in (g, u, y, rows, tw if packed else dw, dx, *grads.values())]
     assert all(torch.equal(a, b) for a, b in zip(run(True), run(False)))
+
+
+# ------------------------------------------------------------------------------------------------
+# large calls
+
+@pytest.mark.slow
+def test_gradient_of_the_most_rows():
+    """The most rows that a call takes, of a width that puts P H / 8, the threads of the gathering of x, past 2^32: the
+    gradients of the last rows, which a group of their own holds, against their definition."""
+    T, k, E, H, I, last = 262140, 16, 16, 8320, 128, 75
+    P = T * k
+    assert P == 65535 * 64 and P * H // 8 > 1 << 32
+    torch.cuda.empty_cache()
+    shape = N.make_shape(T, H, E, k, I)
+    size = N.moe_train_workspace_size(shape)
+    if torch.cuda.mem_get_info()[0] < size + P * H * 2 + (20 << 30):
+        pytest.skip("needs 150 GB of GPU memory")
+    say("most rows", P, H)
+    gen = gen_of(3)
+    x = normal(gen, (T, H), torch.bfloat16)
+    w = {"gate": normal(gen, (E, H, I), torch.bfloat16, H ** -0.5), "up": normal(gen, (E, H, I), torch.bfloat16, H ** -0.5),
+         "down": normal(gen, (E, I, H), torch.bfloat16, I ** -0.5)}
+    g, u = (torch.zeros((P, I), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    dy = torch.zeros((P, H), dtype=torch.bfloat16, device=DEV)
+    for t, n in ((g, I), (u, I), (dy, H)):
+        t[P - last:] = normal(gen, (last, n), torch.bfloat16)
+    slot = torch.arange(P, dtype=torch.int32, device=DEV) % T
+    off = torch.full((E + 1,), P - last, dtype=torch.int32, device=DEV)
+    off[0], off[E] = 0, P
+    grads = {n: torch.full_like(t, 5.0) for n, t in w.items()}
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+    N.moe_gated_ffn_backward(shape, x, off, slot, w, g, u, dy, None, grads, ws)
+    torch.cuda.synchronize()
+    assert all((t[:E - 1] == 0).all() for t in grads.values())
+    rows = x[slot[P - last:].long()].double()
+    mats = [w[n][E - 1].double() for n in ("gate", "up", "down")]
+    want = backward(rows, *mats, g[P - last:].double(), u[P - last:].double(), dy[P - last:].double(), torch.bfloat16)
+    for n in ("gate", "up", "down"):
+        check("d" + n, grads[n][E - 1], *want["d" + n])
+    del ws, dy, g, u, x
+    torch.cuda.empty_cache()
