@@ -162,8 +162,9 @@ __device__ __forceinline__ void tile(const TrainArgs& a, int bx, int by, int bz,
     fetch_tokens(k0 + AHEAD * TK, set);
   };
 
-  // A round's sums are added to the total at its end: the error of a product stays at that of a chain of 128
-  // additions (3.6 2^-24 of its norm at K = 2048 and at 640)
+  // A round's sums are added to the total at its end. On values of random sign the error of a product of K elements is
+  // 0.43 sqrt(64 + K / 256) 2^-24 of its norm, where one chain's is 0.43 sqrt(K / 2): measured 3.5 2^-24 at K = 640,
+  // 4.1 at 7168, 5.2 at 20000 and 10.6 at 140000, which only the weight gradients of a large group reach
   f32x4 acc[2][RT], total[2][RT];
 #pragma unroll
   for (int t = 0; t < 2; ++t)

@@ -72,3 +72,12 @@ def layout(counts, T, gen, device):
     off[1:] = c.cumsum(0)
     slot = torch.randint(0, max(T, 1), (int(c.sum()),), generator=gen, dtype=torch.int32)
     return off.to(device), slot.to(device)
+
+
+def chain_error(*lengths):
+    """Relative Frobenius error of fp32 products of random signs chained one after the other (a product of the given
+    reduction length each, whose operand is the one before), summed in rounds of 128 elements whose sums are added to
+    a total. One addition rounds by 0.42 2^-24 of its result on average (uniform within half a step, the mantissa
+    logarithmic), taken as 0.5; the partial sums of n terms have the mean square n / 2 of the whole's, so a round
+    contributes 64 such squares, the total's K / 128 additions K / 256, and one more rounding forms an operand."""
+    return 0.5 * A * sum(64 + n / 256 + 1 for n in lengths) ** 0.5

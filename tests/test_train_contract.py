@@ -3,11 +3,14 @@ import contextlib
 import ctypes
 import types
 
+import numpy as np
 import pytest
 import torch
 
 from expert_ffn_layer_amd import layer, native as N
 from inputgen import layers as L
+
+from _train import chain_error
 
 SPEC = L.LayerSpec("train-refusals", T=8, H=256, E=4, k=2, I=128, act="f32", w_routed="f32", w_shared="f32", seed=1)
 
@@ -174,3 +177,32 @@ def test_combine_gradient_refuses_overlapping_outputs(kw):
     s = N.make_shape(4, 256, 2, 2, 128)
     rc = N.load().moe_combine_backward(ctypes.byref(s), *[P(v) for v in a.values()], None)
     assert rc == 1 and "memory" in N.load().moe_last_error().decode()
+
+
+# ------------------------------------------------------------------------------------------------
+# the bound on the error of fp32 products, against sums made in other ways
+
+def summed(a, b, round_length):
+    """a [K, m], b [K, n]: sum_k a[k, :, None] b[k, None, :], each addition rounded to fp32, sums of round_length
+    elements added to a total."""
+    total = np.zeros((a.shape[1], b.shape[1]), np.float32)
+    for k0 in range(0, len(a), round_length):
+        acc = np.zeros_like(total)
+        for k in range(k0, min(k0 + round_length, len(a))):
+            acc = (acc + np.outer(a[k].astype(np.float64), b[k])).astype(np.float32)
+        total = total + acc
+    return total
+
+
+@pytest.mark.parametrize("K", [4096, 20000])
+def test_error_bound_tells_the_ways_of_summing_apart(K):
+    rng = np.random.default_rng(K)
+    a, b = (rng.standard_normal((K, 24)).astype(np.float32) for _ in range(2))
+    want = a.astype(np.float64).T @ b
+
+    def far(x):
+        return np.linalg.norm(x - want) / np.linalg.norm(want)
+    half = [torch.from_numpy(t).bfloat16().float().numpy() for t in (a, b)]
+    assert far(summed(a, b, 128)) <= chain_error(K)
+    assert far(summed(a, b, K)) > chain_error(K)           # one chain
+    assert far(summed(*half, 128)) > 100 * chain_error(K)  # bf16 operands

@@ -7,7 +7,7 @@ from expert_ffn_layer_amd.layer import TrainableLayer
 from inputgen import layers as L
 
 from _gpu import say
-from _train import DT, backward, check
+from _train import DT, backward, chain_error, check
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
@@ -182,6 +182,88 @@ def test_set_tokens_on_a_stream():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     del kept
+
+
+# ------------------------------------------------------------------------------------------------
+# the error of the fp32 products. Gates of 32 and more make the sigmoid 1 in fp32, so that what goes into a product is
+# known to a rounding.
+
+def far(got, want):
+    return ((got.double() - want).norm() / want.norm()).item()
+
+
+def f32_block(T, H, I, seed):
+    gen = gen_of(seed)
+    shape = N.make_shape(T, H, 1, 1, I, act="f32", w_routed="f32")
+    w = {"gate": normal(gen, (1, H, I), torch.float32), "up": normal(gen, (1, H, I), torch.float32),
+         "down": normal(gen, (1, I, H), torch.float32)}
+    return gen, shape, w, torch.empty(N.moe_train_workspace_size(shape), dtype=torch.uint8, device=DEV)
+
+
+@pytest.mark.parametrize("H,T", [(640, 100), (7168, 100), (7168, 2000)])
+def test_f32_error_of_gate_and_up(H, T):
+    say("f32 gate/up", H, T)
+    gen, shape, w, ws = f32_block(T, H, 128, 31)
+    x = normal(gen, (T, H), torch.float32)
+    g, u, y = (torch.empty((T, n), device=DEV) for n in (128, 128, H))
+    N.moe_gated_ffn(shape, x, None, None, w, g, u, y, ws)
+    for got, name in ((g, "gate"), (u, "up")):
+        error = far(got, x.double() @ w[name][0].double())
+        say(name, error / 2.0 ** -24)
+        assert error <= chain_error(H)
+
+
+@pytest.mark.parametrize("I,T", [(640, 128), (8192, 128), (8192, 2048)])
+def test_f32_error_of_down(I, T):
+    """Each row of x picks a row of the weights, so g and u are exact and h has one rounding."""
+    say("f32 down", I, T)
+    H = 128
+    gen, shape, w, ws = f32_block(T, H, I, 32)
+    w["gate"] = torch.rand((1, H, I), generator=gen, device=DEV) * 32 + 32
+    pick = torch.arange(T, device=DEV) % H
+    x = torch.eye(H, device=DEV)[pick].contiguous()
+    y = torch.empty((T, H), device=DEV)
+    N.moe_gated_ffn(shape, x, None, None, w, None, None, y, ws)
+    h = (w["gate"][0].double() * w["up"][0].double())[pick]
+    error = far(y, h @ w["down"][0].double())
+    say(error / 2.0 ** -24)
+    assert error <= chain_error(I)
+
+
+@pytest.mark.parametrize("I,T", [(384, 128), (4096, 128), (4096, 2048)])
+def test_f32_error_of_dx(I, T):
+    """Each row of dy picks a column of Wd, so dh is exact, du = 64 dh too, and dg = dh u has one rounding."""
+    say("f32 dx", I, T)
+    H = 128
+    gen, shape, w, ws = f32_block(T, H, I, 33)
+    pick = torch.arange(T, device=DEV) % H
+    dy = torch.eye(H, device=DEV)[pick].contiguous()
+    g, u = torch.full((T, I), 64.0, device=DEV), normal(gen, (T, I), torch.float32, 64.0)
+    x, dx = normal(gen, (T, H), torch.float32), torch.empty((T, H), device=DEV)
+    N.moe_gated_ffn_backward(shape, x, None, None, w, g, u, dy, dx, None, ws)
+    dh = w["down"][0].double().T[pick]
+    want = (dh * u.double()) @ w["gate"][0].double().T + (dh * 64) @ w["up"][0].double().T
+    error = far(dx, want)
+    say(error / 2.0 ** -24)
+    assert error <= chain_error(2 * I)
+
+
+@pytest.mark.parametrize("T", [1000, 20_000, 140_000])
+def test_f32_error_of_the_weight_gradients(T):
+    """h = 64 u is exact, du = 64 dh and dg = dh u are as far off as dh."""
+    say("f32 weight gradients", T)
+    H = I = 128
+    gen, shape, w, ws = f32_block(T, H, I, 34)
+    x, dy = normal(gen, (T, H), torch.float32), normal(gen, (T, H), torch.float32)
+    g, u = torch.full((T, I), 64.0, device=DEV), normal(gen, (T, I), torch.float32)
+    grads = {n: torch.empty_like(t) for n, t in w.items()}
+    N.moe_gated_ffn_backward(shape, x, None, None, w, g, u, dy, None, grads, ws)
+    dh = dy.double() @ w["down"][0].double().T
+    want = {"gate": x.double().T @ (dh * u.double()), "up": x.double().T @ (dh * 64), "down": (64 * u.double()).T @ dy.double()}
+    for name, bound in (("gate", chain_error(H, T)), ("up", chain_error(H, T)), ("down", chain_error(T))):
+        error = far(grads[name][0], want[name])
+        say(name, error / 2.0 ** -24)
+        assert error <= bound, name
 
 
 # ------------------------------------------------------------------------------------------------
