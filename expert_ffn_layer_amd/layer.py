@@ -196,5 +196,5 @@ class TrainableLayer:
     def step(self, lr, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.0, stream=None, **more):
         """One AdamW step of every expert matrix by grads; more: moe_adamw's lr_dev, step_dev, grad_scale, seed."""
         self._work_on(stream, *more.values())
+        N.moe_adamw(self.optimizer, lr, beta1, beta2, eps, weight_decay, self.steps + 1, stream=stream, **more)
         self.steps += 1
-        N.moe_adamw(self.optimizer, lr, beta1, beta2, eps, weight_decay, self.steps, stream=stream, **more)

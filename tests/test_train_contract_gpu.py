@@ -115,6 +115,23 @@ def test_layer_results_outlive_the_next_batch():
         assert all(torch.equal(a, b) for a, b in zip(out, want))
 
 
+def test_layer_counts_the_steps_it_made():
+    """A refused step is none: the next one is the first."""
+    say("refused step")
+    a, b = build_layer(), build_layer()
+    for lay in (a, b):
+        x, dy = batch(SPEC, 3)
+        lay.forward(x)
+        lay.backward(dy)
+    with pytest.raises(N.MoeError):
+        a.step(-1.0)
+    with pytest.raises(ValueError):
+        a.step(1e-3, step_dev=torch.ones(1, device=DEV))
+    a.step(1e-3)
+    b.step(1e-3)
+    assert a.steps == 1 and all(torch.equal(p, q) for p, q in zip(a.optimizer.keep[0], b.optimizer.keep[0]))
+
+
 def busy(stream):
     """Some 20 ms of other work on the stream, so that what follows waits behind it."""
     a = torch.ones((8192, 8192), dtype=torch.bfloat16, device=DEV)
