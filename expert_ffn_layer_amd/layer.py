@@ -167,6 +167,7 @@ class TrainableLayer:
             _need("bias", bias, torch.float32, (self.E,), device=self.Wr.device)
         self._work_on(stream, x, bias)
         y = _result(x, stream)
+        self.x = None  # until all that backward reads belongs to this batch
         with torch.cuda.device(self.Wr.device):
             N.moe_route_permute(self.shapes[0], x, self.Wr, bias, self.idx, self.w, self.off, self.slot_token,
                                 self.pair_slot, self.ws, stream)

@@ -90,6 +90,26 @@ def test_layer_calls_with_its_own_gpu_as_the_current_one(monkeypatch):
     assert {n for n, _ in calls} == set(names) and {d for _, d in calls} == {"cuda:1"}
 
 
+def test_a_failed_forward_leaves_nothing_to_go_back_through(monkeypatch):
+    """Part of what backward reads is the new batch's then, part the old one's."""
+    def failing(*a):
+        raise N.MoeError(4, "launch")
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(N, "moe_route_permute", lambda *a: None)
+    monkeypatch.setattr(N, "moe_gated_ffn", failing)
+    monkeypatch.setattr(layer, "_need", lambda *a, **kw: None)
+    monkeypatch.setattr(layer, "_result", lambda *a: None)
+    lay = layer.TrainableLayer.__new__(layer.TrainableLayer)
+    for n in "T H E dtype w idx off slot_token pair_slot ws".split():
+        setattr(lay, n, None)
+    lay.Wr, lay._work_on, lay.x = types.SimpleNamespace(device="cuda:0"), lambda *a: None, "the batch before"
+    lay.shapes, lay.weights, lay.y, lay.pre = [1], [{}], [1], [[1, 1]]
+    with pytest.raises(N.MoeError):
+        lay.forward("x")
+    with pytest.raises(RuntimeError):
+        lay.backward("dy")
+
+
 # ------------------------------------------------------------------------------------------------
 # arrays that overlap; addresses are never read
 
