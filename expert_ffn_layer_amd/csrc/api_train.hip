@@ -267,6 +267,8 @@ moe_status moe_adamw(const moe_adamw_config* c, const moe_adamw_tensor* tensors,
     return fail(MOE_ERR_INVALID_ARG, "beta1=%g, beta2=%g must be in [0, 1)", c->beta1, c->beta2);
   if (!(c->eps >= 0.0) || !(c->weight_decay >= 0.0) || (!c->lr_dev && !(c->lr >= 0.0)))
     return fail(MOE_ERR_INVALID_ARG, "lr=%g, eps=%g and weight_decay=%g must not be negative", c->lr, c->eps, c->weight_decay);
+  // the kernel's reciprocal takes smaller divisors for 0, and an element whose m and v are 0 would become NaN
+  if (c->eps > 0.0 && c->eps < 0x1p-126) return fail(MOE_ERR_INVALID_ARG, "eps=%g is neither 0 nor a normal fp32 number", c->eps);
   if (!c->step_dev && c->step < 1) return fail(MOE_ERR_INVALID_ARG, "step=%lld < 1", (long long)c->step);
   if (!al4(c->lr_dev) || !al4(c->grad_scale) || (uintptr_t)c->step_dev % 8)
     return fail(MOE_ERR_INVALID_ARG, "lr_dev and grad_scale must be 4-byte and step_dev 8-byte aligned");

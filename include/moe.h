@@ -471,7 +471,8 @@ moe_status moe_combine_backward(const moe_shape* shape, const void* dy, const vo
  * overlap any of those, but tensors may share a g.
  * moe_adamw_config: lr_dev, step_dev and grad_scale (device, each may be NULL) are read by the kernel
  * in place of lr, step and 1, so that a captured call follows them; step_dev below 1 counts as 1.
- * lr, eps, weight_decay >= 0; beta1, beta2 in [0, 1); step >= 1. Non-finite gradients reach p, m
+ * lr, eps, weight_decay >= 0, eps 0 or at least 2^-126 (with 0, an element whose m and v are 0 is 0 / 0);
+ * beta1, beta2 in [0, 1); step >= 1. Non-finite gradients reach p, m
  * and v as the formulas say; in the E4M3 form p, m and sqrt(v) become NaN where v is infinite, and the
  * other elements of its 256 are not affected. count == 0 enqueues nothing; both structs are host memory
  * read during the call.

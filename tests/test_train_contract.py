@@ -146,6 +146,13 @@ def test_adamw_refuses_device_values_inside_updated_arrays(kw):
     assert rc == 1 and "overlap" in text
 
 
+@pytest.mark.parametrize("eps", [2.0 ** -1074, 1e-44, 1e-39, 2.0 ** -127])
+def test_adamw_refuses_an_eps_below_the_normal_numbers(eps):
+    c = N.MoeAdamwConfig(p_type=1, g_type=1, state=0, lr=1e-3, beta1=0.9, beta2=0.95, eps=eps, step=1)
+    arr = (N.MoeAdamwTensor * 1)(N.MoeAdamwTensor(**tensor(0x10000)))
+    assert N.load().moe_adamw(ctypes.byref(c), arr, 1, None) == 1 and "eps" in N.load().moe_last_error().decode()
+
+
 P = ctypes.c_void_p
 # T 4, k 2, E 2, H 256, I 128 in bf16: x 2048 bytes, rows of H 4096, of I 2048, a weight 131072, offsets 12, slots 32,
 # workspace under 0x10000

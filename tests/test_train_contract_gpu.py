@@ -51,6 +51,26 @@ def test_adamw_8_bit_states_keep_every_nan(g, word):
         assert torch.isfinite(ms).all() and torch.isfinite(vs).all()
 
 
+@pytest.mark.parametrize("state", ["f32", "e4m3"])
+@pytest.mark.parametrize("eps", [1e-44, 1e-39, 2.0 ** -126])
+def test_adamw_smallest_eps(state, eps):
+    """Elements without gradient stay where they are by any eps that is accepted (0 / eps = 0); one that a reciprocal
+    in fp32 cannot take is refused."""
+    say("eps", state, eps)
+    n = 300
+    p, g = torch.ones(n, device=DEV), torch.zeros(n, device=DEV)
+    q8 = state == "e4m3"
+    m, v = (torch.zeros(n, dtype=torch.uint8 if q8 else torch.float32, device=DEV) for _ in range(2))
+    scales = [[torch.zeros(2, device=DEV)] for _ in range(2)] if q8 else [None, None]
+    table = N.adamw_tensors([p], [g], [m], [v], None, *scales)
+    if eps < 2.0 ** -126:
+        with pytest.raises(N.MoeError):
+            N.moe_adamw(table, lr=1e-3, eps=eps, step=1)
+    else:
+        N.moe_adamw(table, lr=1e-3, eps=eps, step=1)
+    assert (p == 1).all()
+
+
 @pytest.mark.parametrize("q8", [False, True])
 def test_adamw_takes_arrays_side_by_side(q8):
     """All arrays of two tensors packed without a gap, and one gradient for both: the same bits as apart."""
