@@ -133,9 +133,11 @@ def _run(tensors, stream, call):
             at.append(None)
         elif t.get_device() != i or i < 0:
             raise ValueError("the tensors of a call are on one GPU")
+        elif not t.is_contiguous():
+            raise ValueError("the tensors of a call are contiguous")
         else:
             at.append(t.data_ptr())
-    if i != torch.cuda.current_device():
+    if i != torch._C._cuda_getDevice():  # the current one
         with torch.cuda.device(i):
             rc = call(at, torch._C._cuda_getCurrentRawStream(i) if stream is None else stream.cuda_stream)
     else:

@@ -304,6 +304,49 @@ def test_f32_error_of_the_weight_gradients(T):
 
 
 # ------------------------------------------------------------------------------------------------
+# the binding
+
+def test_binding_refuses_strided_tensors():
+    """The library takes addresses, so a view of other strides would be read as another matrix."""
+    say("strides")
+    T, H, I = 8, 256, 128
+    shape = N.make_shape(T, H, 1, 1, I)
+    gen = gen_of(5)
+    b = {"x": normal(gen, (T, H), torch.bfloat16), "g": normal(gen, (T, I), torch.bfloat16), "u": normal(gen, (T, I), torch.bfloat16),
+         "dy": normal(gen, (T, H), torch.bfloat16), "y": torch.zeros((T, H), dtype=torch.bfloat16, device=DEV)}
+    w = {"gate": normal(gen, (1, H, I), torch.bfloat16), "up": normal(gen, (1, H, I), torch.bfloat16),
+         "down": normal(gen, (1, I, H), torch.bfloat16)}
+    grads = {n: torch.zeros_like(t) for n, t in w.items()}
+    ws = torch.empty(N.moe_train_workspace_size(shape), dtype=torch.uint8, device=DEV)
+
+    def turned(t):  # the same values under other strides
+        return t.transpose(-1, -2).contiguous().transpose(-1, -2)
+
+    def forward(b, w):
+        N.moe_gated_ffn(shape, b["x"], None, None, w, b["g"], b["u"], b["y"], ws)
+
+    def backward(b, w, grads=grads):
+        N.moe_gated_ffn_backward(shape, b["x"], None, None, w, b["g"], b["u"], b["dy"], b["y"], grads, ws)
+    forward(b, w)
+    backward(b, w)
+    for call, names in ((forward, "xguy"), (backward, ("x", "g", "u", "dy", "y"))):
+        for n in names:
+            with pytest.raises(ValueError):
+                call(b | {n: turned(b[n])}, w)
+        for n in w:
+            with pytest.raises(ValueError):
+                call(b, w | {n: turned(w[n])})
+    for n in w:
+        with pytest.raises(ValueError):
+            backward(b, w, grads | {n: turned(grads[n])})
+    slot, one = torch.zeros((T, 1), dtype=torch.int32, device=DEV), torch.ones((T, 1), device=DEV)
+    rows = torch.zeros_like(b["y"])
+    N.moe_combine_backward(shape, b["dy"], b["y"], slot, one, rows, torch.zeros_like(one))
+    with pytest.raises(ValueError):
+        N.moe_combine_backward(shape, turned(b["dy"]), b["y"], slot, one, rows, torch.zeros_like(one))
+
+
+# ------------------------------------------------------------------------------------------------
 # arguments side by side
 
 @pytest.mark.parametrize("act", ["f32", "bf16"])
