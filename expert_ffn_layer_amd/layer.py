@@ -130,7 +130,7 @@ class TrainableLayer:
 
     def _set_tokens(self, T: int):
         dev, P, act = self.Wr.device, T * self.k, dict(dtype=self.dtype, device=self.Wr.device)
-        self.T = T
+        self.T = self.x = None  # no batch fits until all buffers are there
         self.shapes = [self._shape(T, self.E, self.k)] + [self._shape(T, 1, 1)] * (len(self.weights) - 1)
         ws = max(N.moe_workspace_size(self.shapes[0]), *[N.moe_train_workspace_size(s) for s in self.shapes])
         self.ws = torch.empty(ws, dtype=torch.uint8, device=dev)
@@ -143,7 +143,7 @@ class TrainableLayer:
         self.pre = [[torch.empty((r, self.I), **act) for _ in range(2)] for r in rows]
         self.y, self.dx = ([torch.empty((r, self.H), **act) for r in rows] for _ in range(2))
         self.dy_perm = torch.empty((P, self.H), **act)
-        self.x = None
+        self.T = T
         self.streams = set()  # those that the allocator knows to work on the layer's memory
 
     def _work_on(self, stream, *tensors):

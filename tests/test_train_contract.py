@@ -110,6 +110,34 @@ def test_a_failed_forward_leaves_nothing_to_go_back_through(monkeypatch):
         lay.backward("dy")
 
 
+@pytest.mark.parametrize("fails_at", range(9))
+def test_a_failed_set_tokens_leaves_a_layer_that_takes_no_batch(monkeypatch, fails_at):
+    """Memory that runs out half way leaves buffers of two sizes, which no kernel may see."""
+    lay = layer.TrainableLayer.__new__(layer.TrainableLayer)
+    lay.H, lay.I, lay.E, lay.k, lay.act, lay.dtype, lay.weights = 256, 128, 4, 2, "f32", torch.float32, [{}]
+    lay.Wr = torch.zeros(4)
+    lay.set_tokens(4)
+    lay.x = torch.zeros(4, 256)
+    empty, left = torch.empty, [fails_at]
+
+    def failing(*a, **kw):
+        left[0] -= 1
+        if left[0] < 0:
+            raise MemoryError("no memory")
+        return empty(*a, **kw)
+    monkeypatch.setattr(torch, "empty", failing)
+    with pytest.raises(MemoryError):
+        lay.set_tokens(8)
+    monkeypatch.undo()
+    for T in (4, 8):
+        with pytest.raises(ValueError, match="x:"):
+            lay.forward(torch.zeros(T, 256))
+    with pytest.raises(RuntimeError):
+        lay.backward(torch.zeros(8, 256))
+    lay.set_tokens(8)
+    assert lay.T == 8 and lay.pre[0][0].shape == (16, 128)
+
+
 # ------------------------------------------------------------------------------------------------
 # arrays that overlap; addresses are never read
 
