@@ -34,8 +34,7 @@ class PackedLayer:
         self.spec = spec
         self.shape = N.shape_from_spec(spec, T, path)
         H, I, E = spec.H, spec.I, spec.E
-        with torch.cuda.device(dev):
-            self.Wr, _ = pack(spec.act, Wr.reshape(1, H, E), None, H, E)
+        self.Wr, _ = pack(spec.act, Wr.reshape(1, H, E), None, H, E)
         self.routed = pack_expert_set(routed, spec.w_routed, H, I)
         self.shared = pack_expert_set(shared, spec.w_shared, H, I) if spec.shared else None
         self.ws = torch.empty(N.moe_workspace_size(self.shape), dtype=torch.uint8, device=Wr.device)
