@@ -18,7 +18,9 @@ bool al4(const void* p) { return (uintptr_t)p % 4 == 0; }
 size_t up(size_t x) { return (x + WS_ALIGN - 1) / WS_ALIGN * WS_ALIGN; }
 
 moe_status check_train_shape(const moe_shape* s) {
-  const moe_status r = check_shape(s);
+  moe_shape any = s ? *s : moe_shape{};
+  any.path = MOE_PATH_AUTO;  // the path is the inference forward's
+  const moe_status r = check_shape(s ? &any : nullptr);
   if (r != MOE_OK) return r;
   if (s->w_routed != s->act)
     return fail(MOE_ERR_UNSUPPORTED, "training takes weights of the activations' type, F32 or BF16");

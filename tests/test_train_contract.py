@@ -234,6 +234,14 @@ def test_combine_gradient_refuses_overlapping_outputs(kw):
     assert rc == 1 and "memory" in N.load().moe_last_error().decode()
 
 
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_the_path_does_not_matter_to_training(act):
+    """H = 256 and I = 128 have no prefill kernel, nor have f32 weights: that is the inference forward's matter."""
+    sizes = {N.moe_train_workspace_size(N.make_shape(4, 256, 2, 2, 128, act=act, w_routed=act, path=path))
+             for path in ("auto", "decode", "prefill")}
+    assert len(sizes) == 1
+
+
 # ------------------------------------------------------------------------------------------------
 # the bound on the error of fp32 products, against sums made in other ways
 
