@@ -4,6 +4,8 @@ only; the computation is in the library's kernels.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import native as N
@@ -60,7 +62,7 @@ class PackedLayer:
 def _need(name: str, t: torch.Tensor, dtype, *shapes, device=None):
     if tuple(t.shape) not in shapes or t.dtype != dtype or not t.is_contiguous():
         raise ValueError("%s: a contiguous %s tensor of %s is needed" % (name, dtype, " or ".join(map(str, shapes))))
-    if device is not None and (t.device != device or not t.is_cuda):
+    if device is not None and not (t.is_cuda and t.device == device):
         raise ValueError("%s: a tensor on the layer's GPU is needed" % name)
 
 
@@ -143,31 +145,39 @@ class TrainableLayer:
         self.y, self.dx = ([torch.empty((r, self.H), **act) for r in rows] for _ in range(2))
         self.dy_perm = torch.empty((P, self.H), **act)
         self.T = T
-        self.streams = set()  # those that the allocator knows to work on the layer's memory
+        self.streams = {}  # by handle: those that the allocator knows to work on the layer's memory
+
+    def _gpu(self):
+        """The layer's GPU as the current one."""
+        return contextlib.nullcontext() if torch._C._cuda_getDevice() == self.Wr.get_device() else torch.cuda.device(self.Wr.device)
 
     def _work_on(self, stream, *tensors):
-        """Has the allocator keep tensors, and once per stream everything of the layer, until this call's work has ended."""
-        stream = torch.cuda.current_stream(self.Wr.device) if stream is None else stream
-        if stream.device != self.Wr.device:
+        """This call's stream, until whose work so far has ended the allocator keeps tensors and, from the first call on it
+        on, everything of the layer."""
+        if stream is not None and stream.device != self.Wr.device:
             raise ValueError("stream: one of the layer's GPU is needed")
-        if stream.cuda_stream not in self.streams:
-            self.streams.add(stream.cuda_stream)
+        handle = torch._C._cuda_getCurrentRawStream(self.Wr.get_device()) if stream is None else stream.cuda_stream
+        if handle in self.streams:
+            stream = self.streams[handle]
+        else:
+            stream = self.streams[handle] = torch.cuda.current_stream(self.Wr.device) if stream is None else stream
             tensors += (self.Wr, self.ws, self.idx, self.pair_slot, self.w, self.ones, self.off, self.slot_token, self.dy_perm,
                         *self.y, *self.dx, *[t for pair in self.pre for t in pair],
                         *[t for x in self.optimizer.keep if x is not None for t in x])
         for t in tensors:
-            if torch.is_tensor(t):
+            if torch.is_tensor(t) and t.is_cuda:
                 t.record_stream(stream)
+        return stream
 
     def forward(self, x, bias=None, stream=None):
         """y [T, H]; routing as moe_route, kept in idx and w."""
         _need("x", x, self.dtype, (self.T, self.H), device=self.Wr.device)
         if bias is not None:
             _need("bias", bias, torch.float32, (self.E,), device=self.Wr.device)
-        self._work_on(stream, x, bias)
         y = _result(x, stream)
+        stream = self._work_on(stream, x, bias)
         self.x = None  # until all that backward reads belongs to this batch
-        with torch.cuda.device(self.Wr.device):
+        with self._gpu():
             N.moe_route_permute(self.shapes[0], x, self.Wr, bias, self.idx, self.w, self.off, self.slot_token,
                                 self.pair_slot, self.ws, stream)
             groups = [(self.off, self.slot_token), (None, None)]
@@ -182,9 +192,9 @@ class TrainableLayer:
         if self.x is None:
             raise RuntimeError("backward needs a forward pass on this batch size")
         _need("dy", dy, self.dtype, (self.T, self.H), device=self.Wr.device)
-        self._work_on(stream, self.x, dy)
         dx, dw = _result(dy, stream), _result(self.w, stream)
-        with torch.cuda.device(self.Wr.device):
+        stream = self._work_on(stream, self.x, dy)
+        with self._gpu():
             N.moe_combine_backward(self.shapes[0], dy, self.y[0], self.pair_slot, self.w, self.dy_perm, dw, stream)
             groups = [(self.off, self.slot_token, self.dy_perm), (None, None, dy)]
             for shape, (off, slot, d), w, pre, out, grads in zip(self.shapes, groups, self.weights, self.pre, self.dx, self.grads):
@@ -195,6 +205,6 @@ class TrainableLayer:
 
     def step(self, lr, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.0, stream=None, **more):
         """One AdamW step of every expert matrix by grads; more: moe_adamw's lr_dev, step_dev, grad_scale, seed."""
-        self._work_on(stream, *more.values())
+        stream = self._work_on(stream, *more.values())
         N.moe_adamw(self.optimizer, lr, beta1, beta2, eps, weight_decay, self.steps + 1, stream=stream, **more)
         self.steps += 1

@@ -60,7 +60,7 @@ def test_a_stream_of_another_gpu_is_refused():
     with pytest.raises(ValueError, match="stream"):
         N._run((tensor,), stream, lambda at, st: 0)
     lay = layer.TrainableLayer.__new__(layer.TrainableLayer)
-    lay.Wr, lay.streams = types.SimpleNamespace(device=torch.device("cuda:0")), set()
+    lay.Wr, lay.streams = types.SimpleNamespace(device=torch.device("cuda:0")), {}
     with pytest.raises(ValueError, match="stream"):
         lay._work_on(stream)
 
@@ -75,6 +75,7 @@ def test_layer_calls_with_its_own_gpu_as_the_current_one(monkeypatch):
         yield
         current[0] = before
     monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
     names = ("moe_route_permute", "moe_gated_ffn", "moe_combine", "moe_combine_backward", "moe_gated_ffn_backward")
     for name in names:
         monkeypatch.setattr(N, name, lambda *a, name=name: calls.append((name, current[0])))
@@ -83,7 +84,7 @@ def test_layer_calls_with_its_own_gpu_as_the_current_one(monkeypatch):
     lay = layer.TrainableLayer.__new__(layer.TrainableLayer)
     for n in "T H E dtype w idx off slot_token pair_slot ws ones dy_perm".split():
         setattr(lay, n, None)
-    lay.Wr, lay._work_on = types.SimpleNamespace(device="cuda:1"), lambda *a: None
+    lay.Wr, lay._work_on = types.SimpleNamespace(device="cuda:1", get_device=lambda: 1), lambda *a: None
     lay.shapes, lay.weights, lay.y, lay.dx, lay.grads, lay.pre = [1, 2], [{}, {}], [1, 2], [1, 2], [{}, {}], [[1, 1], [2, 2]]
     lay.forward("x")
     lay.backward("dy")
@@ -94,7 +95,7 @@ def test_a_failed_forward_leaves_nothing_to_go_back_through(monkeypatch):
     """Part of what backward reads is the new batch's then, part the old one's."""
     def failing(*a):
         raise N.MoeError(4, "launch")
-    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(layer.TrainableLayer, "_gpu", lambda self: contextlib.nullcontext())
     monkeypatch.setattr(N, "moe_route_permute", lambda *a: None)
     monkeypatch.setattr(N, "moe_gated_ffn", failing)
     monkeypatch.setattr(layer, "_need", lambda *a, **kw: None)

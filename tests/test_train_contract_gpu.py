@@ -152,6 +152,15 @@ def test_layer_counts_the_steps_it_made():
     assert a.steps == 1 and all(torch.equal(p, q) for p, q in zip(a.optimizer.keep[0], b.optimizer.keep[0]))
 
 
+def test_layer_step_refuses_device_values_on_the_host():
+    say("host values")
+    lay = build_layer()
+    for kw in (dict(lr_dev=torch.ones(1)), dict(step_dev=torch.ones(1, dtype=torch.int64)), dict(grad_scale=torch.ones(1))):
+        with pytest.raises(ValueError):
+            lay.step(1e-3, **kw)
+    assert lay.steps == 0
+
+
 def busy(stream):
     """Some 20 ms of other work on the stream, so that what follows waits behind it."""
     a = torch.ones((8192, 8192), dtype=torch.bfloat16, device=DEV)
