@@ -106,7 +106,9 @@ __device__ __forceinline__ void decode(u32x2 c, float s, float (&v)[AV]) {
   }
 }
 // Random words of the 8-bit form: a multiply-xorshift hash of element index and key, the key one of
-// seed and step. m uses a word's upper 20 bits, the root its lower 20.
+// seed and step. m uses a word's upper 20 bits, the root its lower 20. The multipliers 0x9E3779B1 and 0x85EBCA77 are
+// the first two primes of XXH32, and the shifts of 15 and 13 with the second between them are the first half of its
+// final mix (Y. Collet's published xxHash specification).
 __device__ __forceinline__ uint32_t dither_key(uint32_t seed, uint32_t step) {
   uint32_t k = seed + step * 0x9E3779B9u;
   k = (k ^ (k >> 16)) * 0x85EBCA77u;

@@ -283,7 +283,8 @@ __device__ __forceinline__ void tile(const TrainArgs& a, int bx, int by, int bz,
   }
 }
 
-// 4 waves a SIMD, so 128 registers at most: 1 to 5% faster than 3 waves with some more registers
+// 4 waves a SIMD, so 128 registers at most: 1 to 5% faster than 3 waves with some more registers, although with tiles of
+// 64 rows dx then spills 3 registers, the weight gradients 10 and the launch of both 13 (10 with 32 rows)
 template <int FORM, int TM>
 __global__ void __launch_bounds__(TTHR, 4) train_f32_kernel(const TrainArgs a) {
   __shared__ __align__(16) float lds[LDS_FLOATS];
