@@ -9,6 +9,7 @@
 
 #include "api_util.h"
 #include "common.h"
+#include "gate.h"
 #include "kernels.h"
 
 using namespace moe;
@@ -307,13 +308,31 @@ moe_status do_scores(const moe_shape& s, const void* x, const void* Wr, void* ws
                     "router scores");
 }
 
-// moe_route (or moe_route_hash, with `hash`) without the argument checks.
+// The gate in place of the router's rule: logits (or NULL) receives the scores.
+struct GatedRoute {
+  const moe_gate_rule* rule;
+  float* logits;
+};
+
+// moe_route (or moe_route_hash, with `hash`, or moe_route_gated, with `gated`) without the argument checks.
 moe_status do_route(const moe_shape& s, const void* x, const void* Wr, const float* bias, int32_t* idx,
-                    float* w, void* ws, const Ws& L, hipStream_t st, const HashRoute* hash = nullptr) {
+                    float* w, void* ws, const Ws& L, hipStream_t st, const HashRoute* hash = nullptr,
+                    const GatedRoute* gated = nullptr) {
   if (s.T == 0) return MOE_OK;
   int ldl;
   moe_status rs = do_scores(s, x, Wr, ws, L, st, &ldl);
   if (rs != MOE_OK) return rs;
+  if (gated) {
+    GateArgs a = gate_args(s, *gated->rule);
+    a.logits = at<float>(ws, L.logits);
+    a.ldl = ldl;
+    a.nparts = router_plan(s).ksplit;
+    a.bias = bias;
+    a.sums = gated->logits;
+    a.idx = idx;
+    a.w = w;
+    return hip_status(launch_gate(a, st), "gate");
+  }
   hipError_t e = launch_topk(at<float>(ws, L.logits), ldl, router_plan(s).ksplit, bias, s.T, s.E, s.k,
                              hash ? hash->ids : nullptr, hash ? hash->table : nullptr, hash ? hash->vocab : 0, idx, w, st);
   return hip_status(e, hash ? "hash routing" : "router top-k");
@@ -373,12 +392,12 @@ moe_status record(hipEvent_t ev, hipStream_t st) {
 moe_status do_route_permute(const moe_shape& s, const void* x, const void* Wr, const float* bias, int32_t* idx,
                             float* w, int32_t* off, int32_t* slot_token, int32_t* pair_slot, void* ws, const Ws& L,
                             hipStream_t st, hipEvent_t const* ev, const HashRoute* hash, bool* planned,
-                            bool shared_in_plan = true) {
+                            bool shared_in_plan = true, const GatedRoute* gated = nullptr) {
   moe_status rs;
   *planned = false;
   if (s.T == 0) return do_permute(s, idx, off, slot_token, pair_slot, ws, L, st);
-  if (!use_fused_route(s)) {
-    if ((rs = do_route(s, x, Wr, bias, idx, w, ws, L, st, hash)) != MOE_OK) return rs;
+  if (gated || !use_fused_route(s)) {
+    if ((rs = do_route(s, x, Wr, bias, idx, w, ws, L, st, hash, gated)) != MOE_OK) return rs;
     if (ev && (rs = record(ev[1], st)) != MOE_OK) return rs;
     return do_permute(s, idx, off, slot_token, pair_slot, ws, L, st, true, planned, shared_in_plan);
   }
@@ -683,7 +702,7 @@ SideStream* side_of_current_device(hipStream_t stream, moe_status* st) {
 moe_status do_layer(const moe_shape* shape, const void* x, const void* Wr_packed, const float* bias,
                     const moe_weights* routed, const moe_weights* shared, void* y, int32_t* topk_idx_out,
                     float* topk_w_out, void* ws, size_t ws_bytes, hipStream_t st, hipEvent_t const* ev,
-                    const HashRoute* hash = nullptr, bool overlap = false) {
+                    const HashRoute* hash = nullptr, bool overlap = false, const GatedRoute* gated = nullptr) {
   moe_status s = check_shape(shape);
   if (s != MOE_OK) return s;
   if ((s = check_weights(routed, shape->w_routed, "routed")) != MOE_OK) return s;
@@ -718,7 +737,7 @@ moe_status do_layer(const moe_shape* shape, const void* x, const void* Wr_packed
   }
   bool planned = false;
   if ((s = do_route_permute(*shape, x, Wr_packed, bias, idx, w, off, slot_token, pair_slot, ws, L, st, ev, hash,
-                            &planned, !side)) != MOE_OK)
+                            &planned, !side, gated)) != MOE_OK)
     return s;
   if (ev && (s = record(ev[2], st)) != MOE_OK) return s;
   if ((s = do_ffn(*shape, x, off, slot_token, *routed, shared, y_perm, y_sh, ws, L, st, ev ? ev + 3 : nullptr,
@@ -1053,6 +1072,38 @@ moe_status moe_layer_forward_hash(const moe_shape* shape, const void* x, const v
   const HashRoute h{token_ids, hash_table, vocab};
   return do_layer(shape, x, Wr_packed, bias, routed, shared, y, topk_idx_out, topk_w_out, ws, ws_bytes,
                   (hipStream_t)stream, nullptr, &h, true);
+}
+
+moe_status moe_route_gated(const moe_shape* shape, const moe_gate_rule* rule, const void* x, const void* Wr_packed,
+                           const float* bias, float* logits, int32_t* topk_idx, float* topk_w, void* ws,
+                           size_t ws_bytes, moe_stream_t stream) {
+  moe_status s = check_shape(shape);
+  if (s != MOE_OK) return s;
+  if ((s = check_rule(*shape, rule)) != MOE_OK) return s;
+  if (shape->T && (!x || !Wr_packed || !topk_idx || !topk_w)) return fail(MOE_ERR_INVALID_ARG, "NULL pointer");
+  if (!al16(x) || !al16(Wr_packed)) return misaligned("x and Wr_packed", 16);
+  if (!al4(bias) || !al4(logits) || !al4(topk_idx) || !al4(topk_w)) return misaligned("bias, logits, topk_idx and topk_w", 4);
+  Ws L;
+  if ((s = check_ws(*shape, ws, ws_bytes, &L)) != MOE_OK) return s;
+  const size_t rows = (size_t)shape->T * 4;
+  s = check_outputs({{logits, rows * shape->E}, {topk_idx, rows * shape->k}, {topk_w, rows * shape->k}, {ws, L.total}},
+                    {{x, (size_t)shape->T * shape->H * act_bytes(shape->act)}, {bias, (size_t)shape->E * 4},
+                     {Wr_packed, (size_t)shape->H * pad256(shape->E) * act_bytes(shape->act)}});
+  if (s != MOE_OK) return s;
+  const GatedRoute g{rule, logits};
+  return do_route(*shape, x, Wr_packed, bias, topk_idx, topk_w, ws, L, (hipStream_t)stream, nullptr, &g);
+}
+
+moe_status moe_layer_forward_gated(const moe_shape* shape, const moe_gate_rule* rule, const void* x,
+                                   const void* Wr_packed, const float* bias, const moe_weights* routed,
+                                   const moe_weights* shared, void* y, int32_t* topk_idx_out, float* topk_w_out,
+                                   void* ws, size_t ws_bytes, moe_stream_t stream) {
+  moe_status s = check_shape(shape);
+  if (s != MOE_OK) return s;
+  if ((s = check_rule(*shape, rule)) != MOE_OK) return s;
+  const GatedRoute g{rule, nullptr};
+  return do_layer(shape, x, Wr_packed, bias, routed, shared, y, topk_idx_out, topk_w_out, ws, ws_bytes,
+                  (hipStream_t)stream, nullptr, nullptr, true, &g);
 }
 
 moe_status moe_layer_forward_timed(const moe_shape* shape, const void* x, const void* Wr_packed, const float* bias,

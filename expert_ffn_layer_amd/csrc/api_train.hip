@@ -92,25 +92,6 @@ moe_status train_args(const moe_shape* s, const void* x, const int32_t* off, con
   return MOE_OK;
 }
 
-// Memory of an argument; none where it is NULL
-struct Span {
-  const void* p;
-  size_t bytes;
-};
-bool overlap(const Span& a, const Span& b) {
-  return a.p && b.p && a.bytes && b.bytes && (uintptr_t)a.p < (uintptr_t)b.p + b.bytes && (uintptr_t)b.p < (uintptr_t)a.p + a.bytes;
-}
-// No output shares memory with an input or another output, the workspace being one of them.
-moe_status check_outputs(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
-  for (const Span* o = outputs.begin(); o != outputs.end(); ++o) {
-    for (const Span* other = o + 1; other != outputs.end(); ++other)
-      if (overlap(*o, *other)) return fail(MOE_ERR_INVALID_ARG, "two outputs, or an output and the workspace, share memory");
-    for (const Span& in : inputs)
-      if (overlap(*o, in)) return fail(MOE_ERR_INVALID_ARG, "an output or the workspace shares memory with an input");
-  }
-  return MOE_OK;
-}
-
 hipError_t product(TrainForm form, int act, const TrainArgs& a, hipStream_t st) {
   return act == MOE_F32 ? launch_train_f32(form, a, st) : launch_train_bf16(form, a, st);
 }

@@ -1,0 +1,68 @@
+// Launchers of the orthogonalisation by Newton-Schulz products and of the Muon step (formulas in include/moe.h).
+//
+// Matrices of one size class (short side M, long side N) are worked on together, a chunk of them at a time. In the
+// workspace matrix b of a chunk is X, [Np][Mp] with the long side first, whichever way the user's matrix lies, zeros
+// beyond its size; Gram's matrix A and the polynomial C are [Mp][Mp]. Mp and Np are multiples of 64.
+//
+// X, A and C are held in fp16 times SCALE. All stay in its range: X's singular values are at most the bound that the
+// entry points check, and no element of a matrix exceeds its largest singular value.
+#pragma once
+#include "common.h"
+
+namespace moe {
+
+constexpr int MUON_STACKS = 40;      // stacks of one launch
+constexpr float MUON_SCALE = 4096.f;
+constexpr int MUON_SUMS = 64;        // partial sums of squares of a matrix
+constexpr int MUON_PAD = 64;
+
+struct MuonStack {
+  const void* g;
+  float* m;       // NULL: u = g
+  void* out;      // parameters, or the orthogonalised matrices where m is NULL
+  float* master;
+  float scale;    // the update is lr scale O
+  int first;      // index in the class of its first matrix
+  int wide;       // rows < cols: X is the transpose
+};
+
+struct MuonArgs {
+  MuonStack s[MUON_STACKS];
+  int stacks;
+  int first, count;        // matrices of the chunk, as indices of the class
+  int M, N, Mp, Np;
+  int g_f32, out_f32;
+  int split;               // products of fp16 pairs: fp32 results
+  int nesterov;
+  float momentum, lr, wd;
+  const float *lr_dev, *grad_scale;
+  double eps;
+  float a, b, c;           // the polynomial of this step
+  // workspace
+  double* sums;            // [count][MUON_SUMS]
+  uint16_t *x, *x_lo;      // in
+  uint16_t *xo, *xo_lo;    // out; xo_lo may be x_lo without split
+  uint16_t *A, *A_lo, *C, *C_lo;
+  float *da, *dc;          // [count][Mp]: their diagonals, which are zero in A and C
+};
+
+hipError_t launch_muon_momentum(const MuonArgs& a, hipStream_t st);   // m, and the sums of u's squares
+hipError_t launch_muon_normalize(const MuonArgs& a, hipStream_t st);  // x, x_lo = SCALE u / (|u| + eps)
+enum MuonForm {
+  MF_GRAM,  // A = X^T X
+  MF_POLY,  // C = b A + c A^2
+  MF_STEP,  // X' = a X + X C
+  MF_LAST   // the same into the user's matrices
+};
+hipError_t launch_muon_product(MuonForm form, const MuonArgs& a, hipStream_t st);
+
+#ifdef __HIPCC__
+// The stack of matrix `index` of the class
+__device__ __forceinline__ const MuonStack& muon_stack(const MuonArgs& a, int index) {
+  int s = a.stacks - 1;
+  while (s > 0 && a.s[s].first > index) --s;
+  return a.s[s];
+}
+#endif
+
+}  // namespace moe

@@ -53,6 +53,11 @@ class PackedLayer:
                                  topk_idx, topk_w, self.ws, stream)
         return y
 
+    def forward_gated(self, x, rule, bias, y, topk_idx=None, topk_w=None, stream=None):
+        N.moe_layer_forward_gated(self.shape, rule, x, self.Wr, bias, self.routed, self.shared, y, topk_idx, topk_w,
+                                  self.ws, stream)
+        return y
+
     def forward(self, x, bias, y, topk_idx=None, topk_w=None, stream=None):
         N.moe_layer_forward(self.shape, x, self.Wr, bias, self.routed, self.shared, y, topk_idx, topk_w,
                             self.ws, stream)
@@ -78,20 +83,25 @@ def _result(like: torch.Tensor, stream):
 
 
 class TrainableLayer:
-    """One layer's experts in training: forward, backward and AdamW step over row-major weights of the
+    """One layer's experts in training: forward, backward and AdamW or Muon step over row-major weights of the
     activations' type (gate, up [E, H, I], down [E, I, H]; the shared expert's without the first axis or
     with one of 1). The router is read only; its scores' gradient follows from backward's routing-weight
-    gradient. Allocation and marshalling only, like PackedLayer.
+    gradient, or is what backward returns with a gate. Allocation and marshalling only, like PackedLayer.
 
     forward keeps what backward reads (x itself, not a copy), for the last batch alone. Calls, set_tokens and the
     constructor on one stream follow each other; a call on another stream has to wait for the former ones. No memory that a
     call works on (arguments, the layer's own and results) is handed on before that work has ended, whatever its stream.
-    state: "f32", or "e4m3" for 8-bit optimizer states; master: fp32 master copies of bf16 weights."""
+    state: "f32", or "e4m3" for 8-bit optimizer states; master: fp32 master copies of bf16 weights.
+    rule: a gate (native.make_gate) in place of moe_route's; optimizer: "adamw" (step) or "muon" (muon_step, fp32 momentum)."""
 
     NAMES = ("gate", "up", "down")
+    rule = logits = muon_ws = None
 
     def __init__(self, spec, Wr: torch.Tensor, routed: dict, shared: dict | None = None, T: int | None = None,
-                 state: str = "f32", master: bool = False):
+                 state: str = "f32", master: bool = False, rule=None, optimizer: str = "adamw"):
+        if optimizer not in ("adamw", "muon") or optimizer == "muon" and state != "f32":
+            raise ValueError("optimizer is adamw, or muon with the f32 state")
+        self.rule = rule
         self.H, self.I, self.E, self.k, self.act = spec.H, spec.I, spec.E, spec.k, spec.act
         self.dtype = torch.float32 if spec.act == "f32" else torch.bfloat16
         H, E, dev = spec.H, spec.E, Wr.device
@@ -112,12 +122,17 @@ class TrainableLayer:
             m, v = ([torch.zeros(t.numel(), dtype=torch.uint8, device=t.device) for t in p] for _ in range(2))
             ms, vs = ([torch.zeros((t.numel() + 255) // 256, device=t.device) for t in p] for _ in range(2))
         elif state == "f32":
-            m, v = ([torch.zeros(t.shape, device=t.device) for t in p] for _ in range(2))
+            m, v = ([torch.zeros(t.shape, device=t.device) for t in p] if need else None for need in (True, optimizer == "adamw"))
             ms = vs = None
         else:
             raise ValueError("state is f32 or e4m3")
         copies = [t.float() for t in p] if master else None
-        self.optimizer = N.adamw_tensors(p, g, m, v, copies, ms, vs)
+        if optimizer == "muon":
+            self.optimizer = N.muon_tensors(p, g, m, copies)
+            self.muon_ws = torch.empty(N.moe_muon_workspace_size(self.optimizer), dtype=torch.uint8, device=dev)
+        else:
+            self.optimizer = N.adamw_tensors(p, g, m, v, copies, ms, vs)
+            self.muon_ws = None
         self.steps = 0
         self.set_tokens(spec.T if T is None else T)
 
@@ -138,6 +153,7 @@ class TrainableLayer:
         self.idx, self.pair_slot = (torch.empty((T, self.k), dtype=torch.int32, device=dev) for _ in range(2))
         self.w = torch.empty((T, self.k), dtype=torch.float32, device=dev)
         self.ones = torch.ones((T, self.k), dtype=torch.float32, device=dev)
+        self.logits = torch.empty((T, self.E), dtype=torch.float32, device=dev) if self.rule is not None else None
         self.off = torch.zeros(self.E + 1, dtype=torch.int32, device=dev)
         self.slot_token = torch.empty(P, dtype=torch.int32, device=dev)
         rows = [P] + [T] * (len(self.weights) - 1)
@@ -161,7 +177,7 @@ class TrainableLayer:
             stream = self.streams[handle]
         else:
             stream = self.streams[handle] = torch.cuda.current_stream(self.Wr.device) if stream is None else stream
-            tensors += (self.Wr, self.ws, self.idx, self.pair_slot, self.w, self.ones, self.off, self.slot_token, self.dy_perm,
+            tensors += (self.Wr, self.ws, self.muon_ws, self.logits, self.idx, self.pair_slot, self.w, self.ones, self.off, self.slot_token, self.dy_perm,
                         *self.y, *self.dx, *[t for pair in self.pre for t in pair],
                         *[t for x in self.optimizer.keep if x is not None for t in x])
         for t in tensors:
@@ -170,7 +186,7 @@ class TrainableLayer:
         return stream
 
     def forward(self, x, bias=None, stream=None):
-        """y [T, H]; routing as moe_route, kept in idx and w."""
+        """y [T, H]; routing as moe_route (moe_route_gated with a gate, its logits kept too), kept in idx and w."""
         _need("x", x, self.dtype, (self.T, self.H), device=self.Wr.device)
         if bias is not None:
             _need("bias", bias, torch.float32, (self.E,), device=self.Wr.device)
@@ -178,8 +194,12 @@ class TrainableLayer:
         stream = self._work_on(stream, x, bias)
         self.x = None  # until all that backward reads belongs to this batch
         with self._gpu():
-            N.moe_route_permute(self.shapes[0], x, self.Wr, bias, self.idx, self.w, self.off, self.slot_token,
-                                self.pair_slot, self.ws, stream)
+            if self.rule is None:
+                N.moe_route_permute(self.shapes[0], x, self.Wr, bias, self.idx, self.w, self.off, self.slot_token,
+                                    self.pair_slot, self.ws, stream)
+            else:
+                N.moe_route_gated(self.shapes[0], self.rule, x, self.Wr, bias, self.logits, self.idx, self.w, self.ws, stream)
+                N.moe_permute(self.shapes[0], self.idx, self.off, self.slot_token, self.pair_slot, self.ws, stream)
             groups = [(self.off, self.slot_token), (None, None)]
             for shape, group, w, pre, out in zip(self.shapes, groups, self.weights, self.pre, self.y):
                 N.moe_gated_ffn(shape, x, *group, w, *pre, out, self.ws, stream)
@@ -188,11 +208,13 @@ class TrainableLayer:
         return y
 
     def backward(self, dy, stream=None):
-        """(dx through the experts [T, H], gradient of the routing weights [T, k]), both new tensors; fills grads."""
+        """(dx through the experts [T, H], gradient of the routing weights [T, k]), both new tensors; fills grads. With a
+        gate the second is the gradient of the router's logits [T, E]."""
         if self.x is None:
             raise RuntimeError("backward needs a forward pass on this batch size")
         _need("dy", dy, self.dtype, (self.T, self.H), device=self.Wr.device)
         dx, dw = _result(dy, stream), _result(self.w, stream)
+        dlogits = _result(self.logits, stream) if self.rule is not None else None
         stream = self._work_on(stream, self.x, dy)
         with self._gpu():
             N.moe_combine_backward(self.shapes[0], dy, self.y[0], self.pair_slot, self.w, self.dy_perm, dw, stream)
@@ -201,10 +223,22 @@ class TrainableLayer:
                 N.moe_gated_ffn_backward(shape, self.x, off, slot, w, *pre, d, out, grads, self.ws, stream)
             N.moe_combine(self.shapes[0], self.dx[0], self.pair_slot, self.ones, self.dx[1] if len(self.dx) > 1 else None, dx,
                           stream)
-        return dx, dw
+            if self.rule is not None:
+                N.moe_gate_backward(self.shapes[0], self.rule, self.logits, self.idx, dw, dlogits, stream)
+        return dx, dw if self.rule is None else dlogits
 
     def step(self, lr, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.0, stream=None, **more):
         """One AdamW step of every expert matrix by grads; more: moe_adamw's lr_dev, step_dev, grad_scale, seed."""
+        if self.muon_ws is not None:
+            raise ValueError("a layer with Muon's state takes muon_step")
         stream = self._work_on(stream, *more.values())
         N.moe_adamw(self.optimizer, lr, beta1, beta2, eps, weight_decay, self.steps + 1, stream=stream, **more)
+        self.steps += 1
+
+    def muon_step(self, lr, momentum=0.95, nesterov=True, weight_decay=0.0, stream=None, **more):
+        """One Muon step of every expert matrix by grads; more: moe_muon's steps, coefficients, eps, lr_dev, grad_scale."""
+        if self.muon_ws is None:
+            raise ValueError("muon_step is of a layer with optimizer=\"muon\"")
+        stream = self._work_on(stream, *more.values())
+        N.moe_muon(self.optimizer, self.muon_ws, lr, momentum, nesterov, weight_decay, stream=stream, **more)
         self.steps += 1

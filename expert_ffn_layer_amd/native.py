@@ -14,6 +14,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe.so")
 
 DTYPE = {"f32": 0, "bf16": 1, "fp8": 2, "mxfp4": 3, "mxfp4a8": 4, "mxfp8a8": 5, "int8": 6}
+SCORE = {"softmax": 0, "sigmoid": 1}
 PATH = {"auto": 0, "decode": 1, "prefill": 2}
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
           3: "MOE_ERR_WORKSPACE_TOO_SMALL", 4: "MOE_ERR_HIP"}
@@ -21,7 +22,9 @@ EXPORTS = ("moe_status_string", "moe_last_error", "moe_pack_size", "moe_pack", "
            "moe_route", "moe_route_hash", "moe_permute", "moe_route_permute", "moe_grouped_ffn", "moe_combine",
            "moe_layer_forward", "moe_layer_forward_noalloc", "moe_layer_forward_hash", "moe_layer_forward_timed",
            "moe_quantize_mxfp8", "moe_quantize_int8", "moe_logical_workspace_size", "moe_layer_forward_logical",
-           "moe_train_workspace_size", "moe_gated_ffn", "moe_gated_ffn_backward", "moe_combine_backward", "moe_adamw")
+           "moe_train_workspace_size", "moe_gated_ffn", "moe_gated_ffn_backward", "moe_combine_backward", "moe_adamw",
+           "moe_gate", "moe_gate_backward", "moe_route_gated", "moe_layer_forward_gated",
+           "moe_orthogonalize_workspace_size", "moe_orthogonalize", "moe_muon_workspace_size", "moe_muon")
 # the library's own scratch, the workspace of moe_layer_forward_noalloc
 NOALLOC_SCRATCH_BYTES = 64 << 20
 TIMED_EVENTS = 7
@@ -58,6 +61,26 @@ class MoeAdamwConfig(ctypes.Structure):
     _fields_ = [("p_type", ctypes.c_int), ("g_type", ctypes.c_int), ("state", ctypes.c_int)] + \
                [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")] + \
                [("step", ctypes.c_int64), ("seed", ctypes.c_uint32)] + [(n, ctypes.c_void_p) for n in ("lr_dev", "step_dev", "grad_scale")]
+
+
+class MoeGateRule(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int)] + [(n, ctypes.c_int32) for n in ("groups", "top_groups", "group_top", "renormalize")] + \
+               [("scale", ctypes.c_double)]
+
+
+class MoeNewtonSchulz(ctypes.Structure):
+    _fields_ = [("steps", ctypes.c_int32)] + [(n, ctypes.c_double) for n in ("a", "b", "c", "eps")]
+
+
+class MoeMuonTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("p", "g", "m", "master")] + [(n, ctypes.c_int32) for n in ("count", "rows", "cols")] + \
+               [("scale", ctypes.c_double)]
+
+
+class MoeMuonConfig(ctypes.Structure):
+    _fields_ = [("ns", MoeNewtonSchulz), ("p_type", ctypes.c_int), ("g_type", ctypes.c_int)] + \
+               [(n, ctypes.c_double) for n in ("lr", "momentum", "weight_decay")] + [("nesterov", ctypes.c_int32)] + \
+               [(n, ctypes.c_void_p) for n in ("lr_dev", "grad_scale")]
 
 
 _lib = None
@@ -99,6 +122,15 @@ def load() -> ctypes.CDLL:
         lib.moe_gated_ffn_backward.argtypes = [PS, P, P, P, PW, P, P, P, P, ctypes.POINTER(MoeWeightGrads), P, SZ, P]
         lib.moe_combine_backward.argtypes = [PS, P, P, P, P, P, P, P]
         lib.moe_adamw.argtypes = [ctypes.POINTER(MoeAdamwConfig), ctypes.POINTER(MoeAdamwTensor), I32, P]
+        PR = ctypes.POINTER(MoeGateRule)
+        lib.moe_gate.argtypes = [PS, PR, P, P, P, P, P]
+        lib.moe_gate_backward.argtypes = [PS, PR, P, P, P, P, P]
+        lib.moe_route_gated.argtypes = [PS, PR, P, P, P, P, P, P, P, SZ, P]
+        lib.moe_layer_forward_gated.argtypes = [PS, PR, P, P, P, PW, PW, P, P, P, P, SZ, P]
+        lib.moe_orthogonalize_workspace_size.argtypes = [ctypes.c_int, I32, I32, I32, ctypes.POINTER(SZ)]
+        lib.moe_orthogonalize.argtypes = [ctypes.POINTER(MoeNewtonSchulz), ctypes.c_int, I32, I32, I32, P, P, P, SZ, P]
+        lib.moe_muon_workspace_size.argtypes = [ctypes.c_int, ctypes.POINTER(MoeMuonTensor), I32, ctypes.POINTER(SZ)]
+        lib.moe_muon.argtypes = [ctypes.POINTER(MoeMuonConfig), ctypes.POINTER(MoeMuonTensor), I32, P, SZ, P]
         for name in EXPORTS[2:]:
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
@@ -367,3 +399,139 @@ def moe_adamw(tensors: AdamwTensors, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, 
         c.lr_dev, c.step_dev, c.grad_scale = at[1:]
         return load().moe_adamw(c, tensors.array, len(tensors.array), st)
     _run((tensors.keep[0][0], lr_dev, step_dev, grad_scale), stream, call)
+
+
+def make_gate(score="softmax", groups=1, top_groups=None, group_top=1, renormalize=True, scale=1.0) -> MoeGateRule:
+    """The rule of the gate; top_groups: groups where it is None."""
+    return MoeGateRule(SCORE[score], groups, groups if top_groups is None else top_groups, group_top, bool(renormalize), scale)
+
+
+def _sized(*checks):
+    """(name, tensor or None, dtype, elements) of each argument."""
+    for name, t, dtype, n in checks:
+        if t is not None and (t.dtype != dtype or t.numel() != n):
+            raise ValueError("%s: %d elements of %s are needed" % (name, n, dtype))
+
+
+def moe_gate(shape, rule, logits, bias, topk_idx, topk_w, stream=None):
+    """logits float32 [T, E], bias float32 [E] or None -> topk_idx int32 [T, k], topk_w float32 [T, k]."""
+    import torch
+    P = shape.T * shape.k
+    _sized(("logits", logits, torch.float32, shape.T * shape.E), ("bias", bias, torch.float32, shape.E),
+           ("topk_idx", topk_idx, torch.int32, P), ("topk_w", topk_w, torch.float32, P))
+    _run((logits, bias, topk_idx, topk_w), stream, lambda at, st: load().moe_gate(shape, rule, *at, st))
+
+
+def moe_gate_backward(shape, rule, logits, topk_idx, dtopk_w, dlogits, stream=None):
+    """dlogits float32 [T, E], which may be logits, from the gradient of the weights, float32 [T, k]."""
+    import torch
+    P = shape.T * shape.k
+    _sized(("logits", logits, torch.float32, shape.T * shape.E), ("topk_idx", topk_idx, torch.int32, P),
+           ("dtopk_w", dtopk_w, torch.float32, P), ("dlogits", dlogits, torch.float32, shape.T * shape.E))
+    _run((logits, topk_idx, dtopk_w, dlogits), stream, lambda at, st: load().moe_gate_backward(shape, rule, *at, st))
+
+
+def moe_route_gated(shape, rule, x, Wr_packed, bias, logits, topk_idx, topk_w, ws, stream=None):
+    """logits float32 [T, E] receives the router's scores, or None."""
+    import torch
+    P = shape.T * shape.k
+    _sized(("bias", bias, torch.float32, shape.E), ("logits", logits, torch.float32, shape.T * shape.E),
+           ("topk_idx", topk_idx, torch.int32, P), ("topk_w", topk_w, torch.float32, P))
+    _run((ws, x, Wr_packed, bias, logits, topk_idx, topk_w), stream,
+         lambda at, st: load().moe_route_gated(shape, rule, *at[1:], at[0], ws.nbytes, st))
+
+
+def moe_layer_forward_gated(shape, rule, x, Wr_packed, bias, routed: dict, shared: dict | None, y, topk_idx=None,
+                            topk_w=None, ws=None, stream=None):
+    r, s = weights(routed), weights(shared)
+    _check(load().moe_layer_forward_gated(ctypes.byref(shape), ctypes.byref(rule), _p(x), _p(Wr_packed), _p(bias),
+                                          ctypes.byref(r), None if s is None else ctypes.byref(s), _p(y), _p(topk_idx),
+                                          _p(topk_w), _p(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                                          _stream(stream)))
+
+
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)  # takes singular values from 0.01 to 1 into 0.68 to 1.2 in five steps
+
+
+def moe_orthogonalize_workspace_size(type_: str, count: int, rows: int, cols: int) -> int:
+    b = ctypes.c_size_t()
+    _check(load().moe_orthogonalize_workspace_size(DTYPE[type_], count, rows, cols, ctypes.byref(b)))
+    return b.value
+
+
+def _matrix_type(t):
+    import torch
+    name = {torch.float32: "f32", torch.bfloat16: "bf16"}.get(t.dtype)
+    if name is None:
+        raise ValueError("matrices are float32 or bfloat16")
+    return name
+
+
+def moe_orthogonalize(g, o, ws, steps=5, coefficients=NEWTON_SCHULZ, eps=1e-7, stream=None):
+    """g, o [count, rows, cols] or [rows, cols], float32 or bfloat16."""
+    kind, shape = DTYPE[_matrix_type(g)], tuple(g.shape)
+    if len(shape) not in (2, 3) or tuple(o.shape) != shape or o.dtype != g.dtype:
+        raise ValueError("g and o are matrices, or stacks of them, of one size and type")
+    count, rows, cols = shape if len(shape) == 3 else (1, *shape)
+    ns = MoeNewtonSchulz(steps, *coefficients, eps)
+    _run((g, o, ws), stream, lambda at, st: load().moe_orthogonalize(ns, kind, count, rows, cols, *at, ws.nbytes, st))
+
+
+class MuonTensors:
+    """The table of moe_muon, with references that keep its tensors alive."""
+
+    def __init__(self, array, keep, p_type: str, g_type: str):
+        self.array, self.keep, self.p_type, self.g_type = array, keep, p_type, g_type
+
+
+def muon_tensors(p, g, m, master=None, scale=None) -> MuonTensors:
+    """Lists of tensors, one entry per parameter: matrices [rows, cols] or stacks of them [count, rows, cols]. scale: a
+    number each; None: 0.2 sqrt(max(rows, cols)), which gives the update AdamW's usual size. Made once and used for every
+    step on the same tensors."""
+    import torch
+    lists = [p, g, m, master]
+    if any(x is not None and len(x) != len(p) for x in lists + [scale]):
+        raise ValueError("every list needs one entry per parameter")
+    device = p[0].device if len(p) else None
+    rows = []
+    for i, t in enumerate(p):
+        if t.dim() not in (2, 3):
+            raise ValueError("tensor %d: a matrix or a stack of matrices is needed" % i)
+        if t.dtype != p[0].dtype or g[i].dtype != g[0].dtype:
+            raise ValueError("parameters and gradients are of one type each")
+        _matrix_type(t), _matrix_type(g[i])
+        if any(x is not None and x[i].dtype != torch.float32 for x in (m, master)):
+            raise ValueError("momenta and master copies are float32")
+        if any(x is not None and x[i].shape != t.shape for x in (g, m, master)):
+            raise ValueError("tensor %d: sizes differ" % i)
+        if any(x is not None and (not x[i].is_contiguous() or not x[i].is_cuda or x[i].device != device) for x in lists):
+            raise ValueError("tensor %d: contiguous tensors of one GPU are needed" % i)
+        size = tuple(t.shape) if t.dim() == 3 else (1, *t.shape)
+        rows.append(MoeMuonTensor(*[None if x is None else x[i].data_ptr() for x in lists], *size,
+                                  0.2 * max(size[1:]) ** 0.5 if scale is None else scale[i]))
+    return MuonTensors((MoeMuonTensor * len(p))(*rows), [None if x is None else list(x) for x in lists],
+                       _matrix_type(p[0]) if len(p) else "f32", _matrix_type(g[0]) if len(p) else "f32")
+
+
+def moe_muon_workspace_size(tensors: MuonTensors) -> int:
+    b = ctypes.c_size_t()
+    _check(load().moe_muon_workspace_size(DTYPE[tensors.p_type], tensors.array, len(tensors.array), ctypes.byref(b)))
+    return b.value
+
+
+def moe_muon(tensors: MuonTensors, ws, lr=1e-3, momentum=0.95, nesterov=True, weight_decay=0.0, steps=5,
+             coefficients=NEWTON_SCHULZ, eps=1e-7, lr_dev=None, grad_scale=None, stream=None):
+    """lr_dev, grad_scale: one-element float32 device tensors read in place of lr and 1."""
+    if not len(tensors.array):
+        return
+    import torch
+    for t in (lr_dev, grad_scale):
+        if t is not None and (t.dtype != torch.float32 or not t.numel()):
+            raise ValueError("lr_dev and grad_scale hold a float32")
+    c = MoeMuonConfig(MoeNewtonSchulz(steps, *coefficients, eps), DTYPE[tensors.p_type], DTYPE[tensors.g_type], lr, momentum,
+                      weight_decay, bool(nesterov))
+
+    def call(at, st):
+        c.lr_dev, c.grad_scale = at[2:]
+        return load().moe_muon(c, tensors.array, len(tensors.array), at[1], ws.nbytes, st)
+    _run((tensors.keep[0][0], ws, lr_dev, grad_scale), stream, call)

@@ -505,6 +505,138 @@ typedef struct {
 moe_status moe_adamw(const moe_adamw_config* config, const moe_adamw_tensor* tensors,
                      int32_t count, moe_stream_t stream);
 
+/*
+ * The gate: how today's layers choose experts and weigh them beyond moe_route's one rule. For a token with logits
+ * l[E] and a bias b[E] (or none):
+ *   scores   s = 1 / (1 + e^-l), or the softmax of l over all E
+ *   choice   c = s + b; without a bias the experts are ordered by l, which is the order of s
+ *   groups   n = groups sets of E / n consecutive experts; a group is worth its largest c (group_top 1) or the sum of
+ *            its two largest (group_top 2; its largest alone where it has one); the top_groups best groups stay
+ *   chosen   the k largest c in them
+ *   weights  w = scale s, divided by the sum of the chosen s with renormalize. The bias is not in them.
+ * An expert whose logit or bias is -inf is never chosen: where fewer than k can be, the rest of the row is expert -1
+ * with weight 0, which moe_permute skips and moe_combine leaves out (as in moe_route_hash). Equal choices, and equal
+ * groups, go to the lower index. Choices are formed and compared in 64 bits, so they count as equal only where they
+ * differ by less than about 2^-50; weights are rounded once, to fp32. NaN is the largest choice, and reaches the weights
+ * as the formulas say.
+ */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+typedef struct {
+  moe_score score;
+  int32_t groups;      /* 1 (none) to 64, a divisor of E */
+  int32_t top_groups;  /* 1..groups, with top_groups * (E / groups) >= k */
+  int32_t group_top;   /* 1 or 2 */
+  int32_t renormalize; /* 0 or 1 */
+  double scale;        /* finite */
+} moe_gate_rule;
+
+/*
+ * moe_gate — experts and weights from logits. Of shape, T, E and k are used.
+ *   logits   float[T][E]
+ *   bias     float[E] or NULL
+ *   topk_idx int32[T][k] out, in ascending index, then -1;  topk_w float[T][k] out
+ * Outputs must not overlap inputs or each other. MOE_ERR_INVALID_ARG for a rule outside the limits above.
+ */
+moe_status moe_gate(const moe_shape* shape, const moe_gate_rule* rule, const float* logits, const float* bias,
+                    int32_t* topk_idx, float* topk_w, moe_stream_t stream);
+
+/*
+ * moe_gate_backward — the gradient of moe_gate's weights by the logits, the choice of experts held fixed (the bias
+ * and the groups have none). With r = s / (sum of the chosen s):
+ *   sigmoid  dl = w (1 - s) (dw - sum_j r_j dw_j) renormalised, else w (1 - s) dw; 0 for the others
+ *   softmax  dl = w (dw - sum_j r_j dw_j) renormalised, 0 for the others; else scale s (dw - sum_j s_j dw_j) for every
+ *            expert, dw = 0 for the others
+ *   logits, topk_idx  moe_gate's; an entry outside [0, E) or with a logit of -inf takes no part, equal ones add up
+ *   dtopk_w  float[T][k] (moe_combine_backward's); not read where the entry takes no part
+ *   dlogits  float[T][E] out, every element written; may be logits' memory
+ * The bits of a token's result depend on that token alone. Other rules as moe_gate.
+ */
+moe_status moe_gate_backward(const moe_shape* shape, const moe_gate_rule* rule, const float* logits,
+                             const int32_t* topk_idx, const float* dtopk_w, float* dlogits, moe_stream_t stream);
+
+/*
+ * moe_route_gated — moe_route with the gate in place of its rule: the router's scores of x, then moe_gate on them.
+ *   logits   float[T][E] out, or NULL: the scores, for moe_gate_backward
+ * Other arguments, ownership and errors as moe_route and moe_gate.
+ */
+moe_status moe_route_gated(const moe_shape* shape, const moe_gate_rule* rule, const void* x, const void* Wr_packed,
+                           const float* bias, float* logits, int32_t* topk_idx, float* topk_w, void* ws,
+                           size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_layer_forward_gated — moe_layer_forward with moe_route_gated in place of moe_route (arguments as those two).
+ */
+moe_status moe_layer_forward_gated(const moe_shape* shape, const moe_gate_rule* rule, const void* x,
+                                   const void* Wr_packed, const float* bias, const moe_weights* routed,
+                                   const moe_weights* shared, void* y, int32_t* topk_idx_out, float* topk_w_out,
+                                   void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Newton-Schulz products: a matrix's singular values brought near 1 without a decomposition.
+ *   X_0 = G / (|G| + eps), |G| the Frobenius norm (0 for a matrix of zeros)
+ *   X_{i+1} = a X_i + (b A + c A^2) X_i with A = X_i X_i^T, on the side of fewer rows or columns
+ * so that each step takes a singular value s to a s + b s^3 + c s^5. Every matrix of a stack is on its own: one with an
+ * element that is not finite becomes NaN, the others do not change.
+ * Precision by type: MOE_F32 forms the products of pairs of 16-bit numbers with fp32 sums (about 22 bits); MOE_BF16 those
+ * of fp16 numbers with fp32 sums, X itself and the diagonals of A and its polynomial wider: off by about 0.0005 of its norm
+ * before it is rounded, up to 0.001 where the rank is a few. The same bits on every run: no atomics.
+ */
+typedef struct {
+  int32_t steps;  /* 1..32 */
+  double a, b, c; /* such that, from singular values up to 1, no step takes one above 3.7 or |b A + c A^2| above 14 */
+  double eps;     /* >= 0 */
+} moe_newton_schulz;
+
+/*
+ * moe_orthogonalize — the matrices of a stack.
+ *   type     MOE_F32 or MOE_BF16, of g and o
+ *   g        [count][rows][cols], any sizes from 0 (an empty stack enqueues nothing); the shorter side at most 32768, the
+ *            longer at most 2^20
+ *   o        [count][rows][cols] out; must not overlap g or ws
+ *   ws       moe_orthogonalize_workspace_size bytes, 256-byte aligned; calls that may run at the same time need one each,
+ *            and nothing is kept in it between calls. Long stacks are worked on in parts of it.
+ */
+moe_status moe_orthogonalize_workspace_size(moe_dtype type, int32_t count, int32_t rows, int32_t cols, size_t* bytes);
+moe_status moe_orthogonalize(const moe_newton_schulz* ns, moe_dtype type, int32_t count, int32_t rows, int32_t cols,
+                             const void* g, void* o, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_muon — one Muon step of every matrix of `count` stacks, in place:
+ *   g' = grad_scale g, m = momentum m + g', u = g' + momentum m with nesterov, else m
+ *   p = p - lr weight_decay p - lr scale O, O = u after Newton-Schulz steps
+ * m, O and p are formed in fp32. moe_muon_tensor: device pointers of a stack [count][rows][cols] (sizes as
+ * moe_orthogonalize's), 16-byte aligned; m float, of the stack's size, zeros to start with; master: as
+ * moe_adamw's. scale: a factor of the stack's update, often 0.2 sqrt(max(rows, cols)), which gives it AdamW's usual
+ * size, or sqrt(max(1, cols / rows)). No two of all stacks' p, m and master may share memory; g is only read, and it, the
+ * device values and ws must not overlap any of those. Precision by p_type, as moe_orthogonalize's.
+ * lr_dev and grad_scale (device, each may be NULL) are read by the kernels in place of lr and 1, so that a captured call
+ * follows them. lr, weight_decay >= 0; momentum in [0, 1). Stacks whose matrices have the same sides, in either order, are
+ * worked on together. ws: moe_muon_workspace_size bytes, as moe_orthogonalize's.
+ */
+typedef struct {
+  void* p;
+  const void* g;
+  float* m;
+  float* master; /* or NULL */
+  int32_t count, rows, cols;
+  double scale;
+} moe_muon_tensor;
+
+typedef struct {
+  moe_newton_schulz ns;
+  moe_dtype p_type; /* MOE_F32 or MOE_BF16 */
+  moe_dtype g_type; /* MOE_F32 or MOE_BF16 */
+  double lr, momentum, weight_decay;
+  int32_t nesterov; /* 0 or 1 */
+  const float* lr_dev;
+  const float* grad_scale;
+} moe_muon_config;
+
+moe_status moe_muon_workspace_size(moe_dtype p_type, const moe_muon_tensor* tensors, int32_t count, size_t* bytes);
+moe_status moe_muon(const moe_muon_config* config, const moe_muon_tensor* tensors, int32_t count, void* ws,
+                    size_t ws_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
