@@ -1,8 +1,8 @@
 // Launchers of the orthogonalisation by Newton-Schulz products and of the Muon step (formulas in include/moe.h).
 //
 // Matrices of one size class (short side M, long side N) are worked on together, a chunk of them at a time. In the
-// workspace matrix b of a chunk is X, [Np][Mp] with the long side first, whichever way the user's matrix lies, zeros
-// beyond its size; Gram's matrix A and the polynomial C are [Mp][Mp]. Mp and Np are multiples of 64.
+// workspace matrix b of a chunk is X, [Mp][Np] with the short side first, whichever way the user's matrix lies, zeros
+// beyond its size; Gram's matrix A = X X^T and the polynomial C are [Mp][Mp]. Mp and Np are multiples of 128.
 //
 // X, A and C are held in fp16 times SCALE. All stay in its range: X's singular values are at most the bound that the
 // entry points check, and no element of a matrix exceeds its largest singular value.
@@ -14,7 +14,7 @@ namespace moe {
 constexpr int MUON_STACKS = 40;      // stacks of one launch
 constexpr float MUON_SCALE = 4096.f;
 constexpr int MUON_SUMS = 64;        // partial sums of squares of a matrix
-constexpr int MUON_PAD = 64;
+constexpr int MUON_PAD = 128;
 
 struct MuonStack {
   const void* g;
@@ -23,7 +23,7 @@ struct MuonStack {
   float* master;
   float scale;    // the update is lr scale O
   int first;      // index in the class of its first matrix
-  int wide;       // rows < cols: X is the transpose
+  int wide;       // rows < cols, or X is the transpose
 };
 
 struct MuonArgs {
@@ -49,9 +49,9 @@ struct MuonArgs {
 hipError_t launch_muon_momentum(const MuonArgs& a, hipStream_t st);   // m, and the sums of u's squares
 hipError_t launch_muon_normalize(const MuonArgs& a, hipStream_t st);  // x, x_lo = SCALE u / (|u| + eps)
 enum MuonForm {
-  MF_GRAM,  // A = X^T X
+  MF_GRAM,  // A = X X^T
   MF_POLY,  // C = b A + c A^2
-  MF_STEP,  // X' = a X + X C
+  MF_STEP,  // X' = a X + C X
   MF_LAST   // the same into the user's matrices
 };
 hipError_t launch_muon_product(MuonForm form, const MuonArgs& a, hipStream_t st);

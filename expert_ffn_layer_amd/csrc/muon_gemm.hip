@@ -1,177 +1,527 @@
 // The products of the Newton-Schulz steps (v_mfma_f32_32x32x16_f16); forms as listed in muon.h.
 //
-// out[m][n] = sum_k P(m, k) Q(n, k), a tile of 128 x 128 per workgroup of 4 waves. A and C are symmetric: their tiles
-// on and under the diagonal are computed and written to both places.
+// out[m][n] = sum_k P(m, k) Q(n, k), a tile per workgroup of 4 waves; both operands pass through a ring of two slots of 64
+// reduction elements in LDS (tile_ring.h). X is held with its long side contiguous, so that the product with C, most of
+// the work, reads both operands with their own index contiguous (C is symmetric), and Gram's matrix both with the
+// reduction index. A and C are symmetric: their tiles on and under the diagonal are computed and written to both places.
 //
 // Numerics: sums are fp32. X is a pair of fp16, x + x_lo, 22 bits; the products read x alone (11 bits) unless
-// `split` asks for fp32 results: then x y_lo and x_lo y are added to x y. The diagonals of A and C are kept apart in fp32:
-// where singular values are near each other the diagonal holds most of A and C, and its rounding would be most of the error.
+// SPLIT asks for fp32 results: then x y_lo and x_lo y are added to x y, as two more runs over the reduction. The diagonals
+// of A and C are kept apart in fp32: where singular values are near each other the diagonal holds most of A and C, and its
+// rounding would be most of the error.
+#include <type_traits>
+
 #include "muon.h"
+#include "tile_ring.h"
 
 namespace moe {
 
 namespace {
 
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
-typedef __attribute__((ext_vector_type(4))) uint16_t u16x4;
-typedef __attribute__((ext_vector_type(16))) float f32x16;
+typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
+typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+typedef __attribute__((address_space(3))) uint16_t lds_u16;
 
-constexpr int THR = 256, TILE = 128, BK = 32, LD = BK + 8;
+struct Eight {
+  float v[8];
+};
+__device__ __forceinline__ Eight halves(const u32x4& w) {
+  Eight r;
+  const f16x8 h = __builtin_bit_cast(f16x8, w);
+#pragma unroll
+  for (int z = 0; z < 8; ++z) r.v[z] = (float)h[z];
+  return r;
+}
+__device__ __forceinline__ u32x4 to_halves(const Eight& r) {
+  f16x8 h;
+#pragma unroll
+  for (int z = 0; z < 8; ++z) h[z] = (_Float16)r.v[z];
+  return __builtin_bit_cast(u32x4, h);
+}
+// what rounding to `hi` leaves
+__device__ __forceinline__ u32x4 to_rest(const Eight& r, const u32x4& hi) {
+  const Eight h = halves(hi);
+  Eight d;
+#pragma unroll
+  for (int z = 0; z < 8; ++z) d.v[z] = r.v[z] - h.v[z];
+  return to_halves(d);
+}
 
-__device__ __forceinline__ uint16_t half_bits(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
-__device__ __forceinline__ float half_value(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
+// O, of which v.v holds 8 consecutive elements of a user's row, or the parameters' step by it; `n` of them exist
+__device__ __forceinline__ void write_user(const MuonArgs& a, const MuonStack& s, size_t at, int n, bool whole, float lr, const Eight& v) {
+  const float keep = 1.f - lr * a.wd, step = lr * s.scale;
+  Eight w = v;
+  if (whole) {
+    if (s.m) {
+      Eight old;
+      if (s.master || a.out_f32) {
+        const float* const from = (s.master ? s.master : (const float*)s.out) + at;
+        const f32x4 x = *(const f32x4*)from, y = *(const f32x4*)(from + 4);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          old.v[z] = x[z];
+          old.v[4 + z] = y[z];
+        }
+      } else {
+        const u32x4 x = *(const u32x4*)((const uint16_t*)s.out + at);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          old.v[2 * z] = bf16lo(x[z]);
+          old.v[2 * z + 1] = bf16hi(x[z]);
+        }
+      }
+#pragma unroll
+      for (int z = 0; z < 8; ++z) w.v[z] = old.v[z] * keep - step * v.v[z];
+    }
+    if (s.master || a.out_f32) {
+      float* const to = (s.master ? s.master : (float*)s.out) + at;
+      *(f32x4*)to = f32x4{w.v[0], w.v[1], w.v[2], w.v[3]};
+      *(f32x4*)(to + 4) = f32x4{w.v[4], w.v[5], w.v[6], w.v[7]};
+    }
+    if (!a.out_f32)
+      *(u32x4*)((uint16_t*)s.out + at) = u32x4{pack_bf16x2(w.v[0], w.v[1]), pack_bf16x2(w.v[2], w.v[3]),
+                                               pack_bf16x2(w.v[4], w.v[5]), pack_bf16x2(w.v[6], w.v[7])};
+    return;
+  }
+#pragma unroll
+  for (int z = 0; z < 8; ++z) {
+    if (z >= n) break;
+    const size_t i = at + z;
+    if (s.m) {
+      const float old = s.master ? s.master[i] : a.out_f32 ? ((const float*)s.out)[i] : bf16_to_f32(((const uint16_t*)s.out)[i]);
+      w.v[z] = old * keep - step * v.v[z];
+      if (s.master) s.master[i] = w.v[z];
+    }
+    if (a.out_f32) ((float*)s.out)[i] = w.v[z];
+    else ((uint16_t*)s.out)[i] = __builtin_bit_cast(uint16_t, (__bf16)w.v[z]);
+  }
+}
+
+template <int FORM, int WR, int WC, int MT, int NT, bool SPLIT>
+__global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const MuonArgs a) {
+  constexpr bool SYM = FORM == MF_GRAM || FORM == MF_POLY, KC = FORM == MF_GRAM;
+  constexpr int BM = WR * MT * 32, BN = WC * NT * 32, D = 2;
+  static_assert(BM == BN, "square tiles");
+  using T = Tile<BM, KC, !KC>;
+  constexpr int U = T::U, L = 2 * U;  // loads per wave and stage: of an operand, of both
+  using S = Share<!KC, U>;
+  constexpr int PART = KC ? T::BYTES : T::BYTES / 2;
+  // One array for each part that is freed and filled whole: the compiler then sees which loads to LDS a read waits for
+  constexpr int MORE = KC ? 16 : PART;
+  __shared__ __align__(1024) uint8_t p0[PART], p1[PART], p2[MORE], p3[MORE], q0[PART], q1[PART], q2[MORE], q3[MORE];
+#define P_PART(SLOT, B) ((lds_byte*)((SLOT) + (!KC && (B) ? 2 : 0) == 0 ? p0 : (SLOT) + (!KC && (B) ? 2 : 0) == 1 ? p1 : (SLOT) + (!KC && (B) ? 2 : 0) == 2 ? p2 : p3))
+#define Q_PART(SLOT, B) ((lds_byte*)((SLOT) + (!KC && (B) ? 2 : 0) == 0 ? q0 : (SLOT) + (!KC && (B) ? 2 : 0) == 1 ? q1 : (SLOT) + (!KC && (B) ? 2 : 0) == 2 ? q2 : q3))
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wr = wave / WC, wc = wave % WC;
+
+  // --- the tile. Workgroup b runs on XCD b % 8: each XCD gets an equal run of the chunk's tiles, matrix by matrix, so that
+  // what it runs at a time shares operands in its L2.
+  const int short_tiles = (a.Mp + BM - 1) / BM, long_tiles = (a.Np + BM - 1) / BM;
+  const int tiles = SYM ? short_tiles * (short_tiles + 1) / 2 : short_tiles * long_tiles;
+  const long long all = (long long)a.count * tiles, run = (all + NXCD - 1) / NXCD;
+  const long long id = (blockIdx.x % NXCD) * run + blockIdx.x / NXCD;
+  if (blockIdx.x / NXCD >= run || id >= all) return;
+  const int b = (int)(id / tiles);
+  int tm, tn, rest = (int)(id % tiles);
+  // the user's matrix has its long side first: the last product's tiles lie as it does, with X as P
+  bool turned = false;
+  const MuonStack* user = nullptr;
+  if constexpr (SYM) {
+    tm = 0;
+    while (rest > tm) rest -= ++tm;
+    tn = rest;
+  } else {
+    // 4 tiles of the long side x all of the short one after each other
+    const int g = rest / (4 * short_tiles), wide = min(4, long_tiles - 4 * g);
+    rest -= g * 4 * short_tiles;
+    tn = 4 * g + rest % wide;
+    tm = rest / wide;
+    if constexpr (FORM == MF_LAST) {
+      user = &muon_stack(a, a.first + b);
+      turned = !user->wide;
+      if (turned) {
+        const int t = tm;
+        tm = tn;
+        tn = t;
+      }
+    }
+  }
+  const int m0 = tm * BM, n0 = tn * BM;
+  const int mend = turned ? a.Np : a.Mp, nend = SYM || turned ? a.Mp : a.Np;
+  const size_t xat = (size_t)b * a.Mp * a.Np, aat = (size_t)b * a.Mp * a.Mp;
+  const int K = KC ? a.Np : a.Mp, once = K / BK, nsteps = SPLIT ? 3 * once : once;
+
+  // --- loads: this wave's units of both operands; the lower halves of pairs lie `p_lo`, `q_lo` bytes behind the upper
+  const uint8_t *psrc[U], *qsrc[U];
+  const uint16_t *p, *q;
+  int pld, qld;
+  ptrdiff_t p_lo = 0, q_lo = 0;
+  if constexpr (FORM == MF_GRAM) {
+    p = q = a.x + xat;
+    pld = qld = a.Np;
+    if (SPLIT) p_lo = q_lo = (const uint8_t*)a.x_lo - (const uint8_t*)a.x;
+  } else if constexpr (FORM == MF_POLY) {
+    p = q = a.A + aat;
+    pld = qld = a.Mp;
+    if (SPLIT) p_lo = q_lo = (const uint8_t*)a.A_lo - (const uint8_t*)a.A;
+  } else {
+    p = turned ? a.x + xat : a.C + aat;
+    q = turned ? a.C + aat : a.x + xat;
+    pld = turned ? a.Np : a.Mp;
+    qld = turned ? a.Mp : a.Np;
+    if (SPLIT) {
+      const ptrdiff_t x_lo = (const uint8_t*)a.x_lo - (const uint8_t*)a.x, c_lo = (const uint8_t*)a.C_lo - (const uint8_t*)a.C;
+      p_lo = turned ? x_lo : c_lo;
+      q_lo = turned ? c_lo : x_lo;
+    }
+  }
+  const ptrdiff_t pstride = KC ? BK * 2 : (ptrdiff_t)BK * 2 * pld, qstride = KC ? BK * 2 : (ptrdiff_t)BK * 2 * qld;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int un = T::unit(u, wave), r = T::row(un, lane), c = T::elem(un, lane);
+    // sizes are multiples of 128: past the end, indices that exist are repeated, and not stored
+    if constexpr (KC) {
+      const int m = m0 + r, n = n0 + r;
+      psrc[u] = (const uint8_t*)(p + (size_t)(m < mend ? m : m - 128) * pld + c);
+      qsrc[u] = (const uint8_t*)(q + (size_t)(n < nend ? n : n - 128) * qld + c);
+    } else {
+      const int m = m0 + c, n = n0 + c;
+      psrc[u] = (const uint8_t*)(p + (size_t)r * pld + (m < mend ? m : m - 128));
+      qsrc[u] = (const uint8_t*)(q + (size_t)r * qld + (n < nend ? n : n - 128));
+    }
+  }
+  // One load of stage `step`; the source moves on, from one run over the reduction to the next, and stays on the last step
+  auto load_one = [&](const uint8_t*& src, lds_byte* dst, int step, ptrdiff_t stride, ptrdiff_t second, ptrdiff_t third) __attribute__((always_inline)) {
+    __builtin_amdgcn_global_load_lds((const void*)src, (lds_void*)dst, 16, 0, 0);
+    ptrdiff_t adv = step + 1 < nsteps ? stride : 0;
+    if constexpr (SPLIT) {
+      if (step + 1 == once) adv = second - (once - 1) * stride;
+      if (step + 1 == 2 * once) adv = third - (once - 1) * stride;
+    }
+    src += adv;
+    asm volatile("" : "+v"(src));  // one running pointer a load, not one per load and slot
+  };
+  // P runs x, x, x_lo; Q runs x, x_lo, x
+  auto load_p = [&](int u, int step, auto slot) __attribute__((always_inline)) {
+    const int un = T::unit(u, wave);
+    load_one(psrc[u], P_PART(decltype(slot)::value, u >= U / 2) + (KC ? un : un % (T::UNITS / 2)) * 1024, step, pstride, 0, p_lo);
+  };
+  auto load_q = [&](int u, int step, auto slot) __attribute__((always_inline)) {
+    const int un = T::unit(u, wave);
+    load_one(qsrc[u], Q_PART(decltype(slot)::value, u >= U / 2) + (KC ? un : un % (T::UNITS / 2)) * 1024, step, qstride, q_lo, -q_lo);
+  };
+
+  f32x16 acc[NT][MT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) acc[t][i][j] = 0.f;
+
+  {
+    int pb[KC ? 4 : MT], qb[KC ? 4 : NT];
+#pragma unroll
+    for (int i = 0; i < (KC ? 4 : MT); ++i) pb[i] = KC ? T::kc_at(wr * MT, i, lane) : T::mc_at(wr * MT + i, lane);
+#pragma unroll
+    for (int t = 0; t < (KC ? 4 : NT); ++t) qb[t] = KC ? T::kc_at(wc * NT, t, lane) : T::mc_at(wc * NT + t, lane);
+    bf16x8 pf[2][MT], qf[2][NT];  // two quarters: the one multiplied and the one read
+    auto read_p = [&](int i, auto quarter, auto slot) __attribute__((always_inline)) {
+      constexpr int h = decltype(quarter)::value;
+      lds_byte* const part = P_PART(decltype(slot)::value, h >= 2);
+      pf[h & 1][i] = read_frag<BM, KC>(part + (KC ? pb[h] + i * 4096 : pb[i] + (h & 1) * 16 * (BM * 2)));
+    };
+    auto read_q = [&](int t, auto quarter, auto slot) __attribute__((always_inline)) {
+      constexpr int h = decltype(quarter)::value;
+      lds_byte* const part = Q_PART(decltype(slot)::value, h >= 2);
+      qf[h & 1][t] = read_frag<BN, KC>(part + (KC ? qb[h] + t * 4096 : qb[t] + (h & 1) * 16 * (BN * 2)));
+    };
+    constexpr std::integral_constant<int, 0> C0{};
+    constexpr std::integral_constant<int, 1> C1{};
+    constexpr std::integral_constant<int, 2> C2{};
+    constexpr std::integral_constant<int, 3> C3{};
+    // the n-th load of phase ph of step s; slot: that of step s
+    auto load_nth = [&](auto ph_c, int n, int s, auto slot) __attribute__((always_inline)) {
+      constexpr int ph = decltype(ph_c)::value, each = S::count(ph);
+      constexpr std::integral_constant<int, (decltype(slot)::value + D - 1) % D> before{};
+      const bool is_p = KC ? n >= each : n < each;
+      const int u = S::from(ph) + n % each;
+      // phase 0, and phase 1 for whole slots, still bring stage s + D - 1, into the slot of step s - 1
+      if constexpr (ph == 0 || (KC && ph == 1)) {
+        if (is_p) load_p(u, s + D - 1, before);
+        else load_q(u, s + D - 1, before);
+      } else {
+        if (is_p) load_p(u, s + D, slot);
+        else load_q(u, s + D, slot);
+      }
+    };
+    // Products of quarter h, with the reads of the next quarter early behind them and the phase's loads spread over all
+    auto phase = [&](auto quarter, auto rd_slot, int s, auto slot) __attribute__((always_inline)) {
+      constexpr int h = decltype(quarter)::value, LOADS = 2 * S::count(h);
+      constexpr std::integral_constant<int, (h + 1) % 4> next{};
+      constexpr int PRODUCTS = MT * NT, READS = MT + NT, SPAN = PRODUCTS > 4 ? PRODUCTS * 3 / 4 : PRODUCTS;
+#pragma unroll
+      for (int n = 0; n < PRODUCTS; ++n) {
+        const int t = n % NT, i = n / NT;
+        acc[t][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, qf[h & 1][t]), __builtin_bit_cast(f16x8, pf[h & 1][i]),
+                                                           acc[t][i], 0, 0, 0);
+#pragma unroll
+        for (int r = n * READS / SPAN; r < (n + 1) * READS / SPAN && r < READS; ++r) {
+          if (r < NT) read_q(r, next, rd_slot);
+          else read_p(r - NT, next, rd_slot);
+        }
+#pragma unroll
+        for (int z = n * LOADS / PRODUCTS; z < (n + 1) * LOADS / PRODUCTS; ++z) load_nth(quarter, z, s, slot);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    // Loads that may still be in flight: where the second half of a slot is wanted (after phase 0), those of one step;
+    // where the next stage is wanted (after phase 2), the same, and none with whole slots
+    constexpr int FLY0 = L, FLY2 = KC ? 0 : L;
+    auto body = [&](int s, auto slot) __attribute__((always_inline)) {
+      constexpr std::integral_constant<int, (decltype(slot)::value + 1) % D> other{};
+      // opaque in every step, so that the slot stays a constant and does not become a register per slot and fragment
+#pragma unroll
+      for (int i = 0; i < MT && !KC; ++i) asm volatile("" : "+v"(pb[i]));
+#pragma unroll
+      for (int t = 0; t < NT && !KC; ++t) asm volatile("" : "+v"(qb[t]));
+      phase(C0, slot, s, slot);
+      if constexpr (!KC) {
+        MOE_WAIT_LGKM0();
+        MOE_WAIT_VMCNT(FLY0);
+        __builtin_amdgcn_s_barrier();
+      }
+      phase(C1, slot, s, slot);
+      phase(C2, slot, s, slot);
+      MOE_WAIT_LGKM0();
+      MOE_WAIT_VMCNT(FLY2);
+      __builtin_amdgcn_s_barrier();
+      phase(C3, other, s, slot);
+    };
+    // what the steps before the first would have loaded, stage 0 first
+#pragma unroll
+    for (int u = 0; u < U; ++u) load_q(u, 0, C0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) load_p(u, 0, C0);
+    constexpr int FIRST = KC ? 0 : U / 2;  // of stage 1, before phase 3 of step -1
+#pragma unroll
+    for (int u = 0; u < FIRST; ++u) load_q(u, 1, C1);
+#pragma unroll
+    for (int u = 0; u < FIRST; ++u) load_p(u, 1, C1);
+#pragma unroll
+    for (int n = 0; n < 2 * S::count(3); ++n) load_nth(C3, n, -1, C1);
+    MOE_WAIT_VMCNT(2 * FIRST + 2 * S::count(3));
+    __builtin_amdgcn_s_barrier();
+#pragma unroll
+    for (int t = 0; t < NT; ++t) read_q(t, C0, C0);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) read_p(i, C0, C0);
+    for (int s = 0; s < nsteps; s += 2) {  // sizes are multiples of 128: pairs of steps
+      body(s, C0);
+      body(s + 1, C1);
+    }
+    MOE_WAIT_VMCNT(0);  // loads in flight land before the workgroup's LDS is used for other things
+  }
+
+  // --- results. Element 4 q + j of a tile is column 8 q + 4 (lane / 32) + j of row lane % 32. Each wave passes blocks of
+  // 32 rows x 64 columns through 8 KiB of LDS of its own, so that a lane goes on with 8 consecutive columns of a row;
+  // 16-byte chunk c of a row sits at c ^ (row % 16), which keeps both directions free of bank conflicts. Mirrored blocks pass
+  // through another 4.5 KiB as 64 rows of 32, 72 bytes apart. The parts of the ring serve for both.
+  __builtin_amdgcn_s_barrier();
+  static_assert((KC ? PART / 2 : PART) >= 8192, "a part of the ring per wave");
+  lds_byte* const ep = KC ? (lds_byte*)(wave & 2 ? q1 : q0) + (wave & 1) * (PART / 2) : (lds_byte*)(wave == 0 ? q0 : wave == 1 ? q1 : wave == 2 ? q2 : q3);
+  lds_byte* const mirror = KC ? (lds_byte*)(wave & 2 ? p1 : p0) + (wave & 1) * (PART / 2) : (lds_byte*)(wave == 0 ? p0 : wave == 1 ? p1 : wave == 2 ? p2 : p3);
+  const float inv = 1.f / MUON_SCALE;
+  const int wrow = m0 + wr * MT * 32, wcol = n0 + wc * NT * 32, r32 = lane & 31, hi4 = lane >> 5, c8 = lane & 7, r8 = lane >> 3;
+  // The lanes of a wave exchange data through LDS: its accesses run in the order in which they are issued, and this keeps
+  // the compiler from changing that order.
+  auto in_order = [] { __asm__ volatile("" ::: "memory"); };
+  constexpr int BLOCKS = NT / 2;
+  const float* const diagonal = FORM == MF_GRAM ? nullptr : (FORM == MF_POLY ? a.da : a.dc) + (size_t)b * a.Mp;
+  const float lr = FORM == MF_LAST ? (a.lr_dev ? *a.lr_dev : a.lr) : 0.f;
+  if (FORM == MF_LAST && turned) {
+    // X lies across: its part is added where a lane's columns are rows of X, 32 lanes along one
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int m = wrow + i * 32 + r32;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int n = wcol + t * 32 + 8 * (e >> 2) + 4 * hi4 + (e & 3);
+          float x = 0.f;
+          if (m < mend && n < nend) {
+            const size_t at = xat + (size_t)n * a.Np + m;
+            x = (a.a + diagonal[n]) * ((float)__builtin_bit_cast(_Float16, a.x[at]) + (float)__builtin_bit_cast(_Float16, a.x_lo[at]));
+          }
+          acc[t][i][e] = acc[t][i][e] * inv + x;
+        }
+      }
+  }
+  // What a block's results are formed with (the element itself of A or X, and its lower part) is fetched a block ahead
+  constexpr bool OLD = FORM != MF_GRAM;
+  u32x4 hw[2][4], lw[2][4];
+  auto fetch = [&](int blk, int set) __attribute__((always_inline)) {
+    const int n = wcol + blk % BLOCKS * 64 + c8 * 8;
+    const uint16_t* const hi = FORM == MF_POLY ? a.A + aat : a.x + xat;
+    const uint16_t* const lo = FORM == MF_POLY ? a.A_lo + aat : a.x_lo + xat;
+    const int ld = FORM == MF_POLY ? a.Mp : a.Np;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int m = wrow + blk / BLOCKS * 32 + it * 8 + r8;
+      hw[set][it] = lw[set][it] = u32x4{0u, 0u, 0u, 0u};
+      if (m < mend && n < nend) {
+        hw[set][it] = *(const u32x4*)(hi + (size_t)m * ld + n);
+        if (FORM != MF_POLY || SPLIT) lw[set][it] = *(const u32x4*)(lo + (size_t)m * ld + n);
+      }
+    }
+  };
+  if (OLD && !turned) fetch(0, 0);
+#pragma unroll
+  for (int blk = 0; blk < MT * BLOCKS; ++blk) {
+    if (OLD && !turned && blk + 1 < MT * BLOCKS) fetch(blk + 1, (blk + 1) & 1);
+    const int i = blk / BLOCKS, n = wcol + blk % BLOCKS * 64 + c8 * 8;
+    in_order();
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const f32x16& v = acc[2 * (blk % BLOCKS) + z][i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *(lds_f32x4*)(ep + r32 * 256 + (((z * 8 + 2 * j + hi4) ^ (r32 & 15)) << 4)) = f32x4{v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
+    }
+    in_order();
+    Eight dn;  // the diagonal at this lane's columns
+    if constexpr (FORM == MF_POLY) {
+#pragma unroll
+      for (int z = 0; z < 8; ++z) dn.v[z] = n < nend ? diagonal[n + z] : 0.f;
+    }
+    u32x4 low[4];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int row = it * 8 + r8, m = wrow + i * 32 + row;
+      const f32x4 v0 = *(const lds_f32x4*)(ep + row * 256 + (((2 * c8) ^ (row & 15)) << 4));
+      const f32x4 v1 = *(const lds_f32x4*)(ep + row * 256 + (((2 * c8 + 1) ^ (row & 15)) << 4));
+      const bool inside = m < mend && n < nend;
+      Eight r;
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        r.v[z] = v0[z];
+        r.v[4 + z] = v1[z];
+      }
+      Eight x{};
+      if (OLD && !turned) {
+        x = halves(hw[blk & 1][it]);
+        if (FORM != MF_POLY || SPLIT) {
+          const Eight lo = halves(lw[blk & 1][it]);
+#pragma unroll
+          for (int z = 0; z < 8; ++z) x.v[z] += lo.v[z];
+        }
+      }
+      if constexpr (SYM) {
+        const float dm = FORM == MF_POLY && inside ? diagonal[m] : 0.f;
+#pragma unroll
+        for (int z = 0; z < 8; ++z) {
+          const float v = r.v[z] * inv;
+          r.v[z] = v;
+          if constexpr (FORM == MF_POLY) r.v[z] = a.b * x.v[z] + a.c * ((dm + dn.v[z]) * x.v[z] + v);
+          if (m == n + z) {
+            const float d = FORM == MF_GRAM ? v * inv : a.b * dm + a.c * (dm * dm + v * inv);
+            if (inside) (FORM == MF_GRAM ? a.da : a.dc)[(size_t)b * a.Mp + m] = d;
+            r.v[z] = 0.f;
+          }
+        }
+        uint16_t* const out = (FORM == MF_GRAM ? a.A : a.C) + aat;
+        uint16_t* const out_lo = (FORM == MF_GRAM ? a.A_lo : a.C_lo) + aat;
+        const u32x4 hi = to_halves(r);
+        if constexpr (SPLIT) low[it] = to_rest(r, hi);
+        if (inside) {
+          *(u32x4*)(out + (size_t)m * a.Mp + n) = hi;
+          if (SPLIT) *(u32x4*)(out_lo + (size_t)m * a.Mp + n) = low[it];
+        }
+        if (tm != tn) {
+#pragma unroll
+          for (int z = 0; z < 8; ++z) *(lds_u16*)(mirror + (c8 * 8 + z) * 72 + row * 2) = (uint16_t)(hi[z >> 1] >> (16 * (z & 1)));
+        }
+      } else {
+        if (!turned) {
+          const float f = a.a + (inside ? diagonal[m] : 0.f);
+#pragma unroll
+          for (int z = 0; z < 8; ++z) r.v[z] = f * x.v[z] + r.v[z] * inv;
+        }
+        if constexpr (FORM == MF_STEP) {
+          const u32x4 hi = to_halves(r), lo = to_rest(r, hi);
+          if (inside) {
+            *(u32x4*)(a.xo + xat + (size_t)m * a.Np + n) = hi;
+            *(u32x4*)(a.xo_lo + xat + (size_t)m * a.Np + n) = lo;
+          }
+        } else {
+          const int rows = turned ? a.N : a.M, cols = turned ? a.M : a.N;
+          if (m < rows && n < cols) {
+#pragma unroll
+            for (int z = 0; z < 8; ++z) r.v[z] *= inv;
+            const size_t at = (size_t)(a.first + b - user->first) * a.M * a.N + (size_t)m * cols + n;
+            // rows and matrices begin on 16 bytes where the columns are a multiple of 8
+            write_user(a, *user, at, min(8, cols - n), cols % 8 == 0, lr, r);
+          }
+        }
+      }
+    }
+    if constexpr (SYM) {
+      auto across = [&](uint16_t* out) __attribute__((always_inline)) {
+        in_order();
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+          const int row = it * 8 + r8, mm = wcol + blk % BLOCKS * 64 + row, nn = wrow + i * 32 + c8 * 4;
+          const u32x2 v = *(const lds_u32x2*)(mirror + row * 72 + c8 * 8);
+          if (mm < nend && nn < mend) *(u32x2*)(out + (size_t)mm * a.Mp + nn) = v;
+        }
+        in_order();
+      };
+      if (tm != tn) {
+        across((FORM == MF_GRAM ? a.A : a.C) + aat);
+        if constexpr (SPLIT) {
+#pragma unroll
+          for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int z = 0; z < 8; ++z)
+              *(lds_u16*)(mirror + (c8 * 8 + z) * 72 + (it * 8 + r8) * 2) = (uint16_t)(low[it][z >> 1] >> (16 * (z & 1)));
+          across((FORM == MF_GRAM ? a.A_lo : a.C_lo) + aat);
+        }
+      }
+    }
+  }
+}
+
+template <int FORM, int WR, int WC, int MT, int NT>
+hipError_t launch(const MuonArgs& a, hipStream_t st) {
+  constexpr int B = WR * MT * 32;
+  const long long m = (a.Mp + B - 1) / B, n = (a.Np + B - 1) / B;
+  const long long all = (FORM == MF_GRAM || FORM == MF_POLY ? m * (m + 1) / 2 : m * n) * a.count;
+  const unsigned grid = (unsigned)((all + NXCD - 1) / NXCD * NXCD);
+  if (a.split) product_kernel<FORM, WR, WC, MT, NT, true><<<grid, THR, 0, st>>>(a);
+  else product_kernel<FORM, WR, WC, MT, NT, false><<<grid, THR, 0, st>>>(a);
+  return hipGetLastError();
+}
 
 template <int FORM>
-__global__ void __launch_bounds__(THR) product_kernel(const MuonArgs a) {
-  constexpr bool SYM = FORM == MF_GRAM || FORM == MF_POLY;
-  __shared__ __align__(16) uint16_t ps[TILE * LD], qs[TILE * LD];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wr = wave >> 1, wc = wave & 1;
-  const int b = blockIdx.y;
-  const int rows = SYM ? a.Mp : a.Np, K = FORM == MF_GRAM ? a.Np : a.Mp;
-  int tm, tn;
-  if (SYM) {
-    tm = 0;
-    int id = blockIdx.x;
-    while (id > tm) id -= ++tm;
-    tn = id;
-  } else {
-    const int cols = (a.Mp + TILE - 1) / TILE;
-    tm = blockIdx.x / cols;
-    tn = blockIdx.x % cols;
-  }
-  const int m0 = tm * TILE, n0 = tn * TILE;
-  const size_t xat = (size_t)b * a.Np * a.Mp, aat = (size_t)b * a.Mp * a.Mp;
-
-  f32x16 acc[2][2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
-
-  for (int pass = 0; pass < (a.split ? 3 : 1); ++pass) {
-    const uint16_t *p, *q;
-    if (FORM == MF_GRAM) {
-      p = (pass == 2 ? a.x_lo : a.x) + xat;
-      q = (pass == 1 ? a.x_lo : a.x) + xat;
-    } else if (FORM == MF_POLY) {
-      p = (pass == 2 ? a.A_lo : a.A) + aat;
-      q = (pass == 1 ? a.A_lo : a.A) + aat;
-    } else {
-      p = (pass == 2 ? a.x_lo : a.x) + xat;
-      q = (pass == 1 ? a.C_lo : a.C) + aat;
-    }
-    for (int k0 = 0; k0 < K; k0 += BK) {
-      __syncthreads();
-      for (int i = tid; i < TILE * BK / 4; i += THR) {
-        if (FORM == MF_GRAM) {  // [k][m] in memory
-          const int k = i / (TILE / 4), m = i % (TILE / 4) * 4;
-          u16x4 v{}, w{};
-          if (m0 + m < a.Mp) v = *(const u16x4*)(p + (size_t)(k0 + k) * a.Mp + m0 + m);
-          if (n0 + m < a.Mp) w = *(const u16x4*)(q + (size_t)(k0 + k) * a.Mp + n0 + m);
-          for (int z = 0; z < 4; ++z) {
-            ps[(m + z) * LD + k] = v[z];
-            qs[(m + z) * LD + k] = w[z];
-          }
-        } else {
-          const int m = i / (BK / 4), k = i % (BK / 4) * 4;
-          u16x4 v{}, w{};
-          if (m0 + m < rows) v = *(const u16x4*)(p + (size_t)(m0 + m) * a.Mp + k0 + k);
-          if (n0 + m < a.Mp) w = *(const u16x4*)(q + (size_t)(n0 + m) * a.Mp + k0 + k);
-          *(u16x4*)(ps + m * LD + k) = v;
-          *(u16x4*)(qs + m * LD + k) = w;
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int h = 0; h < BK; h += 16) {
-        f16x8 pf[2], qf[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          pf[i] = *(const f16x8*)(ps + (wr * 64 + i * 32 + (lane & 31)) * LD + h + 8 * (lane >> 5));
-          qf[i] = *(const f16x8*)(qs + (wc * 64 + i * 32 + (lane & 31)) * LD + h + 8 * (lane >> 5));
-        }
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            acc[t][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(qf[t], pf[i], acc[t][i], 0, 0, 0);
-      }
-    }
-  }
-
-  // element 4 q + j of a tile is column 8 q + 4 (lane / 32) + j of row lane % 32
-  const float inv = 1.f / MUON_SCALE;
-  const float lr = a.lr_dev ? *a.lr_dev : a.lr;
-  for (int t = 0; t < 2; ++t)
-    for (int i = 0; i < 2; ++i)
-      for (int e = 0; e < 16; ++e) {
-        const int m = m0 + wr * 64 + i * 32 + (lane & 31), n = n0 + wc * 64 + t * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-        if (m >= rows || n >= a.Mp) continue;
-        const float v = acc[t][i][e] * inv;  // times SCALE
-        if (SYM) {
-          float* const d = (FORM == MF_GRAM ? a.da : a.dc) + (size_t)b * a.Mp;
-          uint16_t* const out = (FORM == MF_GRAM ? a.A : a.C) + aat;
-          uint16_t* const out_lo = (FORM == MF_GRAM ? a.A_lo : a.C_lo) + aat;
-          float r = v;
-          if (FORM == MF_POLY) {
-            const float* const da = a.da + (size_t)b * a.Mp;
-            if (m == n) {
-              r = MUON_SCALE * (a.b * da[m] + a.c * (da[m] * da[m] + v * inv));
-            } else {
-              float x = half_value(a.A[aat + (size_t)m * a.Mp + n]);
-              if (a.split) x += half_value(a.A_lo[aat + (size_t)m * a.Mp + n]);
-              r = a.b * x + a.c * ((da[m] + da[n]) * x + v);
-            }
-          }
-          if (m == n) {
-            d[m] = r * inv;
-            r = 0.f;
-          }
-          const uint16_t hi = half_bits(r), lo = half_bits(r - half_value(hi));
-          out[(size_t)m * a.Mp + n] = hi;
-          if (a.split) out_lo[(size_t)m * a.Mp + n] = lo;
-          if (tm != tn) {
-            out[(size_t)n * a.Mp + m] = hi;
-            if (a.split) out_lo[(size_t)n * a.Mp + m] = lo;
-          }
-        } else {
-          const size_t at = xat + (size_t)m * a.Mp + n;
-          const float x = half_value(a.x[at]) + half_value(a.x_lo[at]);
-          const float r = (a.a + a.dc[(size_t)b * a.Mp + n]) * x + v;
-          if (FORM == MF_STEP) {
-            const uint16_t hi = half_bits(r);
-            a.xo[at] = hi;
-            a.xo_lo[at] = half_bits(r - half_value(hi));
-          } else {
-            if (m >= a.N || n >= a.M) continue;
-            const MuonStack& s = muon_stack(a, a.first + b);
-            const size_t o = (size_t)(a.first + b - s.first) * a.M * a.N + (s.wide ? (size_t)n * a.N + m : (size_t)m * a.M + n);
-            float w = r * inv;
-            if (s.m) {
-              const float old = s.master ? s.master[o] : a.out_f32 ? ((const float*)s.out)[o] : bf16_to_f32(((const uint16_t*)s.out)[o]);
-              w = old * (1.f - lr * a.wd) - lr * s.scale * w;
-              if (s.master) s.master[o] = w;
-            }
-            if (a.out_f32) ((float*)s.out)[o] = w;
-            else ((uint16_t*)s.out)[o] = __builtin_bit_cast(uint16_t, (__bf16)w);
-          }
-        }
-      }
+hipError_t choose(const MuonArgs& a, hipStream_t st) {
+  const long long m = (a.Mp + 255) / 256, n = (a.Np + 255) / 256;
+  const long long tiles = (FORM == MF_GRAM || FORM == MF_POLY ? m * (m + 1) / 2 : m * n) * a.count;
+  return tiles >= 224 ? launch<FORM, 2, 2, 4, 4>(a, st) : launch<FORM, 2, 2, 2, 2>(a, st);
 }
 
 }  // namespace
 
 hipError_t launch_muon_product(MuonForm form, const MuonArgs& a, hipStream_t st) {
-  const unsigned m = (a.Mp + TILE - 1) / TILE, n = (a.Np + TILE - 1) / TILE, sym = m * (m + 1) / 2;
   switch (form) {
-    case MF_GRAM: product_kernel<MF_GRAM><<<dim3(sym, a.count), THR, 0, st>>>(a); break;
-    case MF_POLY: product_kernel<MF_POLY><<<dim3(sym, a.count), THR, 0, st>>>(a); break;
-    case MF_STEP: product_kernel<MF_STEP><<<dim3(m * n, a.count), THR, 0, st>>>(a); break;
-    case MF_LAST: product_kernel<MF_LAST><<<dim3(m * n, a.count), THR, 0, st>>>(a); break;
+    case MF_GRAM: return choose<MF_GRAM>(a, st);
+    case MF_POLY: return choose<MF_POLY>(a, st);
+    case MF_STEP: return choose<MF_STEP>(a, st);
+    case MF_LAST: return choose<MF_LAST>(a, st);
   }
-  return hipGetLastError();
+  return hipErrorInvalidValue;
 }
 
 }  // namespace moe

@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(THR) momentum_kernel(const MuonArgs a) {
   if (threadIdx.x == 0) a.sums[b * MUON_SUMS + part] = part_sum[0] + part_sum[1] + part_sum[2] + part_sum[3];
 }
 
-// A tile of 64 x 64 of X; wide matrices are transposed through LDS.
+// A tile of 64 x 64 of X; matrices with the long side first are transposed through LDS.
 __global__ void __launch_bounds__(THR) normalize_kernel(const MuonArgs a) {
   __shared__ float tile[64][65];
   const int b = blockIdx.z, n0 = blockIdx.x * 64, j0 = blockIdx.y * 64;
@@ -62,15 +62,15 @@ __global__ void __launch_bounds__(THR) normalize_kernel(const MuonArgs a) {
       if (s.m) u = a.nesterov ? u + a.momentum * s.m[i] : s.m[i];
       v = (float)(u * f);
     }
-    if (s.wide) tile[c][r] = v;
-    else tile[r][c] = v;
+    if (s.wide) tile[r][c] = v;
+    else tile[c][r] = v;
   }
   __syncthreads();
-  const size_t at = (size_t)b * a.Np * a.Mp;
+  const size_t at = (size_t)b * a.Mp * a.Np;
   for (int r = r0; r < 64; r += 4) {
     const float v = tile[r][c];
     const _Float16 hi = (_Float16)v, lo = (_Float16)(v - (float)hi);
-    const size_t i = at + (size_t)(n0 + r) * a.Mp + j0 + c;
+    const size_t i = at + (size_t)(j0 + r) * a.Np + n0 + c;
     a.x[i] = __builtin_bit_cast(uint16_t, hi);
     a.x_lo[i] = __builtin_bit_cast(uint16_t, lo);
   }
