@@ -77,8 +77,8 @@ moe_status check_ns(const moe_newton_schulz* ns) {
   for (int i = 0; i < ns->steps; ++i) {
     const double t1 = top * top;
     auto f = [&](double t) { return t >= 0.0 && t <= t1 ? fabs(sqrt(t) * (a + t * (b + t * c))) : 0.0; };
-    auto g = [&](double t) { return t >= 0.0 && t <= t1 ? fabs(t * (b + t * c)) : 0.0; };
-    double most = f(t1), poly = std::max(g(t1), c != 0.0 ? g(-b / (2.0 * c)) : 0.0);
+    auto g = [&](double t) { return t >= 0.0 && t <= t1 ? fabs(a + t * (b + t * c)) : 0.0; };
+    double most = f(t1), poly = std::max(std::max(g(0.0), g(t1)), c != 0.0 ? g(-b / (2.0 * c)) : 0.0);
     // where d/ds (a s + b s^3 + c s^5) = a + 3 b t + 5 c t^2 is 0
     const double d = 9.0 * b * b - 20.0 * a * c;
     if (c != 0.0 && d >= 0.0) {
@@ -94,8 +94,8 @@ moe_status check_ns(const moe_newton_schulz* ns) {
   return MOE_OK;
 }
 
-// All steps of the matrices of one class, `total` of them in the stacks of a.
-hipError_t run_class(MuonArgs a, const Class& c, const moe_newton_schulz& ns, int total, void* ws, hipStream_t st) {
+// All steps of the matrices of one class, `total` of them in the stacks of a, the first `wide` with their short side first.
+hipError_t run_class(MuonArgs a, const Class& c, const moe_newton_schulz& ns, int total, int wide, void* ws, hipStream_t st) {
   char* const w = (char*)ws;
   a.M = c.M;
   a.N = c.N;
@@ -124,12 +124,26 @@ hipError_t run_class(MuonArgs a, const Class& c, const moe_newton_schulz& ns, in
     e = launch_muon_momentum(a, st);
     if (e == hipSuccess) e = launch_muon_normalize(a, st);
     for (int i = 0; i < ns.steps && e == hipSuccess; ++i) {
+      const bool last = i + 1 == ns.steps;
+      a.whole_c = last;
       e = launch_muon_product(MF_GRAM, a, st);
       if (e == hipSuccess) e = launch_muon_product(MF_POLY, a, st);
-      if (e == hipSuccess) e = launch_muon_product(i + 1 < ns.steps ? MF_STEP : MF_LAST, a, st);
+      if (e != hipSuccess || last) break;
+      MuonArgs s = a;
+      if (!c.split && i + 2 == ns.steps) s.xo_lo = nullptr;  // the last step reads x alone
+      e = launch_muon_product(MF_STEP, s, st);
       std::swap(a.x, a.xo);
       std::swap(a.x_lo, a.xo_lo);
     }
+    // the matrices that are wide, then the others
+    const int n = std::min(std::max(wide - first, 0), a.count), all = a.count;
+    for (int turned = 0; turned < 2 && e == hipSuccess; ++turned) {
+      a.turned = turned;
+      a.skip = turned ? n : 0;
+      a.count = turned ? all - n : n;
+      if (a.count) e = launch_muon_product(MF_LAST, a, st);
+    }
+    a.skip = 0;
   }
   return e;
 }
@@ -252,7 +266,7 @@ moe_status moe_orthogonalize(const moe_newton_schulz* ns, moe_dtype type, int32_
   a.s[0] = MuonStack{g, nullptr, o, nullptr, 1.f, 0, rows < cols};
   a.stacks = 1;
   a.g_f32 = a.out_f32 = type == MOE_F32;
-  return hip_status(run_class(a, c, *ns, count, ws, (hipStream_t)stream), "orthogonalisation");
+  return hip_status(run_class(a, c, *ns, count, rows < cols ? count : 0, ws, (hipStream_t)stream), "orthogonalisation");
 }
 
 moe_status moe_muon_workspace_size(moe_dtype p_type, const moe_muon_tensor* tensors, int32_t count, size_t* bytes) {
@@ -306,14 +320,17 @@ moe_status moe_muon(const moe_muon_config* c, const moe_muon_tensor* tensors, in
     a.wd = (float)c->weight_decay;
     a.lr_dev = c->lr_dev;
     a.grad_scale = c->grad_scale;
-    int first = 0;
-    for (int i = 0; i < n; ++i) {
-      const moe_muon_tensor& t = tensors[of[i]];
-      a.s[i] = MuonStack{t.g, t.m, t.p, t.master, (float)t.scale, first, t.rows < t.cols};
-      first += t.count;
-    }
+    int first = 0, wide = 0, at = 0;
+    for (int turned = 0; turned < 2; ++turned)
+      for (int i = 0; i < n; ++i) {
+        const moe_muon_tensor& t = tensors[of[i]];
+        if ((t.rows < t.cols) == (turned != 0)) continue;
+        a.s[at++] = MuonStack{t.g, t.m, t.p, t.master, (float)t.scale, first, !turned};
+        first += t.count;
+        if (!turned) wide = first;
+      }
     const moe_muon_tensor& t = tensors[of[0]];
-    return hip_status(run_class(a, class_of(t.rows, t.cols, matrices, c->p_type == MOE_F32), c->ns, matrices, ws, (hipStream_t)stream),
+    return hip_status(run_class(a, class_of(t.rows, t.cols, matrices, c->p_type == MOE_F32), c->ns, matrices, wide, ws, (hipStream_t)stream),
                       "Muon");
   });
 }

@@ -23,13 +23,16 @@ struct MuonStack {
   float* master;
   float scale;    // the update is lr scale O
   int first;      // index in the class of its first matrix
-  int wide;       // rows < cols, or X is the transpose
+  int wide;       // rows < cols, or X is the transpose; stacks with it come first
 };
 
 struct MuonArgs {
   MuonStack s[MUON_STACKS];
   int stacks;
   int first, count;        // matrices of the chunk, as indices of the class
+  int skip;                // of the chunk, those that come before the launch's
+  int turned;              // MF_LAST: the launch's matrices have their long side first
+  int whole_c;             // MF_POLY: C's diagonal stands in C, too
   int M, N, Mp, Np;
   int g_f32, out_f32;
   int split;               // products of fp16 pairs: fp32 results
@@ -41,16 +44,16 @@ struct MuonArgs {
   // workspace
   double* sums;            // [count][MUON_SUMS]
   uint16_t *x, *x_lo;      // in
-  uint16_t *xo, *xo_lo;    // out; xo_lo may be x_lo without split
+  uint16_t *xo, *xo_lo;    // out; xo_lo may be x_lo without split, or NULL
   uint16_t *A, *A_lo, *C, *C_lo;
-  float *da, *dc;          // [count][Mp]: their diagonals, which are zero in A and C
+  float *da, *dc;          // [count][Mp]: the diagonals of A and of a I + C, which are zero in A, and in C but for whole_c and split
 };
 
 hipError_t launch_muon_momentum(const MuonArgs& a, hipStream_t st);   // m, and the sums of u's squares
 hipError_t launch_muon_normalize(const MuonArgs& a, hipStream_t st);  // x, x_lo = SCALE u / (|u| + eps)
 enum MuonForm {
   MF_GRAM,  // A = X X^T
-  MF_POLY,  // C = b A + c A^2
+  MF_POLY,  // C = b A + c A^2, and its diagonal with a
   MF_STEP,  // X' = a X + C X
   MF_LAST   // the same into the user's matrices
 };

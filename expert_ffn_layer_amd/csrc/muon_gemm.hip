@@ -8,7 +8,10 @@
 // Numerics: sums are fp32. X is a pair of fp16, x + x_lo, 22 bits; the products read x alone (11 bits) unless
 // SPLIT asks for fp32 results: then x y_lo and x_lo y are added to x y, as two more runs over the reduction. The diagonals
 // of A and C are kept apart in fp32: where singular values are near each other the diagonal holds most of A and C, and its
-// rounding would be most of the error.
+// rounding would be most of the error. C's diagonal, which holds a too, multiplies the whole of X: what rounding adds to
+// directions that X lacks would grow by a = 3.4 in every step. The last step has none after it: it takes x alone, and C's
+// diagonal as the fp16 that stands in C, so that it has X to read in the product only (with SPLIT every step does: the pairs
+// hold all of both).
 #include <type_traits>
 
 #include "muon.h"
@@ -49,57 +52,44 @@ __device__ __forceinline__ u32x4 to_rest(const Eight& r, const u32x4& hi) {
   return to_halves(d);
 }
 
-// O, of which v.v holds 8 consecutive elements of a user's row, or the parameters' step by it; `n` of them exist
-__device__ __forceinline__ void write_user(const MuonArgs& a, const MuonStack& s, size_t at, int n, bool whole, float lr, const Eight& v) {
-  const float keep = 1.f - lr * a.wd, step = lr * s.scale;
-  Eight w = v;
-  if (whole) {
-    if (s.m) {
-      Eight old;
-      if (s.master || a.out_f32) {
-        const float* const from = (s.master ? s.master : (const float*)s.out) + at;
-        const f32x4 x = *(const f32x4*)from, y = *(const f32x4*)(from + 4);
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          old.v[z] = x[z];
-          old.v[4 + z] = y[z];
-        }
-      } else {
-        const u32x4 x = *(const u32x4*)((const uint16_t*)s.out + at);
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          old.v[2 * z] = bf16lo(x[z]);
-          old.v[2 * z + 1] = bf16hi(x[z]);
-        }
-      }
-#pragma unroll
-      for (int z = 0; z < 8; ++z) w.v[z] = old.v[z] * keep - step * v.v[z];
-    }
-    if (s.master || a.out_f32) {
-      float* const to = (s.master ? s.master : (float*)s.out) + at;
-      *(f32x4*)to = f32x4{w.v[0], w.v[1], w.v[2], w.v[3]};
-      *(f32x4*)(to + 4) = f32x4{w.v[4], w.v[5], w.v[6], w.v[7]};
-    }
-    if (!a.out_f32)
-      *(u32x4*)((uint16_t*)s.out + at) = u32x4{pack_bf16x2(w.v[0], w.v[1]), pack_bf16x2(w.v[2], w.v[3]),
-                                               pack_bf16x2(w.v[4], w.v[5]), pack_bf16x2(w.v[6], w.v[7])};
-    return;
+// Where the last product goes. O in the matrices' type; parameters of that type; bf16 parameters with fp32 copies
+enum Out { OUT_NONE, OUT_O, OUT_P, OUT_MASTER };
+
+// 8 consecutive fp32 (8 words) or bf16 (4 words) of a row
+template <bool F32>
+struct Row8 {
+  u32x4 w[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ __forceinline__ Row8<F32> load8(const void* p, size_t at) {
+  Row8<F32> r;
+  if constexpr (F32) {
+    r.w[0] = *(const u32x4*)((const float*)p + at);
+    r.w[1] = *(const u32x4*)((const float*)p + at + 4);
+  } else {
+    r.w[0] = *(const u32x4*)((const uint16_t*)p + at);
   }
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ Eight values(const Row8<F32>& r) {
+  Eight v;
 #pragma unroll
   for (int z = 0; z < 8; ++z) {
-    if (z >= n) break;
-    const size_t i = at + z;
-    if (s.m) {
-      const float old = s.master ? s.master[i] : a.out_f32 ? ((const float*)s.out)[i] : bf16_to_f32(((const uint16_t*)s.out)[i]);
-      w.v[z] = old * keep - step * v.v[z];
-      if (s.master) s.master[i] = w.v[z];
-    }
-    if (a.out_f32) ((float*)s.out)[i] = w.v[z];
-    else ((uint16_t*)s.out)[i] = __builtin_bit_cast(uint16_t, (__bf16)w.v[z]);
+    if constexpr (F32) v.v[z] = __uint_as_float(r.w[z >> 2][z & 3]);
+    else v.v[z] = z & 1 ? bf16hi(r.w[0][z >> 1]) : bf16lo(r.w[0][z >> 1]);
   }
+  return v;
+}
+__device__ __forceinline__ void store_f32(float* p, size_t at, const Eight& v) {
+  *(f32x4*)(p + at) = f32x4{v.v[0], v.v[1], v.v[2], v.v[3]};
+  *(f32x4*)(p + at + 4) = f32x4{v.v[4], v.v[5], v.v[6], v.v[7]};
+}
+__device__ __forceinline__ void store_bf16(uint16_t* p, size_t at, const Eight& v) {
+  *(u32x4*)(p + at) = u32x4{pack_bf16x2(v.v[0], v.v[1]), pack_bf16x2(v.v[2], v.v[3]), pack_bf16x2(v.v[4], v.v[5]), pack_bf16x2(v.v[6], v.v[7])};
 }
 
-template <int FORM, int WR, int WC, int MT, int NT, bool SPLIT>
+template <int FORM, int WR, int WC, int MT, int NT, bool SPLIT, int OUT>
 __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const MuonArgs a) {
   constexpr bool SYM = FORM == MF_GRAM || FORM == MF_POLY, KC = FORM == MF_GRAM;
   constexpr int BM = WR * MT * 32, BN = WC * NT * 32, D = 2;
@@ -115,6 +105,8 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const
 #define Q_PART(SLOT, B) ((lds_byte*)((SLOT) + (!KC && (B) ? 2 : 0) == 0 ? q0 : (SLOT) + (!KC && (B) ? 2 : 0) == 1 ? q1 : (SLOT) + (!KC && (B) ? 2 : 0) == 2 ? q2 : q3))
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / WC, wc = wave % WC;
+  // the user's matrices have their long side first: the last product's tiles lie as they do, with X as P
+  const bool turned = FORM == MF_LAST && a.turned;
 
   // --- the tile. Workgroup b runs on XCD b % 8: each XCD gets an equal run of the chunk's tiles, matrix by matrix, so that
   // what it runs at a time shares operands in its L2.
@@ -123,11 +115,8 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const
   const long long all = (long long)a.count * tiles, run = (all + NXCD - 1) / NXCD;
   const long long id = (blockIdx.x % NXCD) * run + blockIdx.x / NXCD;
   if (blockIdx.x / NXCD >= run || id >= all) return;
-  const int b = (int)(id / tiles);
+  const int b = a.skip + (int)(id / tiles);
   int tm, tn, rest = (int)(id % tiles);
-  // the user's matrix has its long side first: the last product's tiles lie as it does, with X as P
-  bool turned = false;
-  const MuonStack* user = nullptr;
   if constexpr (SYM) {
     tm = 0;
     while (rest > tm) rest -= ++tm;
@@ -138,14 +127,10 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const
     rest -= g * 4 * short_tiles;
     tn = 4 * g + rest % wide;
     tm = rest / wide;
-    if constexpr (FORM == MF_LAST) {
-      user = &muon_stack(a, a.first + b);
-      turned = !user->wide;
-      if (turned) {
-        const int t = tm;
-        tm = tn;
-        tn = t;
-      }
+    if (turned) {
+      const int t = tm;
+      tm = tn;
+      tn = t;
     }
   }
   const int m0 = tm * BM, n0 = tn * BM;
@@ -338,51 +323,48 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const
   // The lanes of a wave exchange data through LDS: its accesses run in the order in which they are issued, and this keeps
   // the compiler from changing that order.
   auto in_order = [] { __asm__ volatile("" ::: "memory"); };
-  constexpr int BLOCKS = NT / 2;
+  constexpr int BLOCKS = NT / 2, ALL = MT * BLOCKS;
   const float* const diagonal = FORM == MF_GRAM ? nullptr : (FORM == MF_POLY ? a.da : a.dc) + (size_t)b * a.Mp;
-  const float lr = FORM == MF_LAST ? (a.lr_dev ? *a.lr_dev : a.lr) : 0.f;
-  if (FORM == MF_LAST && turned) {
-    // X lies across: its part is added where a lane's columns are rows of X, 32 lanes along one
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int m = wrow + i * 32 + r32;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int n = wcol + t * 32 + 8 * (e >> 2) + 4 * hi4 + (e & 3);
-          float x = 0.f;
-          if (m < mend && n < nend) {
-            const size_t at = xat + (size_t)n * a.Np + m;
-            x = (a.a + diagonal[n]) * ((float)__builtin_bit_cast(_Float16, a.x[at]) + (float)__builtin_bit_cast(_Float16, a.x_lo[at]));
-          }
-          acc[t][i][e] = acc[t][i][e] * inv + x;
-        }
-      }
+  // What a block's results are formed with is fetched AHEAD blocks before: the elements themselves of A or X, or the
+  // user's parameters. A block takes about 1 us, a load from memory 2 to 3 while all CUs write.
+  constexpr bool OLD_HI = FORM == MF_POLY || (FORM == MF_STEP && !SPLIT), OLD_LO = (FORM == MF_POLY && SPLIT) || (FORM == MF_STEP && !SPLIT);
+  constexpr bool OLD_P = OUT == OUT_P || OUT == OUT_MASTER, P_F32 = SPLIT || OUT == OUT_MASTER;
+  constexpr int AHEAD = ALL < 3 ? ALL : 3;
+  const uint16_t* const old_hi = FORM == MF_POLY ? a.A + aat : a.x + xat;
+  const uint16_t* const old_lo = FORM == MF_POLY ? a.A_lo + aat : a.x_lo + xat;
+  const int ld = FORM == MF_POLY ? a.Mp : a.Np;
+  const MuonStack* const user = FORM == MF_LAST ? &muon_stack(a, a.first + b) : nullptr;
+  const int rows = turned ? a.N : a.M, cols = turned ? a.M : a.N;  // of the user's matrix
+  const size_t uat = FORM == MF_LAST ? (size_t)(a.first + b - user->first) * a.M * a.N : 0;
+  const bool whole = cols % 8 == 0;  // rows and matrices begin on 16 bytes, and no 8 columns pass their end
+  void* const params = FORM == MF_LAST ? (OUT == OUT_MASTER ? (void*)user->master : user->out) : nullptr;
+  float keep = 0.f, step = 0.f;
+  if constexpr (OLD_P) {
+    const float lr = a.lr_dev ? *a.lr_dev : a.lr;
+    keep = 1.f - lr * a.wd;
+    step = lr * user->scale;
   }
-  // What a block's results are formed with (the element itself of A or X, and its lower part) is fetched a block ahead
-  constexpr bool OLD = FORM != MF_GRAM;
-  u32x4 hw[2][4], lw[2][4];
-  auto fetch = [&](int blk, int set) __attribute__((always_inline)) {
-    const int n = wcol + blk % BLOCKS * 64 + c8 * 8;
-    const uint16_t* const hi = FORM == MF_POLY ? a.A + aat : a.x + xat;
-    const uint16_t* const lo = FORM == MF_POLY ? a.A_lo + aat : a.x_lo + xat;
-    const int ld = FORM == MF_POLY ? a.Mp : a.Np;
+  u32x4 hw[AHEAD][OLD_HI ? 4 : 1], lw[AHEAD][OLD_LO ? 4 : 1];
+  Row8<P_F32> pw[AHEAD][OLD_P ? 4 : 1];
+  auto fetch = [&](int blk) __attribute__((always_inline)) {
+    const int n = wcol + blk % BLOCKS * 64 + c8 * 8, set = blk % AHEAD;
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const int m = wrow + blk / BLOCKS * 32 + it * 8 + r8;
-      hw[set][it] = lw[set][it] = u32x4{0u, 0u, 0u, 0u};
-      if (m < mend && n < nend) {
-        hw[set][it] = *(const u32x4*)(hi + (size_t)m * ld + n);
-        if (FORM != MF_POLY || SPLIT) lw[set][it] = *(const u32x4*)(lo + (size_t)m * ld + n);
-      }
+      // past the end an element that exists, which is not used
+      const size_t at = m < mend && n < nend ? (size_t)m * ld + n : 0;
+      if constexpr (OLD_HI) hw[set][it] = *(const u32x4*)(old_hi + at);
+      if constexpr (OLD_LO) lw[set][it] = *(const u32x4*)(old_lo + at);
+      if constexpr (OLD_P)
+        if (whole) pw[set][it] = load8<P_F32>(params, uat + (m < rows && n < cols ? (size_t)m * cols + n : 0));
     }
   };
-  if (OLD && !turned) fetch(0, 0);
 #pragma unroll
-  for (int blk = 0; blk < MT * BLOCKS; ++blk) {
-    if (OLD && !turned && blk + 1 < MT * BLOCKS) fetch(blk + 1, (blk + 1) & 1);
-    const int i = blk / BLOCKS, n = wcol + blk % BLOCKS * 64 + c8 * 8;
+  for (int blk = 0; blk < AHEAD - 1; ++blk) fetch(blk);
+#pragma unroll
+  for (int blk = 0; blk < ALL; ++blk) {
+    if (blk + AHEAD - 1 < ALL) fetch(blk + AHEAD - 1);
+    const int i = blk / BLOCKS, n = wcol + blk % BLOCKS * 64 + c8 * 8, set = blk % AHEAD;
     in_order();
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
@@ -395,7 +377,7 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const
     Eight dn;  // the diagonal at this lane's columns
     if constexpr (FORM == MF_POLY) {
 #pragma unroll
-      for (int z = 0; z < 8; ++z) dn.v[z] = n < nend ? diagonal[n + z] : 0.f;
+      for (int z = 0; z < 8; ++z) dn.v[z] = diagonal[n < nend ? n + z : z];
     }
     u32x4 low[4];
 #pragma unroll
@@ -407,35 +389,37 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const
       Eight r;
 #pragma unroll
       for (int z = 0; z < 4; ++z) {
-        r.v[z] = v0[z];
-        r.v[4 + z] = v1[z];
+        r.v[z] = v0[z] * inv;
+        r.v[4 + z] = v1[z] * inv;
       }
       Eight x{};
-      if (OLD && !turned) {
-        x = halves(hw[blk & 1][it]);
-        if (FORM != MF_POLY || SPLIT) {
-          const Eight lo = halves(lw[blk & 1][it]);
+      if constexpr (OLD_HI) x = halves(hw[set][it]);
+      if constexpr (OLD_LO) {
+        const Eight lo = halves(lw[set][it]);
 #pragma unroll
-          for (int z = 0; z < 8; ++z) x.v[z] += lo.v[z];
-        }
+        for (int z = 0; z < 8; ++z) x.v[z] += lo.v[z];
       }
       if constexpr (SYM) {
-        const float dm = FORM == MF_POLY && inside ? diagonal[m] : 0.f;
+        const float dm = FORM == MF_POLY ? diagonal[m < mend ? m : 0] : 0.f;
+        Eight q = r;
+        if constexpr (FORM == MF_POLY) {
 #pragma unroll
-        for (int z = 0; z < 8; ++z) {
-          const float v = r.v[z] * inv;
-          r.v[z] = v;
-          if constexpr (FORM == MF_POLY) r.v[z] = a.b * x.v[z] + a.c * ((dm + dn.v[z]) * x.v[z] + v);
-          if (m == n + z) {
-            const float d = FORM == MF_GRAM ? v * inv : a.b * dm + a.c * (dm * dm + v * inv);
-            if (inside) (FORM == MF_GRAM ? a.da : a.dc)[(size_t)b * a.Mp + m] = d;
-            r.v[z] = 0.f;
-          }
+          for (int z = 0; z < 8; ++z) q.v[z] = a.b * x.v[z] + a.c * ((dm + dn.v[z]) * x.v[z] + r.v[z]);
+        }
+        if (tm == tn) {
+#pragma unroll
+          for (int z = 0; z < 8; ++z)
+            if (m == n + z) {
+              const float d = FORM == MF_GRAM ? r.v[z] * inv : a.a + a.b * dm + a.c * (dm * dm + r.v[z] * inv);
+              if (inside) (FORM == MF_GRAM ? a.da : a.dc)[(size_t)b * a.Mp + m] = d;
+              // C keeps its diagonal where the product that reads it adds nothing to it
+              q.v[z] = FORM == MF_POLY && (SPLIT || a.whole_c) ? d * MUON_SCALE : 0.f;
+            }
         }
         uint16_t* const out = (FORM == MF_GRAM ? a.A : a.C) + aat;
         uint16_t* const out_lo = (FORM == MF_GRAM ? a.A_lo : a.C_lo) + aat;
-        const u32x4 hi = to_halves(r);
-        if constexpr (SPLIT) low[it] = to_rest(r, hi);
+        const u32x4 hi = to_halves(q);
+        if constexpr (SPLIT) low[it] = to_rest(q, hi);
         if (inside) {
           *(u32x4*)(out + (size_t)m * a.Mp + n) = hi;
           if (SPLIT) *(u32x4*)(out_lo + (size_t)m * a.Mp + n) = low[it];
@@ -444,26 +428,40 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const
 #pragma unroll
           for (int z = 0; z < 8; ++z) *(lds_u16*)(mirror + (c8 * 8 + z) * 72 + row * 2) = (uint16_t)(hi[z >> 1] >> (16 * (z & 1)));
         }
-      } else {
-        if (!turned) {
-          const float f = a.a + (inside ? diagonal[m] : 0.f);
+      } else if constexpr (FORM == MF_STEP) {
+        if constexpr (!SPLIT) {
+          const float f = diagonal[m < mend ? m : 0];
 #pragma unroll
-          for (int z = 0; z < 8; ++z) r.v[z] = f * x.v[z] + r.v[z] * inv;
+          for (int z = 0; z < 8; ++z) r.v[z] += f * x.v[z];
         }
-        if constexpr (FORM == MF_STEP) {
-          const u32x4 hi = to_halves(r), lo = to_rest(r, hi);
-          if (inside) {
-            *(u32x4*)(a.xo + xat + (size_t)m * a.Np + n) = hi;
-            *(u32x4*)(a.xo_lo + xat + (size_t)m * a.Np + n) = lo;
-          }
-        } else {
-          const int rows = turned ? a.N : a.M, cols = turned ? a.M : a.N;
-          if (m < rows && n < cols) {
+        const u32x4 hi = to_halves(r);
+        if (inside) *(u32x4*)(a.xo + xat + (size_t)m * a.Np + n) = hi;
+        if (a.xo_lo) {
+          const u32x4 lo = to_rest(r, hi);
+          if (inside) *(u32x4*)(a.xo_lo + xat + (size_t)m * a.Np + n) = lo;
+        }
+      } else {
 #pragma unroll
-            for (int z = 0; z < 8; ++z) r.v[z] *= inv;
-            const size_t at = (size_t)(a.first + b - user->first) * a.M * a.N + (size_t)m * cols + n;
-            // rows and matrices begin on 16 bytes where the columns are a multiple of 8
-            write_user(a, *user, at, min(8, cols - n), cols % 8 == 0, lr, r);
+        for (int z = 0; z < 8; ++z) r.v[z] *= inv;
+        const size_t at = uat + (size_t)m * cols + n;
+        if (whole) {
+          if constexpr (OLD_P) {
+            const Eight old = values<P_F32>(pw[set][it]);
+#pragma unroll
+            for (int z = 0; z < 8; ++z) r.v[z] = old.v[z] * keep - step * r.v[z];
+          }
+          if (m < rows && n < cols) {
+            if constexpr (P_F32) store_f32((float*)params, at, r);
+            if constexpr (!SPLIT) store_bf16((uint16_t*)user->out, at, r);
+          }
+        } else if (m < rows) {
+#pragma unroll
+          for (int z = 0; z < 8; ++z) {
+            if (n + z >= cols) break;
+            float w = r.v[z];
+            if constexpr (OLD_P) w = (P_F32 ? ((const float*)params)[at + z] : bf16_to_f32(((const uint16_t*)params)[at + z])) * keep - step * w;
+            if constexpr (P_F32) ((float*)params)[at + z] = w;
+            if constexpr (!SPLIT) ((uint16_t*)user->out)[at + z] = __builtin_bit_cast(uint16_t, (__bf16)w);
           }
         }
       }
@@ -500,8 +498,24 @@ hipError_t launch(const MuonArgs& a, hipStream_t st) {
   const long long m = (a.Mp + B - 1) / B, n = (a.Np + B - 1) / B;
   const long long all = (FORM == MF_GRAM || FORM == MF_POLY ? m * (m + 1) / 2 : m * n) * a.count;
   const unsigned grid = (unsigned)((all + NXCD - 1) / NXCD * NXCD);
-  if (a.split) product_kernel<FORM, WR, WC, MT, NT, true><<<grid, THR, 0, st>>>(a);
-  else product_kernel<FORM, WR, WC, MT, NT, false><<<grid, THR, 0, st>>>(a);
+#define MOE_PRODUCT(SPLIT, OUT) product_kernel<FORM, WR, WC, MT, NT, SPLIT, OUT><<<grid, THR, 0, st>>>(a)
+  if constexpr (FORM == MF_LAST) {
+    const MuonStack& s = a.s[0];  // all stacks have what the first has
+    if (!s.m) {
+      if (a.split) MOE_PRODUCT(true, OUT_O);
+      else MOE_PRODUCT(false, OUT_O);
+    } else if (s.master) {
+      MOE_PRODUCT(false, OUT_MASTER);
+    } else if (a.split) {
+      MOE_PRODUCT(true, OUT_P);
+    } else {
+      MOE_PRODUCT(false, OUT_P);
+    }
+  } else {
+    if (a.split) MOE_PRODUCT(true, OUT_NONE);
+    else MOE_PRODUCT(false, OUT_NONE);
+  }
+#undef MOE_PRODUCT
   return hipGetLastError();
 }
 

@@ -584,7 +584,7 @@ moe_status moe_layer_forward_gated(const moe_shape* shape, const moe_gate_rule* 
  */
 typedef struct {
   int32_t steps;  /* 1..32 */
-  double a, b, c; /* such that, from singular values up to 1, no step takes one above 3.7 or |b A + c A^2| above 14 */
+  double a, b, c; /* such that, from singular values up to 1, no step takes one above 3.7 or |a I + b A + c A^2| above 14 */
   double eps;     /* >= 0 */
 } moe_newton_schulz;
 

@@ -85,7 +85,8 @@ def newton_schulz(g, steps=5, coef=NS, eps=1e-7):
 
 def rounded_steps(g, steps=5, coef=NS, eps=1e-7):
     """The same with the roundings that the 16-bit products' operands take and nothing else: x to fp16 in the products,
-    to a pair of them beside; A and C to fp16 but for their diagonals. In 64 bits otherwise."""
+    to a pair of them beside; A and C to fp16 but for their diagonals; in the last step x to fp16 alone, and C's diagonal.
+    In 64 bits otherwise."""
     a, b, c = coef
     S = 4096.0
     x = g.double()
@@ -97,15 +98,16 @@ def rounded_steps(g, steps=5, coef=NS, eps=1e-7):
     half = lambda t: t.half().double()  # noqa: E731
     diagonal = lambda t: torch.diagonal(t, dim1=1, dim2=2).clone()  # noqa: E731
     bare = lambda t: half(t - torch.diag_embed(diagonal(t)))  # noqa: E731
-    for _ in range(steps):
+    for i in range(steps):
         h = half(x)
-        x = h + half(x - h)
+        x = h + half(x - h) if i + 1 < steps else h
         A = torch.bmm(h, h.transpose(1, 2).contiguous()) / S
         d, A = diagonal(A) / S, bare(A)
         A2 = torch.bmm(A, A) / S
         C = b * A + c * ((d[:, :, None] + d[:, None, :]) * A + A2)
         dc, C = b * d + c * (d * d + diagonal(A2) / S), bare(C)
-        x = (a + dc)[:, :, None] * x + torch.bmm(C, h) / S
+        dc = a + dc if i + 1 < steps else half((a + dc) * S) / S
+        x = dc[:, :, None] * x + torch.bmm(C, h) / S
     x = x / S
     return x if wide else x.transpose(1, 2).contiguous()
 
