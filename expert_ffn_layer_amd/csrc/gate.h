@@ -18,6 +18,7 @@ struct GateArgs {
   double scale;
   int ldl, nparts, T, E, k;
   int sigmoid, renormalize, groups, top_groups, group_top;
+  int whole;              // rows are read 16 bytes at a time (set by the launch)
 };
 
 GateArgs gate_args(const moe_shape& s, const moe_gate_rule& r);  // of T, E, k and the rule, for logits [T][E]

@@ -2,18 +2,103 @@
 // c = s + b (l itself without a bias: the same order):
 //   a group's value is its largest c or the sum of its two largest; the best groups stay; the k largest c in them are chosen
 //   w_j = scale s_j, divided by the sum of the chosen s where the rule says so.
-// Scores and choices are formed in 64 bits, so that the order is that of the real numbers wherever two choices differ by
-// more than about 2^-50. Order keys are those doubles as unsigned integers: 0 for an expert that is off (logit or bias
-// -inf), the largest for NaN.
-// A wave takes a token; lane l holds experts l, l + 64, ...
+// The order is to be that of the real numbers. Choices are formed in fp32 first. Where those that border on each other (the
+// last chosen and the first that is not, of experts and of groups) are further apart than fp32 can be off, the order is
+// settled. The few tokens where they are not (one in 1000 of sigmoids over 256 experts) are done again, each by a whole wave,
+// with choices in 64 bits; those with NaN or infinity, by order keys of 64 bits. Weights are formed of the chosen only.
 #include "gate.h"
 
 namespace moe {
 
 namespace {
 
-constexpr int WAVES = 4;
+constexpr int WAVES = 4, LIST = 16;
 constexpr uint64_t KEY_NAN = ~0ull;
+
+// LDS that a wave's lanes exchange data through: its accesses run in the order in which they are issued, and this keeps
+// the compiler from changing that order.
+__device__ __forceinline__ void in_order() { __asm__ volatile("" ::: "memory"); }
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+// f over each run of LN lanes, in all of them
+template <int LN, typename F>
+__device__ __forceinline__ float reduce(float v, F f) {
+  auto step = [&](uint32_t o) { v = f(v, __uint_as_float(o)); };
+  if (LN > 1) step(dpp<0xB1>(__float_as_uint(v)));   // lane ^ 1
+  if (LN > 2) step(dpp<0x4E>(__float_as_uint(v)));   // lane ^ 2
+  if (LN > 4) step(dpp<0x141>(__float_as_uint(v)));  // the other half of 8
+  if (LN > 8) step(dpp<0x140>(__float_as_uint(v)));  // the other half of 16
+  if (LN > 16) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  }
+  if (LN > 32) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  }
+  return v;
+}
+__device__ __forceinline__ float larger(float a, float b) { return a > b ? a : b; }
+// The largest of an array, where none is NaN; the compiler's own form would quiet every operand first
+template <int N>
+__device__ __forceinline__ float largest(const float (&v)[N]) {
+  float m[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) m[j] = v[j];
+#pragma unroll
+  for (int n = N; n > 1; n = (n + 2) / 3) {
+#pragma unroll
+    for (int i = 0; i < (n + 2) / 3; ++i) {
+      const float a = m[3 * i], b = m[3 * i + 1 < n ? 3 * i + 1 : 3 * i], c = m[3 * i + 2 < n ? 3 * i + 2 : 3 * i];
+      if (3 * i + 1 < n) __asm__("v_max3_f32 %0, %1, %2, %3" : "=v"(m[i]) : "v"(a), "v"(b), "v"(c));
+      else m[i] = a;
+    }
+  }
+  return m[0];
+}
+// The same for the maximum of numbers, with the moves in the instruction; two wait states behind the one that wrote v
+template <int LN>
+__device__ __forceinline__ float run_max(float v) {
+#define MOE_MAX(HOW) __asm__("s_nop 1\n\tv_max_f32_dpp %0, %1, %1 " HOW " row_mask:0xf bank_mask:0xf" : "=v"(v) : "v"(v))
+  if (LN > 1) MOE_MAX("quad_perm:[1,0,3,2]");
+  if (LN > 2) MOE_MAX("quad_perm:[2,3,0,1]");
+  if (LN > 4) MOE_MAX("row_half_mirror");
+  if (LN > 8) MOE_MAX("row_mirror");
+#undef MOE_MAX
+  if (LN > 16) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = larger(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  }
+  if (LN > 32) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = larger(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  }
+  return v;
+}
+template <int LN>
+__device__ __forceinline__ float run_min(float v) { return reduce<LN>(v, [](float a, float b) { return a < b ? a : b; }); }
+template <int LN>
+__device__ __forceinline__ float run_sum(float v) { return reduce<LN>(v, [](float a, float b) { return a + b; }); }
+// The same for 64 bits, over runs of `lanes`
+template <typename F>
+__device__ __forceinline__ double reduce64(double v, int lanes, F f) {
+  auto both = [&](auto move) {
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = move((uint32_t)u), hi = move((uint32_t)(u >> 32));
+    v = f(v, __longlong_as_double((long long)((uint64_t)hi << 32 | lo)));
+  };
+  if (lanes > 1) both([](uint32_t x) { return dpp<0xB1>(x); });
+  if (lanes > 2) both([](uint32_t x) { return dpp<0x4E>(x); });
+  if (lanes > 4) both([](uint32_t x) { return dpp<0x141>(x); });
+  if (lanes > 8) both([](uint32_t x) { return dpp<0x140>(x); });
+  for (int d = 16; d < lanes; d <<= 1) both([&](uint32_t x) { return (uint32_t)__shfl_xor((int)x, d); });
+  return v;
+}
+__device__ __forceinline__ double larger64(double a, double b) { return a > b ? a : b; }
+__device__ __forceinline__ double sum64(double a, double b) { return a + b; }
 
 __device__ __forceinline__ uint64_t order_key(double v) {
   if (v != v) return KEY_NAN;
@@ -24,74 +109,92 @@ __device__ __forceinline__ double key_value(uint64_t k) {
   if (k == KEY_NAN) return __longlong_as_double(0x7FF8000000000000ll);
   return __longlong_as_double((long long)((k >> 63) ? k & ~(1ull << 63) : ~k));
 }
-
 __device__ __forceinline__ double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
+__device__ __forceinline__ float nan_max(float a, float b) { return a != a ? a : (b != b || b > a) ? b : a; }
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-  return v;
+// Place of element i of a wave's rows in LDS: 16 bytes apart every 128, so that lanes that read runs of 32 do so without
+// bank conflicts
+__host__ __device__ __forceinline__ int place(int i) { return i + 4 * (i >> 5); }
+
+struct Chosen {
+  int e;
+  float l;
+};
+
+// e^(a - b); the rounding of the difference is made up for, so that the result is off by 2^-23 of itself or little more
+__device__ __forceinline__ float exp_diff(float a, float b) {
+  const float d = a - b, z = d - a, rest = (a - (d - z)) - (b + z);
+  const float e = expf(d);
+  return d == d && rest == rest ? __builtin_fmaf(e, rest, e) : e;
 }
-// NaN if any is
-__device__ __forceinline__ float wave_max(float v) {
+
+// Weights of one token by the LN lanes q = 0.. that belong to it: list holds its n chosen in ascending order. m, inv: a
+// softmax's largest logit and 1 / sum (NaN for one of NaN or infinity).
+//   e^(x - most) / (1 + e^-|l|) for a sigmoid with x = min(l, 0), e^(l - m) for a softmax; where weights are renormalised
+//   only the ratio to the sum is taken, with the largest exponent as 0, so that scores that vanish keep their ratios
+// In fp32: about ten roundings.
+template <int LN>
+__device__ __forceinline__ void write_weights(const GateArgs& a, const Chosen* list, int n, long long t, int q, bool on, float m, float inv) {
+  constexpr int PER = LIST > LN ? LIST / LN : 1;
+  Chosen mine[PER];
+  float s[PER], sum = 0.f, top = -INFINITY;
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const float o = __shfl_xor(v, d);
-    v = v != v ? v : (o != o || o > v) ? o : v;
+  for (int i = 0; i < PER; ++i) {
+    mine[i] = Chosen{-1, -INFINITY};
+    if (q + i * LN < n) mine[i] = list[q + i * LN];
+    top = nan_max(top, a.sigmoid && mine[i].l > 0.f ? 0.f : mine[i].l);
   }
-  return v;
-}
-
-template <int PL>
-__global__ void __launch_bounds__(64 * WAVES) gate_kernel(const GateArgs a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const long long t = (long long)blockIdx.x * WAVES + wave;
-  extern __shared__ uint64_t shared_keys[];
-  uint64_t* const keys = shared_keys + (size_t)wave * a.E;
-  if (t >= a.T) return;  // no barrier below: a wave works alone
-  const int E = a.E;
-  float l[PL];
-  uint64_t key[PL];
+  float most = a.sigmoid ? 0.f : m;
+  if (a.renormalize) {
+    top = reduce<LN>(top, nan_max);
+    most = top == -INFINITY ? 0.f : top;
+  }
 #pragma unroll
-  for (int j = 0; j < PL; ++j) {
-    const int e = lane + 64 * j;
-    l[j] = -INFINITY;
-    if (e < E) {
-      float v = 0.f;
-      for (int p = 0; p < a.nparts; ++p) v += a.logits[((size_t)p * a.T + t) * a.ldl + e];
-      l[j] = v;
-      if (a.sums) a.sums[t * E + e] = v;
+  for (int i = 0; i < PER; ++i) {
+    const float v = mine[i].l;
+    s[i] = v == -INFINITY ? 0.f : exp_diff(a.sigmoid && v > 0.f ? 0.f : v, most);
+    if (a.sigmoid) s[i] /= 1.f + expf(-__builtin_fabsf(v));
+    sum += s[i];
+  }
+  const float factor = (float)a.scale * (a.renormalize ? (inv != inv ? inv : 1.f / run_sum<LN>(sum)) : inv);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int j = q + i * LN;
+    if (on && j < a.k) {
+      a.idx[t * a.k + j] = mine[i].e;
+      a.w[t * a.k + j] = j < n ? s[i] * factor : 0.f;
     }
   }
-  double m = 0.0, inv = 1.0;  // softmax: s = e^(l - m) inv
+}
+
+// One token by a whole wave, with choices in 64 bits: row(e) is its logit, keys an array of E in LDS. Order keys are the
+// choices as unsigned integers: 0 for an expert that is off (logit or bias -inf), the largest for NaN.
+template <typename Row>
+__device__ void ordered_token(const GateArgs& a, long long t, Row row, uint64_t* keys, Chosen* list) {
+  const int lane = threadIdx.x & 63, E = a.E;
+  float m = 0.f;
+  double inv = 1.0;
   if (!a.sigmoid) {
-    float top = l[0];
-#pragma unroll
-    for (int j = 1; j < PL; ++j) top = top != top ? top : (l[j] != l[j] || l[j] > top) ? l[j] : top;
-    top = wave_max(top);
-    m = top == -INFINITY ? 0.0 : (double)top;
+    float top = -INFINITY;
+    for (int e = lane; e < E; e += 64) top = nan_max(top, row(e));
+    top = reduce<64>(top, nan_max);
+    m = top == -INFINITY ? 0.f : top;
     double z = 0.0;
-#pragma unroll
-    for (int j = 0; j < PL; ++j) z += l[j] == -INFINITY ? 0.0 : exp((double)l[j] - m);
-    inv = 1.0 / wave_sum(z);
+    for (int e = lane; e < E; e += 64) z += row(e) == -INFINITY ? 0.0 : exp((double)row(e) - (double)m);
+    inv = 1.0 / reduce64(z, 64, sum64);
   }
-  const bool by_score = a.bias || (a.groups > 1 && a.group_top == 2);
-#pragma unroll
-  for (int j = 0; j < PL; ++j) {
-    const int e = lane + 64 * j;
-    key[j] = 0;
-    if (e >= E || l[j] == -INFINITY) continue;
-    const float b = a.bias ? a.bias[e] : 0.f;
-    if (b == -INFINITY) continue;
-    const double s = !by_score ? (double)l[j] : a.sigmoid ? sigmoid64(l[j]) : exp((double)l[j] - m) * inv;
-    key[j] = order_key(s + (double)b);
-  }
+  auto key_of = [&](int e, bool score) {
+    const float l = row(e), b = a.bias ? a.bias[e] : 0.f;
+    if (l == -INFINITY || b == -INFINITY) return (uint64_t)0;
+    const double s = !score ? (double)l : a.sigmoid ? sigmoid64(l) : exp((double)l - (double)m) * inv;
+    return order_key(s + (double)b);
+  };
+  in_order();
+  const bool pairs = a.groups > 1 && a.group_top == 2;
+  for (int e = lane; e < E; e += 64) keys[e] = key_of(e, a.bias || pairs);
+  in_order();
   if (a.groups > 1) {
     const int n = E / a.groups;
-#pragma unroll
-    for (int j = 0; j < PL; ++j)
-      if (lane + 64 * j < E) keys[lane + 64 * j] = key[j];
-    __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     uint64_t mine = 0;
     if (lane < a.groups) {
       uint64_t first = 0, second = 0;
@@ -104,7 +207,7 @@ __global__ void __launch_bounds__(64 * WAVES) gate_kernel(const GateArgs a) {
           second = v;
         }
       }
-      mine = a.group_top == 2 && second ? order_key(key_value(first) + key_value(second)) : first;
+      mine = pairs && second ? order_key(key_value(first) + key_value(second)) : first;
     }
     int rank = 0;
     for (int g = 0; g < a.groups; ++g) {
@@ -112,23 +215,25 @@ __global__ void __launch_bounds__(64 * WAVES) gate_kernel(const GateArgs a) {
       rank += v > mine || (v == mine && g < lane);
     }
     const uint64_t stays = __ballot(lane < a.groups && rank < a.top_groups);
-#pragma unroll
-    for (int j = 0; j < PL; ++j)
-      if (lane + 64 * j < E && !((stays >> ((lane + 64 * j) / n)) & 1)) key[j] = 0;
-    // the scores were needed for the groups only: without a bias the logits order the experts
+    in_order();
+    for (int e = lane; e < E; e += 64) {
+      if (!((stays >> (e / n)) & 1)) keys[e] = 0;
+      else if (pairs && !a.bias) keys[e] = key_of(e, false);  // the logits order the experts
+    }
+    in_order();
   }
-  // k rounds: the largest key, the lowest index among equals
-  uint32_t taken = 0;  // of this lane's experts
-  int left = a.k;
-  for (int r = 0; r < a.k; ++r) {
+  // k rounds: the largest key, the lowest index among equals; lane r keeps the r-th
+  int n = 0, mine = 1 << 30;
+  for (; n < a.k; ++n) {
     uint64_t best = 0;
     int at = 1 << 30;
-#pragma unroll
-    for (int j = 0; j < PL; ++j)
-      if (!((taken >> j) & 1) && key[j] > best) {
-        best = key[j];
-        at = lane + 64 * j;
+    for (int e = lane; e < E; e += 64) {
+      const uint64_t v = keys[e];
+      if (v > best) {
+        best = v;
+        at = e;
       }
+    }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const uint64_t v = __shfl_xor(best, d);
@@ -139,145 +244,511 @@ __global__ void __launch_bounds__(64 * WAVES) gate_kernel(const GateArgs a) {
       }
     }
     if (best == 0) break;
-    --left;
-    if ((at & 63) == lane) taken |= 1u << (at >> 6);
+    in_order();
+    if ((at & 63) == lane) keys[at] = 0;
+    in_order();
+    if (lane == n) mine = at;
   }
-  // weights: e^(x - most) / (1 + e^-|l|) for a sigmoid with x = min(l, 0), e^(l - m) for a softmax; only the ratio
-  // to the sum is taken where weights are renormalised, with the largest exponent as 0
-  double most = m;
-  if (a.renormalize) {
-    float top = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < PL; ++j)
-      if ((taken >> j) & 1) {
-        const float x = a.sigmoid && l[j] > 0.f ? 0.f : l[j];
-        top = top != top ? top : (x != x || x > top) ? x : top;
-      }
-    top = wave_max(top);
-    most = top == -INFINITY ? 0.0 : (double)top;
+  int rank = 0;
+  for (int i = 0; i < n; ++i) rank += __shfl(mine, i) < mine;
+  in_order();
+  if (lane < n) list[rank] = Chosen{mine, row(mine)};
+  in_order();
+  write_weights<64>(a, list, n, t, lane, true, m, (float)inv);
+  in_order();
+}
+
+// Bytes of LDS of a wave that takes `tokens`: their rows, a list each, the keys of one
+__host__ __device__ __forceinline__ int tile_floats(const GateArgs& a, int tokens) { return (place(tokens * a.ldl) + 7) / 4 * 4; }
+__host__ __device__ __forceinline__ int wave_bytes(const GateArgs& a, int tokens) {
+  return tile_floats(a, tokens) * 4 + tokens * LIST * (int)sizeof(Chosen) + (a.E + 1) / 2 * 16;
+}
+
+// The rows of a wave's tokens, with their parts added, to LDS and to sums
+__device__ __forceinline__ void stage(const GateArgs& a, long long t0, int tokens, float* tile) {
+  const int lane = threadIdx.x & 63, n = tokens * a.ldl;
+  const float* const from = a.logits + t0 * a.ldl;
+  const size_t part = (size_t)a.T * a.ldl;
+  if (a.whole) {
+    for (int i = 4 * lane; i < n; i += 256) {
+      f32x4 v = *(const f32x4*)(from + i);
+      for (int p = 1; p < a.nparts; ++p) v += *(const f32x4*)(from + p * part + i);
+      *(f32x4*)(tile + place(i)) = v;
+    }
+  } else {
+    for (int i = lane; i < n; i += 64) {
+      float v = from[i];
+      for (int p = 1; p < a.nparts; ++p) v += from[p * part + i];
+      tile[place(i)] = v;
+    }
   }
-  double s[PL], sum = 0.0;
+  in_order();
+  if (a.sums)
+    for (int i = lane; i < tokens * a.E; i += 64) a.sums[t0 * a.E + i] = tile[place(i / a.E * a.ldl + i % a.E)];
+}
+
+__host__ __device__ __forceinline__ int backward_wave_bytes(const GateArgs& a) {
+  return (64 / LIST * a.E + 3) / 4 * 16 + 64 * (int)sizeof(Chosen);
+}
+
+__global__ void __launch_bounds__(64 * WAVES) gate_exact_kernel(const GateArgs a) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  const int wave = threadIdx.x >> 6;
+  const long long t = (long long)blockIdx.x * WAVES + wave;
+  if (t >= a.T) return;  // no barrier below: a wave works alone
+  float* const tile = (float*)(lds + (size_t)wave * wave_bytes(a, 1));
+  Chosen* const list = (Chosen*)(tile + tile_floats(a, 1));
+  stage(a, t, 1, tile);
+  ordered_token(a, t, [&](int e) { return tile[place(e)]; }, (uint64_t*)(list + LIST), list);
+}
+
+// Where a lane's experts are: those of one group follow each other in its LN / groups lanes, so that lanes and places
+// within a lane are in the experts' order.
+struct Place {
+  int size, lanes, per, g, e0, n;  // experts and lanes of a group, experts of a lane; this lane's group, first expert and experts
+};
+template <int LN>
+__device__ __forceinline__ Place place_of(const GateArgs& a, int q, bool on) {
+  Place p;
+  p.size = a.E / a.groups;
+  p.lanes = LN / a.groups;
+  p.per = (p.size + p.lanes - 1) / p.lanes;
+  p.g = q / p.lanes;
+  const int before = q % p.lanes * p.per;
+  p.e0 = p.g * p.size + before;
+  p.n = !on || before >= p.size ? 0 : p.size - before < p.per ? p.size - before : p.per;
+  return p;
+}
+
+// Whether the lane's group is one of the best: worth is the same in all lanes of a group
+template <int LN>
+__device__ __forceinline__ bool group_stays(const GateArgs& a, const Place& p, float worth, int first_lane) {
+  int rank = 0;
+  for (int o = 0; o < a.groups; ++o) {
+    const float w = __shfl(worth, first_lane + o * p.lanes);
+    rank += w > worth || (w == worth && o < p.g);
+  }
+  return rank < a.top_groups;
+}
+
+// The two largest of v over the lanes of a group
+template <int PL>
+__device__ __forceinline__ void two_largest(const float (&v)[PL], int lanes, float& first, float& second) {
+  first = second = -INFINITY;
 #pragma unroll
   for (int j = 0; j < PL; ++j) {
-    s[j] = 0.0;
-    if ((taken >> j) & 1) {
-      const double v = l[j];
-      if (!a.sigmoid) s[j] = exp(v - most);
-      else if (!a.renormalize) s[j] = sigmoid64(v);
-      else s[j] = exp((v > 0.0 ? 0.0 : v) - most) / (1.0 + exp(-__builtin_fabs(v)));
-    }
-    sum += s[j];
+    second = __builtin_amdgcn_fmed3f(first, second, v[j]);
+    first = larger(first, v[j]);
   }
-  // inv is NaN for a softmax of NaN or infinity
-  const double factor = a.scale * (a.renormalize ? (inv != inv ? inv : 1.0 / wave_sum(sum)) : inv);
-  int base = 0;
-#pragma unroll
-  for (int j = 0; j < PL; ++j) {
-    const uint64_t pick = __ballot((taken >> j) & 1);
-    if ((taken >> j) & 1) {
-      const int rank = base + __popcll(pick & ((1ull << lane) - 1));
-      a.idx[t * a.k + rank] = lane + 64 * j;
-      a.w[t * a.k + rank] = (float)(s[j] * factor);
-    }
-    base += __popcll(pick);
-  }
-  if (lane >= a.k - left && lane < a.k) {
-    a.idx[t * a.k + lane] = -1;
-    a.w[t * a.k + lane] = 0.f;
+  for (int d = 1; d < lanes; d <<= 1) {
+    const float f = __shfl_xor(first, d), s = __shfl_xor(second, d);
+    second = larger(__builtin_amdgcn_fmed3f(first, second, f), s);
+    first = larger(first, f);
   }
 }
 
-// dl_e = ds/dl by the chosen weights' gradient; r_j = s_j / (sum of the chosen s):
-//   sigmoid, renormalised  scale r_j (1 - s_j) (dw_j - sum_i r_i dw_i)      else  scale s_j (1 - s_j) dw_j
-//   softmax, renormalised  scale r_j (dw_j - sum_i r_i dw_i)                else  scale p_e ([e chosen] dw_e - sum_i p_i dw_i)
-// Lane j < k holds the j-th chosen expert; every lane then writes the experts lane, lane + 64, ...
+// Bit j: v[j] is -inf
+template <int PL>
+__device__ __forceinline__ uint32_t lowest_bits(const float (&v)[PL]) {
+  uint32_t bits = 0;
+#pragma unroll
+  for (int j = PL - 1; j >= 0; --j)
+    __asm__("v_cmp_eq_f32 vcc, %1, %2\n\tv_addc_co_u32 %0, vcc, %0, %0, vcc" : "+v"(bits) : "v"(v[j]), "v"(-INFINITY) : "vcc");
+  return bits;
+}
+
+// k rounds, each of which takes the largest v of a token's LN lanes away. taken: bits of this lane's; got: rounds that found
+// one; top and last: the first and the last that was taken; left: the largest that stays. Equal ones go in one round: then
+// more are taken than rounds, which the caller has to look for.
+struct Rounds {
+  uint32_t taken;
+  int got;
+  float top, last, left;
+};
+template <int LN, int PL>
+__device__ __forceinline__ Rounds take_largest(float (&v)[PL], int k) {
+  Rounds r{0u, 0, -INFINITY, -INFINITY, -INFINITY};
+  const uint32_t off = lowest_bits(v);
+  for (int i = 0;; ++i) {
+    const float best = run_max<LN>(largest(v));
+    r.left = best;
+    if (i == k) break;
+    const bool has = best > -INFINITY;
+    r.got += has;
+    r.last = has ? best : r.last;
+    r.top = i == 0 ? best : r.top;
+#pragma unroll
+    for (int j = 0; j < PL; ++j) v[j] = v[j] == best ? -INFINITY : v[j];
+  }
+  r.taken = lowest_bits(v) & ~off;
+  return r;
+}
+
+// The taken experts of a token to its list, in ascending order
+// (at most LIST of them); returns how many there are
+template <int LN, typename Row>
+__device__ __forceinline__ int write_list(uint32_t taken, int q, int e0, Row row, Chosen* list) {
+  const int count = __popc(taken);
+  int upto = count;
+#pragma unroll
+  for (int d = 1; d < LN; d <<= 1) {
+    const int o = __shfl_up(upto, d, LN);
+    if (q >= d) upto += o;
+  }
+  int at = upto - count;
+  in_order();
+  while (taken && at < LIST) {
+    const int j = __ffs((int)taken) - 1;
+    taken &= taken - 1;
+    list[at++] = Chosen{e0 + j, row(e0 + j)};
+  }
+  in_order();
+  return __shfl(upto, LN - 1, LN);
+}
+
+// One token by a whole wave, without NaN or infinity, where fp32 leaves the order open: choices in 64 bits
+template <int PL, typename Row>
+__device__ __forceinline__ void exact_token(const GateArgs& a, long long t, Row row, Chosen* list, float m) {
+  const int lane = threadIdx.x & 63;
+  const Place p = place_of<64>(a, lane, true);
+  double c[PL], inv = 1.0, z = 0.0;
+#pragma unroll
+  for (int j = 0; j < PL; ++j) {
+    const double l = j < p.n ? row(p.e0 + j) : -INFINITY;
+    c[j] = a.sigmoid ? sigmoid64(l) : exp(l - (double)m);
+    z += c[j];
+  }
+  if (!a.sigmoid) inv = 1.0 / reduce64(z, 64, sum64);
+#pragma unroll
+  for (int j = 0; j < PL; ++j)
+    c[j] = j < p.n && row(p.e0 + j) > -INFINITY ? c[j] * inv + (a.bias ? (double)a.bias[p.e0 + j] : 0.0) : -INFINITY;
+  if (a.groups > 1) {
+    // the largest of the group, and the largest of the others: all but the first place that has it
+    double here = c[0];
+#pragma unroll
+    for (int j = 1; j < PL; ++j) here = larger64(here, c[j]);
+    const double first = reduce64(here, p.lanes, larger64);
+    double worth = first;
+    if (a.group_top == 2) {
+      const uint64_t has = __ballot(here == first) >> (p.g * p.lanes) & (~0ull >> (64 - p.lanes));
+      bool skip = lane - p.g * p.lanes == __ffsll((long long)has) - 1;
+      double second = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < PL; ++j) {
+        const bool it = skip && c[j] == first;
+        skip = skip && !it;
+        second = it ? second : larger64(second, c[j]);
+      }
+      second = reduce64(second, p.lanes, larger64);
+      worth = second > -INFINITY ? first + second : first;
+    }
+    int rank = 0;
+    for (int o = 0; o < a.groups; ++o) {
+      const double w = __shfl(worth, o * p.lanes);
+      rank += w > worth || (w == worth && o < p.g);
+    }
+#pragma unroll
+    for (int j = 0; j < PL; ++j) {
+      if (rank >= a.top_groups) c[j] = -INFINITY;
+      else if (!a.bias && c[j] > -INFINITY) c[j] = row(p.e0 + j);  // the logits order the experts
+    }
+  }
+  uint32_t taken = 0;
+  int got = 0;
+  for (; got < a.k; ++got) {
+    double here = c[0];
+#pragma unroll
+    for (int j = 1; j < PL; ++j) here = larger64(here, c[j]);
+    const double best = reduce64(here, 64, larger64);
+    if (!(best > -INFINITY)) break;
+    bool take = __ffsll((long long)__ballot(here == best)) - 1 == lane;
+#pragma unroll
+    for (int j = 0; j < PL; ++j) {
+      const bool it = take && c[j] == best;
+      c[j] = it ? -INFINITY : c[j];
+      taken |= it ? 1u << j : 0u;
+      take = take && !it;
+    }
+  }
+  write_list<64>(taken, lane, p.e0, row, list);
+  write_weights<64>(a, list, got, t, lane, true, m, (float)inv);
+  in_order();
+}
+
+// LN lanes a token, up to PL experts a lane; 64 / LN tokens take their rounds together. Few lanes a token share the
+// reductions over lanes among more tokens, many make a token's rounds shorter. XPL: experts of a lane where 64 take a token.
+template <int LN, int PL, int XPL>
+__global__ void __launch_bounds__(64 * WAVES) gate_kernel(const GateArgs a) {
+  constexpr int TOKENS = 64 / LN;
+  extern __shared__ __align__(16) uint8_t lds[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane % LN, mine = lane / LN, first_lane = mine * LN;
+  const long long t0 = ((long long)blockIdx.x * WAVES + wave) * TOKENS;
+  if (t0 >= a.T) return;  // no barrier below: a wave works alone
+  const int tokens = a.T - t0 < TOKENS ? (int)(a.T - t0) : TOKENS;
+  const bool on = mine < tokens;
+  float* const tile = (float*)(lds + (size_t)wave * wave_bytes(a, TOKENS));
+  Chosen* const lists = (Chosen*)(tile + tile_floats(a, TOKENS));
+  const Place p = place_of<LN>(a, q, on);
+  const int row = mine * a.ldl + p.e0;
+  const bool fours = a.whole && p.size % 4 == 0 && p.per % 4 == 0;  // and so are all numbers and places
+  float l[PL], v[PL];
+#pragma unroll
+  for (int j = 0; j < PL; ++j) v[j] = 0.f;
+  if (a.bias && fours) {
+#pragma unroll
+    for (int j = 0; j < PL; j += 4)
+      if (j < p.n) {
+        const f32x4 x = *(const f32x4*)(a.bias + p.e0 + j);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) v[j + z] = x[z];
+      }
+  } else if (a.bias) {
+#pragma unroll
+    for (int j = 0; j < PL; ++j)
+      if (j < p.n) v[j] = a.bias[p.e0 + j];
+  }
+  stage(a, t0, tokens, tile);
+  if (fours) {
+#pragma unroll
+    for (int j = 0; j < PL; j += 4) {
+      const f32x4 x = *(const f32x4*)(tile + place(j < p.n ? row + j : 0));
+#pragma unroll
+      for (int z = 0; z < 4; ++z) l[j + z] = j < p.n ? x[z] : -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < PL; ++j) {
+      const float x = tile[place(j < p.n ? row + j : 0)];
+      l[j] = j < p.n ? x : -INFINITY;
+    }
+  }
+
+  bool unsure = false, strange = false;
+  float m = 0.f, inv = 1.f, top = 1.f;  // top: the largest score that there may be
+  const bool pairs = a.groups > 1 && a.group_top == 2, scored = a.bias || pairs;
+  const float inv_log2 = 1.4426950408889634f;
+  if (!a.sigmoid && (scored || !a.renormalize)) {
+    m = run_max<LN>(largest(l));
+    strange = m == INFINITY;
+    m = m == -INFINITY ? 0.f : m;
+    double z[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+    for (int j = 0; j < PL; ++j) z[j % 4] += (double)__builtin_amdgcn_exp2f((l[j] - m) * inv_log2);
+    inv = top = (float)(1.0 / reduce64((z[0] + z[1]) + (z[2] + z[3]), LN, sum64));
+  }
+  // fp32 choices of size c are off by less than tol(c) / 3: the sum with b by 2^-24 of c; the score by 2^-22 of top, of which
+  // a sigmoid's 1 + e and its reciprocal make 2^-24 and 2^-23, and e, 2^-23 by itself and |x| 2^-23.4 by its argument, makes
+  // s (1 - s) times that, 0.42 2^-23 at most; a softmax's e^x likewise, with e^x |x| < 0.37, and 1 / sum 2^-23.
+  auto tol = [&](float c) { return 0x1.8p-21f * top + 0x1.8p-23f * __builtin_fabsf(c); };
+  bool nan = false;
+#pragma unroll
+  for (int j = 0; j < PL; ++j) {
+    float c = l[j];
+    if (scored) {
+      const float x = __builtin_amdgcn_exp2f((a.sigmoid ? -l[j] : l[j] - m) * inv_log2);
+      const float s = a.sigmoid ? __builtin_amdgcn_rcpf(1.f + x) : x * top;
+      c = s + v[j];
+      c = l[j] == -INFINITY ? -INFINITY : c;
+    }
+    nan |= c != c;
+    v[j] = c;
+  }
+  strange |= run_max<LN>(nan ? 1.f : 0.f) > 0.f;
+  if (a.groups > 1) {
+    float first, second;
+    two_largest<PL>(v, p.lanes, first, second);
+    const float worth = pairs && second > -INFINITY ? first + second : first;
+    const bool stays = group_stays<LN>(a, p, worth, first_lane);
+    if (scored) {
+      const float low = run_min<LN>(stays ? worth : INFINITY), high = run_max<LN>(stays ? -INFINITY : worth);
+      unsure |= high > -INFINITY && low - high <= 2.f * tol(low);
+    }
+#pragma unroll
+    for (int j = 0; j < PL; ++j) v[j] = !stays || v[j] == -INFINITY ? -INFINITY : pairs && !a.bias ? l[j] : v[j];
+  }
+  const Rounds r = take_largest<LN, PL>(v, a.k);
+  if (a.bias) unsure |= r.got == a.k && r.left > -INFINITY && r.last - r.left <= tol(r.last);
+  // infinite choices have no differences, and an infinite logit makes its softmax's weights NaN
+  strange |= r.top == INFINITY && (!a.sigmoid || a.bias);
+  Chosen* const list = lists + mine * LIST;
+  unsure |= write_list<LN>(r.taken, q, p.e0, [&](int e) { return tile[place(mine * a.ldl + e)]; }, list) > r.got;
+  write_weights<LN>(a, list, r.got, t0 + mine, q, on && !unsure && !strange, m, inv);
+  in_order();
+  const uint64_t open = __ballot(unsure && !strange && on && q == 0), odd = __ballot(strange && on && q == 0);
+  for (uint64_t again = open | odd; again; again &= again - 1) {
+    const int at = __ffsll((long long)again) - 1, i = at / LN;
+    auto from = [&](int e) { return tile[place(i * a.ldl + e)]; };
+    if ((open >> at) & 1) {
+      exact_token<XPL>(a, t0 + i, from, lists + i * LIST, __shfl(m, at));
+    } else {
+      ordered_token(a, t0 + i, from, (uint64_t*)(lists + TOKENS * LIST), lists + i * LIST);
+    }
+  }
+}
+
+// The gradient, for r_j = s_j / (sum of the chosen s):
+//   sigmoid, renormalised  dl_j = scale r_j (1 - s_j) (dw_j - sum_i r_i dw_i)    else  scale s_j (1 - s_j) dw_j
+//   softmax, renormalised  dl_j = scale r_j (dw_j - sum_i r_i dw_i)              else  scale p_e ([e chosen] dw_e - sum_i p_i dw_i)
+// 0 elsewhere in the first three, which read the chosen logits only and are bound by writing zeros.
+
+// An entry of a token: its expert (negative: it takes no part) and gradient
+struct Entry {
+  int e;
+  float d;
+};
+
+// The forms with zeros: 16 lanes a token. Rows are put together in LDS and written 16 bytes a lane.
 __global__ void __launch_bounds__(64 * WAVES) gate_backward_kernel(const GateArgs a) {
+  constexpr int LN = LIST, TOKENS = 64 / LN;
+  extern __shared__ __align__(16) uint8_t lds[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane % LN, mine = lane / LN, E = a.E, k = a.k;
+  const long long t0 = ((long long)blockIdx.x * (blockDim.x >> 6) + wave) * TOKENS, t = t0 + mine;
+  if (t0 >= a.T) return;  // no barrier below: a wave works alone
+  const int n = (int)(a.T - t0 < TOKENS ? a.T - t0 : TOKENS) * E;  // elements of the wave's rows
+  float* const tile = (float*)(lds + (size_t)wave * backward_wave_bytes(a));
+  Entry* const list = (Entry*)(tile + (TOKENS * E + 3) / 4 * 4) + mine * LIST;
+  int e = -1;
+  float dw = 0.f, l = -INFINITY;
+  if (t < a.T && q < k) {
+    e = a.chosen[t * k + q];
+    dw = a.dw[t * k + q];
+  }
+  for (int i = 4 * lane; i < TOKENS * E; i += 256) *(f32x4*)(tile + i) = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (e >= 0 && e < E) l = a.logits[t * E + e];
+  const bool here = l != -INFINITY;  // takes part
+  dw = here ? dw : 0.f;
+  // r, and 1 - s for a sigmoid, both to a few roundings however far the logit is
+  const float x = a.sigmoid && l > 0.f ? 0.f : l;
+  float most = 0.f;
+  if (a.renormalize) {
+    const float top = reduce<LN>(here ? x : -INFINITY, nan_max);
+    most = top == -INFINITY ? 0.f : top;
+  }
+  float r = here ? exp_diff(x, most) : 0.f, rest = 1.f;
+  if (a.sigmoid && here) {
+    const float small = expf(-__builtin_fabsf(l)), f = 1.f / (1.f + small);
+    r *= f;
+    rest = (l > 0.f ? small : 1.f) * f;
+  }
+  float d = dw;
+  if (a.renormalize) {
+    r *= 1.f / run_sum<LN>(r);
+    r = here ? r : 0.f;
+    // dw less its mean: products and sum in 64 bits, since the two may nearly be the same
+    d = (float)((double)dw - reduce64((double)r * dw, LN, sum64));
+  }
+  d = here ? (float)a.scale * r * rest * d : 0.f;
+  list[q] = Entry{here ? e : -1 - q, d};
+  in_order();
+  if (here) {
+    float sum = 0.f;
+    bool first = true;
+    for (int i = 0; i < k; ++i) {
+      const Entry o = list[i];
+      sum += o.e == e ? o.d : 0.f;
+      first = first && (o.e != e || i >= q);
+    }
+    if (first) tile[mine * E + e] = sum;
+  }
+  in_order();
+  float* const to = a.dlogits + t0 * E;
+  if (a.whole) {
+    for (int i = 4 * lane; i < n; i += 256) *(f32x4*)(to + i) = *(const f32x4*)(tile + i);
+  } else {
+    for (int i = lane; i < n; i += 64) to[i] = tile[i];
+  }
+}
+
+// A softmax that is not renormalised: a wave a token, experts lane, lane + 64, ...
+template <int PL>
+__global__ void __launch_bounds__(64 * WAVES) gate_backward_dense_kernel(const GateArgs a) {
+  __shared__ Entry lists[WAVES][LIST];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, E = a.E, k = a.k;
   const long long t = (long long)blockIdx.x * WAVES + wave;
-  if (t >= a.T) return;
-  const float* const row = a.logits + t * a.ldl;
-  const bool dense = !a.sigmoid && !a.renormalize;
+  if (t >= a.T) return;  // no barrier below: a wave works alone
+  const float* const row = a.logits + t * E;
   int e = -1;
-  float l = -INFINITY;
-  double dw = 0.0;
+  float dw = 0.f, l[PL], p[PL], top = -INFINITY;
   if (lane < k) {
     e = a.chosen[t * k + lane];
-    if (e < 0 || e >= E) e = -1;
-    else l = row[e];
-    if (l == -INFINITY) e = -1;
-    if (e >= 0) dw = a.dw[t * k + lane];
+    dw = a.dw[t * k + lane];
   }
-  double m = 0.0, inv = 1.0;
-  if (dense) {
-    float top = -INFINITY;
-    for (int i = lane; i < E; i += 64) {
-      const float v = row[i];
-      top = top != top ? top : (v != v || v > top) ? v : top;
-    }
-    top = wave_max(top);
-    m = top == -INFINITY ? 0.0 : (double)top;
-    double z = 0.0;
-    for (int i = lane; i < E; i += 64) z += row[i] == -INFINITY ? 0.0 : exp((double)row[i] - m);
-    inv = 1.0 / wave_sum(z);
-  } else if (a.renormalize) {
-    const float x = a.sigmoid && l > 0.f ? 0.f : l;
-    const float top = wave_max(e >= 0 ? x : -INFINITY);
-    m = top == -INFINITY ? 0.0 : (double)top;
+#pragma unroll
+  for (int j = 0; j < PL; ++j) {
+    l[j] = lane + 64 * j < E ? row[lane + 64 * j] : -INFINITY;
+    top = nan_max(top, l[j]);
   }
-  double r = 0.0, rest = 1.0;  // score (over the sum), 1 - score
-  if (e >= 0) {
-    const double v = l;
-    if (!a.sigmoid) {
-      r = exp(v - m) * inv;
-    } else {
-      const double q = exp(-__builtin_fabs(v));
-      rest = (v > 0.0 ? q : 1.0) / (1.0 + q);
-      r = a.renormalize ? exp((v > 0.0 ? 0.0 : v) - m) / (1.0 + q) : (v > 0.0 ? 1.0 : q) / (1.0 + q);
-    }
+  const float at = e >= 0 && e < E ? row[e] : -INFINITY;
+  const bool here = at != -INFINITY;
+  top = reduce<64>(top, nan_max);
+  const float m = top == -INFINITY ? 0.f : top;
+  float z = 0.f;
+#pragma unroll
+  for (int j = 0; j < PL; ++j) {
+    p[j] = l[j] == -INFINITY ? 0.f : exp_diff(l[j], m);
+    z += p[j];
   }
-  if (a.renormalize) {
-    const double z = wave_sum(r);
-    r = e >= 0 ? r / z : 0.0;
+  const float inv = 1.f / run_sum<64>(z);
+  const double mean = reduce64(here ? (double)dw * exp_diff(at, m) * inv : 0.0, 64, sum64);
+  Entry* const list = lists[wave];
+  if (lane < LIST) list[lane] = Entry{here ? e : -1, dw};
+  in_order();
+#pragma unroll
+  for (int j = 0; j < PL; ++j) {
+    const int i = lane + 64 * j;
+    float sum = 0.f;
+    for (int o = 0; o < k; ++o) sum += list[o].e == i ? list[o].d : 0.f;
+    if (i < E) a.dlogits[t * E + i] = l[j] == -INFINITY ? 0.f : (float)a.scale * (p[j] * inv) * (float)((double)sum - mean);
   }
-  const double mean = a.renormalize || dense ? wave_sum(r * dw) : 0.0;
-  double d;
-  if (dense) d = dw;
-  else d = a.scale * r * (a.sigmoid ? rest : 1.0) * (dw - mean);
-  if (e < 0) d = 0.0;
-  for (int i0 = 0; i0 < E; i0 += 64) {
-    const int i = i0 + lane;
-    double out = 0.0;
-    for (int j = 0; j < k; ++j) {
-      const int ej = __shfl(e, j);
-      const double dj = __shfl(d, j);
-      if (ej == i) out += dj;
-    }
-    if (i >= E) break;
-    if (dense) out = row[i] == -INFINITY ? 0.0 : a.scale * exp((double)row[i] - m) * inv * (out - mean);
-    a.dlogits[t * E + i] = (float)out;
-  }
+}
+
+template <int LN, int PL, int XPL>
+void launch(const GateArgs& a, hipStream_t st) {
+  constexpr int TOKENS = 64 / LN * WAVES;
+  gate_kernel<LN, PL, XPL><<<dim3((unsigned)((a.T + TOKENS - 1) / TOKENS)), dim3(64 * WAVES), WAVES * wave_bytes(a, 64 / LN), st>>>(a);
 }
 
 }  // namespace
 
-hipError_t launch_gate(const GateArgs& a, hipStream_t st) {
+hipError_t launch_gate(const GateArgs& args, hipStream_t st) {
+  GateArgs a = args;
   if (a.T == 0) return hipSuccess;
-  const dim3 grid((unsigned)((a.T + WAVES - 1) / WAVES)), block(64 * WAVES);
-  const size_t lds = a.groups > 1 ? (size_t)WAVES * a.E * 8 : 0;
-  const int pl = (a.E + 63) / 64;
-#define MOE_GATE(PL) gate_kernel<PL><<<grid, block, lds, st>>>(a)
-  if (pl <= 1) MOE_GATE(1);
-  else if (pl <= 2) MOE_GATE(2);
-  else if (pl <= 4) MOE_GATE(4);
-  else if (pl <= 8) MOE_GATE(8);
-  else MOE_GATE(16);
-#undef MOE_GATE
+  a.whole = a.ldl % 4 == 0 && (uintptr_t)a.logits % 16 == 0 && (uintptr_t)a.bias % 16 == 0;
+  if (a.groups & (a.groups - 1)) {  // groups that share no run of lanes evenly
+    gate_exact_kernel<<<dim3((unsigned)((a.T + WAVES - 1) / WAVES)), dim3(64 * WAVES), WAVES * wave_bytes(a, 1), st>>>(a);
+    return hipGetLastError();
+  }
+  // Lanes of a token. A wave a token is the shortest way for few tokens; for many, 8 to 16 experts a lane. 256 experts in 8
+  // groups: 2048 tokens 7.5 us by 64 lanes each, 8.5 by 16; 16384 tokens 29.6 by 64, 20.7 by 32, 17.2 by 16, 21.4 by 8. 64
+  // experts, 16384 tokens: 6.1 us by 8 lanes, 9.4 by 16.
+  int ln = a.T <= 2048 ? 64 : a.E <= 128 ? 8 : a.E <= 256 ? 16 : a.E <= 512 ? 32 : 64;
+  if (ln < a.groups) ln = a.groups;
+  const int lanes = ln / a.groups, per = (a.E / a.groups + lanes - 1) / lanes;  // lanes of a group, experts of a lane
+  if (ln == 8 && per <= 8) launch<8, 8, 4>(a, st);
+  else if (ln == 8) launch<8, 16, 4>(a, st);
+  else if (ln == 16) launch<16, 16, 4>(a, st);
+  else if (ln == 32) launch<32, 16, 8>(a, st);
+  else if (per <= 4) launch<64, 4, 4>(a, st);
+  else if (per <= 8) launch<64, 8, 8>(a, st);
+  else launch<64, 16, 16>(a, st);
   return hipGetLastError();
 }
 
-hipError_t launch_gate_backward(const GateArgs& a, hipStream_t st) {
+hipError_t launch_gate_backward(const GateArgs& args, hipStream_t st) {
+  GateArgs a = args;
   if (a.T == 0) return hipSuccess;
-  gate_backward_kernel<<<dim3((unsigned)((a.T + WAVES - 1) / WAVES)), dim3(64 * WAVES), 0, st>>>(a);
+  a.whole = a.E % 4 == 0 && (uintptr_t)a.dlogits % 16 == 0;
+  if (a.sigmoid || a.renormalize) {
+    const int waves = a.E <= 512 ? WAVES : WAVES / 2, tokens = 64 / LIST * waves;  // at most 34 KiB of LDS
+    gate_backward_kernel<<<dim3((unsigned)((a.T + tokens - 1) / tokens)), dim3(64 * waves), waves * backward_wave_bytes(a), st>>>(a);
+    return hipGetLastError();
+  }
+  const dim3 grid((unsigned)((a.T + WAVES - 1) / WAVES)), block(64 * WAVES);
+  const int pl = (a.E + 63) / 64;
+  if (pl <= 2) gate_backward_dense_kernel<2><<<grid, block, 0, st>>>(a);
+  else if (pl <= 4) gate_backward_dense_kernel<4><<<grid, block, 0, st>>>(a);
+  else if (pl <= 8) gate_backward_dense_kernel<8><<<grid, block, 0, st>>>(a);
+  else gate_backward_dense_kernel<16><<<grid, block, 0, st>>>(a);
   return hipGetLastError();
 }
 

@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const
       constexpr int ph = decltype(ph_c)::value, each = S::count(ph);
       constexpr std::integral_constant<int, (decltype(slot)::value + D - 1) % D> before{};
       const bool is_p = KC ? n >= each : n < each;
-      const int u = S::from(ph) + n % each;
+      const int u = S::from(ph) + (is_p == KC ? n - each : n);
       // phase 0, and phase 1 for whole slots, still bring stage s + D - 1, into the slot of step s - 1
       if constexpr (ph == 0 || (KC && ph == 1)) {
         if (is_p) load_p(u, s + D - 1, before);
