@@ -113,6 +113,10 @@ hipError_t run_class(MuonArgs a, const Class& c, const moe_newton_schulz& ns, in
   a.A_lo = (uint16_t*)(w + c.A_lo);
   a.C = (uint16_t*)(w + c.C);
   a.C_lo = (uint16_t*)(w + c.C_lo);
+  if (muon_small(c.M, c.N)) {
+    a.count = total;
+    return launch_muon_small(a, ns.steps, st);
+  }
   hipError_t e = hipSuccess;
   for (int first = 0; first < total && e == hipSuccess; first += c.chunk) {
     a.first = first;

@@ -59,6 +59,10 @@ enum MuonForm {
 };
 hipError_t launch_muon_product(MuonForm form, const MuonArgs& a, hipStream_t st);
 
+// All of it for small matrices, without a workspace
+bool muon_small(int M, int N);
+hipError_t launch_muon_small(const MuonArgs& a, int steps, hipStream_t st);
+
 #ifdef __HIPCC__
 // The stack of matrix `index` of the class
 __device__ __forceinline__ const MuonStack& muon_stack(const MuonArgs& a, int index) {
