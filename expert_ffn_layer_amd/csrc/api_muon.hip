@@ -16,7 +16,7 @@ size_t up(size_t x) { return (x + WS_ALIGN - 1) / WS_ALIGN * WS_ALIGN; }
 
 // Matrices of one size class, and what the workspace holds of a chunk of them
 struct Class {
-  int M, N, Mp, Np, chunk;
+  int M, N, Mp, Np, chunk, parts;
   bool split;
   size_t sums, x, x_lo, xo, xo_lo, A, A_lo, C, C_lo, da, dc, total;
 };
@@ -43,7 +43,8 @@ Class class_of(int rows, int cols, long long count, bool split) {
     o += up(bytes);
     return at;
   };
-  c.sums = take(k * MUON_SUMS * 8);
+  c.parts = muon_parts((long long)c.M * c.N);
+  c.sums = take(k * c.parts * 8);
   c.da = take(k * c.Mp * 4);
   c.dc = take(k * c.Mp * 4);
   c.x = take(k * xb);
@@ -102,6 +103,7 @@ hipError_t run_class(MuonArgs a, const Class& c, const moe_newton_schulz& ns, in
   a.Mp = c.Mp;
   a.Np = c.Np;
   a.split = c.split;
+  a.parts = c.parts;
   a.eps = ns.eps;
   a.a = (float)ns.a;
   a.b = (float)ns.b;

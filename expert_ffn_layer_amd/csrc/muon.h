@@ -13,7 +13,6 @@ namespace moe {
 
 constexpr int MUON_STACKS = 40;      // stacks of one launch
 constexpr float MUON_SCALE = 4096.f;
-constexpr int MUON_SUMS = 64;        // partial sums of squares of a matrix
 constexpr int MUON_PAD = 128;
 
 struct MuonStack {
@@ -42,13 +41,15 @@ struct MuonArgs {
   double eps;
   float a, b, c;           // the polynomial of this step
   // workspace
-  double* sums;            // [count][MUON_SUMS]
+  int parts;               // partial sums of squares of a matrix
+  double* sums;            // [count][parts]
   uint16_t *x, *x_lo;      // in
   uint16_t *xo, *xo_lo;    // out; xo_lo may be x_lo without split, or NULL
   uint16_t *A, *A_lo, *C, *C_lo;
   float *da, *dc;          // [count][Mp]: the diagonals of A and of a I + C, which are zero in A, and in C but for whole_c and split
 };
 
+int muon_parts(long long elements);
 hipError_t launch_muon_momentum(const MuonArgs& a, hipStream_t st);   // m, and the sums of u's squares
 hipError_t launch_muon_normalize(const MuonArgs& a, hipStream_t st);  // x, x_lo = SCALE u / (|u| + eps)
 enum MuonForm {

@@ -1,6 +1,6 @@
 // The products of the Newton-Schulz steps (v_mfma_f32_32x32x16_f16); forms as listed in muon.h.
 //
-// out[m][n] = sum_k P(m, k) Q(n, k), a tile per workgroup of 4 waves; both operands pass through a ring of two slots of 64
+// out[m][n] = sum_k P(m, k) Q(n, k), a tile per workgroup of 4 waves; both operands pass through a ring of D slots of 64
 // reduction elements in LDS (tile_ring.h). X is held with its long side contiguous, so that the product with C, most of
 // the work, reads both operands with their own index contiguous (C is symmetric), and Gram's matrix both with the
 // reduction index. A and C are symmetric: their tiles on and under the diagonal are computed and written to both places.
@@ -89,20 +89,21 @@ __device__ __forceinline__ void store_bf16(uint16_t* p, size_t at, const Eight& 
   *(u32x4*)(p + at) = u32x4{pack_bf16x2(v.v[0], v.v[1]), pack_bf16x2(v.v[2], v.v[3]), pack_bf16x2(v.v[4], v.v[5]), pack_bf16x2(v.v[6], v.v[7])};
 }
 
-template <int FORM, int WR, int WC, int MT, int NT, bool SPLIT, int OUT>
+template <int FORM, int WR, int WC, int MT, int NT, int D, bool SPLIT, int OUT>
 __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const MuonArgs a) {
   constexpr bool SYM = FORM == MF_GRAM || FORM == MF_POLY, KC = FORM == MF_GRAM;
-  constexpr int BM = WR * MT * 32, BN = WC * NT * 32, D = 2;
+  constexpr int BM = WR * MT * 32, BN = WC * NT * 32;
   static_assert(BM == BN, "square tiles");
-  using T = Tile<BM, KC, !KC>;
+  constexpr bool HV = !KC && D == 2;  // slots freed and filled by halves of 32 reduction elements
+  using T = Tile<BM, KC, HV>;
   constexpr int U = T::U, L = 2 * U;  // loads per wave and stage: of an operand, of both
-  using S = Share<!KC, U>;
-  constexpr int PART = KC ? T::BYTES : T::BYTES / 2;
+  using S = Share<HV, U>;
+  constexpr int PART = HV ? T::BYTES / 2 : T::BYTES;
   // One array for each part that is freed and filled whole: the compiler then sees which loads to LDS a read waits for
-  constexpr int MORE = KC ? 16 : PART;
+  constexpr int MORE = HV || D == 4 ? PART : 16;
   __shared__ __align__(1024) uint8_t p0[PART], p1[PART], p2[MORE], p3[MORE], q0[PART], q1[PART], q2[MORE], q3[MORE];
-#define P_PART(SLOT, B) ((lds_byte*)((SLOT) + (!KC && (B) ? 2 : 0) == 0 ? p0 : (SLOT) + (!KC && (B) ? 2 : 0) == 1 ? p1 : (SLOT) + (!KC && (B) ? 2 : 0) == 2 ? p2 : p3))
-#define Q_PART(SLOT, B) ((lds_byte*)((SLOT) + (!KC && (B) ? 2 : 0) == 0 ? q0 : (SLOT) + (!KC && (B) ? 2 : 0) == 1 ? q1 : (SLOT) + (!KC && (B) ? 2 : 0) == 2 ? q2 : q3))
+#define P_PART(SLOT, B) ((lds_byte*)((SLOT) + (HV && (B) ? 2 : 0) == 0 ? p0 : (SLOT) + (HV && (B) ? 2 : 0) == 1 ? p1 : (SLOT) + (HV && (B) ? 2 : 0) == 2 ? p2 : p3))
+#define Q_PART(SLOT, B) ((lds_byte*)((SLOT) + (HV && (B) ? 2 : 0) == 0 ? q0 : (SLOT) + (HV && (B) ? 2 : 0) == 1 ? q1 : (SLOT) + (HV && (B) ? 2 : 0) == 2 ? q2 : q3))
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / WC, wc = wave % WC;
   // the user's matrices have their long side first: the last product's tiles lie as they do, with X as P
@@ -191,11 +192,11 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const
   // P runs x, x, x_lo; Q runs x, x_lo, x
   auto load_p = [&](int u, int step, auto slot) __attribute__((always_inline)) {
     const int un = T::unit(u, wave);
-    load_one(psrc[u], P_PART(decltype(slot)::value, u >= U / 2) + (KC ? un : un % (T::UNITS / 2)) * 1024, step, pstride, 0, p_lo);
+    load_one(psrc[u], P_PART(decltype(slot)::value, u >= U / 2) + (HV ? un % (T::UNITS / 2) : un) * 1024, step, pstride, 0, p_lo);
   };
   auto load_q = [&](int u, int step, auto slot) __attribute__((always_inline)) {
     const int un = T::unit(u, wave);
-    load_one(qsrc[u], Q_PART(decltype(slot)::value, u >= U / 2) + (KC ? un : un % (T::UNITS / 2)) * 1024, step, qstride, q_lo, -q_lo);
+    load_one(qsrc[u], Q_PART(decltype(slot)::value, u >= U / 2) + (HV ? un % (T::UNITS / 2) : un) * 1024, step, qstride, q_lo, -q_lo);
   };
 
   f32x16 acc[NT][MT];
@@ -216,12 +217,12 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const
     auto read_p = [&](int i, auto quarter, auto slot) __attribute__((always_inline)) {
       constexpr int h = decltype(quarter)::value;
       lds_byte* const part = P_PART(decltype(slot)::value, h >= 2);
-      pf[h & 1][i] = read_frag<BM, KC>(part + (KC ? pb[h] + i * 4096 : pb[i] + (h & 1) * 16 * (BM * 2)));
+      pf[h & 1][i] = read_frag<BM, KC>(part + (KC ? pb[h] + i * 4096 : pb[i] + (HV ? h & 1 : h) * 16 * (BM * 2)));
     };
     auto read_q = [&](int t, auto quarter, auto slot) __attribute__((always_inline)) {
       constexpr int h = decltype(quarter)::value;
       lds_byte* const part = Q_PART(decltype(slot)::value, h >= 2);
-      qf[h & 1][t] = read_frag<BN, KC>(part + (KC ? qb[h] + t * 4096 : qb[t] + (h & 1) * 16 * (BN * 2)));
+      qf[h & 1][t] = read_frag<BN, KC>(part + (KC ? qb[h] + t * 4096 : qb[t] + (HV ? h & 1 : h) * 16 * (BN * 2)));
     };
     constexpr std::integral_constant<int, 0> C0{};
     constexpr std::integral_constant<int, 1> C1{};
@@ -231,10 +232,10 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const
     auto load_nth = [&](auto ph_c, int n, int s, auto slot) __attribute__((always_inline)) {
       constexpr int ph = decltype(ph_c)::value, each = S::count(ph);
       constexpr std::integral_constant<int, (decltype(slot)::value + D - 1) % D> before{};
-      const bool is_p = KC ? n >= each : n < each;
-      const int u = S::from(ph) + (is_p == KC ? n - each : n);
+      const bool is_p = HV ? n < each : n >= each;
+      const int u = S::from(ph) + (is_p != HV ? n - each : n);
       // phase 0, and phase 1 for whole slots, still bring stage s + D - 1, into the slot of step s - 1
-      if constexpr (ph == 0 || (KC && ph == 1)) {
+      if constexpr (ph == 0 || (!HV && ph == 1)) {
         if (is_p) load_p(u, s + D - 1, before);
         else load_q(u, s + D - 1, before);
       } else {
@@ -263,8 +264,8 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const
       }
     };
     // Loads that may still be in flight: where the second half of a slot is wanted (after phase 0), those of one step;
-    // where the next stage is wanted (after phase 2), the same, and none with whole slots
-    constexpr int FLY0 = L, FLY2 = KC ? 0 : L;
+    // where the next stage is wanted (after phase 2), the same, and those of D - 2 steps with whole slots
+    constexpr int FLY0 = L, FLY2 = HV ? L : (D - 2) * L;
     auto body = [&](int s, auto slot) __attribute__((always_inline)) {
       constexpr std::integral_constant<int, (decltype(slot)::value + 1) % D> other{};
       // opaque in every step, so that the slot stays a constant and does not become a register per slot and fragment
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const
 #pragma unroll
       for (int t = 0; t < NT && !KC; ++t) asm volatile("" : "+v"(qb[t]));
       phase(C0, slot, s, slot);
-      if constexpr (!KC) {
+      if constexpr (HV) {
         MOE_WAIT_LGKM0();
         MOE_WAIT_VMCNT(FLY0);
         __builtin_amdgcn_s_barrier();
@@ -286,24 +287,41 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const
       phase(C3, other, s, slot);
     };
     // what the steps before the first would have loaded, stage 0 first
+    auto stage = [&](int step, auto slot) __attribute__((always_inline)) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) load_q(u, 0, C0);
+      for (int u = 0; u < U; ++u) load_q(u, step, slot);
 #pragma unroll
-    for (int u = 0; u < U; ++u) load_p(u, 0, C0);
-    constexpr int FIRST = KC ? 0 : U / 2;  // of stage 1, before phase 3 of step -1
+      for (int u = 0; u < U; ++u) load_p(u, step, slot);
+    };
+    stage(0, C0);
+    if constexpr (D == 4) {
+      stage(1, C1);
+      stage(2, C2);
+    }
+    constexpr int FIRST = HV ? U / 2 : 0;  // of stage 1, before phase 3 of step -1
 #pragma unroll
     for (int u = 0; u < FIRST; ++u) load_q(u, 1, C1);
 #pragma unroll
     for (int u = 0; u < FIRST; ++u) load_p(u, 1, C1);
+    constexpr std::integral_constant<int, D - 1> last{};
 #pragma unroll
-    for (int n = 0; n < 2 * S::count(3); ++n) load_nth(C3, n, -1, C1);
-    MOE_WAIT_VMCNT(2 * FIRST + 2 * S::count(3));
+    for (int n = 0; n < 2 * S::count(3); ++n) load_nth(C3, n, -1, last);
+    MOE_WAIT_VMCNT((D - 2) * L + 2 * FIRST + 2 * S::count(3));
     __builtin_amdgcn_s_barrier();
 #pragma unroll
     for (int t = 0; t < NT; ++t) read_q(t, C0, C0);
 #pragma unroll
     for (int i = 0; i < MT; ++i) read_p(i, C0, C0);
-    for (int s = 0; s < nsteps; s += 2) {  // sizes are multiples of 128: pairs of steps
+    int s = 0;
+    if constexpr (D == 4) {
+      for (; s + 2 < nsteps; s += 4) {
+        body(s, C0);
+        body(s + 1, C1);
+        body(s + 2, C2);
+        body(s + 3, C3);
+      }
+    }
+    for (; s < nsteps; s += 2) {  // sizes are multiples of 128: pairs of steps
       body(s, C0);
       body(s + 1, C1);
     }
@@ -315,9 +333,10 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const
   // 16-byte chunk c of a row sits at c ^ (row % 16), which keeps both directions free of bank conflicts. Mirrored blocks pass
   // through another 4.5 KiB as 64 rows of 32, 72 bytes apart. The parts of the ring serve for both.
   __builtin_amdgcn_s_barrier();
-  static_assert((KC ? PART / 2 : PART) >= 8192, "a part of the ring per wave");
-  lds_byte* const ep = KC ? (lds_byte*)(wave & 2 ? q1 : q0) + (wave & 1) * (PART / 2) : (lds_byte*)(wave == 0 ? q0 : wave == 1 ? q1 : wave == 2 ? q2 : q3);
-  lds_byte* const mirror = KC ? (lds_byte*)(wave & 2 ? p1 : p0) + (wave & 1) * (PART / 2) : (lds_byte*)(wave == 0 ? p0 : wave == 1 ? p1 : wave == 2 ? p2 : p3);
+  constexpr bool FOUR = HV || D == 4;  // parts of an operand
+  static_assert((FOUR ? PART : PART / 2) >= 8192, "a part of the ring per wave");
+  lds_byte* const ep = !FOUR ? (lds_byte*)(wave & 2 ? q1 : q0) + (wave & 1) * (PART / 2) : (lds_byte*)(wave == 0 ? q0 : wave == 1 ? q1 : wave == 2 ? q2 : q3);
+  lds_byte* const mirror = !FOUR ? (lds_byte*)(wave & 2 ? p1 : p0) + (wave & 1) * (PART / 2) : (lds_byte*)(wave == 0 ? p0 : wave == 1 ? p1 : wave == 2 ? p2 : p3);
   const float inv = 1.f / MUON_SCALE;
   const int wrow = m0 + wr * MT * 32, wcol = n0 + wc * NT * 32, r32 = lane & 31, hi4 = lane >> 5, c8 = lane & 7, r8 = lane >> 3;
   // The lanes of a wave exchange data through LDS: its accesses run in the order in which they are issued, and this keeps
@@ -492,13 +511,13 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const
   }
 }
 
-template <int FORM, int WR, int WC, int MT, int NT>
+template <int FORM, int WR, int WC, int MT, int NT, int D>
 hipError_t launch(const MuonArgs& a, hipStream_t st) {
   constexpr int B = WR * MT * 32;
   const long long m = (a.Mp + B - 1) / B, n = (a.Np + B - 1) / B;
   const long long all = (FORM == MF_GRAM || FORM == MF_POLY ? m * (m + 1) / 2 : m * n) * a.count;
   const unsigned grid = (unsigned)((all + NXCD - 1) / NXCD * NXCD);
-#define MOE_PRODUCT(SPLIT, OUT) product_kernel<FORM, WR, WC, MT, NT, SPLIT, OUT><<<grid, THR, 0, st>>>(a)
+#define MOE_PRODUCT(SPLIT, OUT) product_kernel<FORM, WR, WC, MT, NT, D, SPLIT, OUT><<<grid, THR, 0, st>>>(a)
   if constexpr (FORM == MF_LAST) {
     const MuonStack& s = a.s[0];  // all stacks have what the first has
     if (!s.m) {
@@ -521,9 +540,12 @@ hipError_t launch(const MuonArgs& a, hipStream_t st) {
 
 template <int FORM>
 hipError_t choose(const MuonArgs& a, hipStream_t st) {
-  const long long m = (a.Mp + 255) / 256, n = (a.Np + 255) / 256;
-  const long long tiles = (FORM == MF_GRAM || FORM == MF_POLY ? m * (m + 1) / 2 : m * n) * a.count;
-  return tiles >= 224 ? launch<FORM, 2, 2, 4, 4>(a, st) : launch<FORM, 2, 2, 2, 2>(a, st);
+  auto tiles = [&](int b) {
+    const long long m = (a.Mp + b - 1) / b, n = (a.Np + b - 1) / b;
+    return (FORM == MF_GRAM || FORM == MF_POLY ? m * (m + 1) / 2 : m * n) * a.count;
+  };
+  if (tiles(256) >= 224) return launch<FORM, 2, 2, 4, 4, 2>(a, st);
+  return tiles(128) <= 256 ? launch<FORM, 2, 2, 2, 2, 4>(a, st) : launch<FORM, 2, 2, 2, 2, 2>(a, st);
 }
 
 }  // namespace

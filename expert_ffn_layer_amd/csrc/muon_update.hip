@@ -7,79 +7,139 @@ namespace {
 
 constexpr int THR = 256;
 
+constexpr int PART = 16384;  // elements of a workgroup that sums
+
+// `4` consecutive elements, or one
+__device__ __forceinline__ f32x4 load_g4(const MuonArgs& a, const void* g, size_t i, float gs) {
+  f32x4 v;
+  if (a.g_f32) {
+    v = *(const f32x4*)((const float*)g + i);
+  } else {
+    const u32x2 w = *(const u32x2*)((const uint16_t*)g + i);
+    v = f32x4{bf16lo(w[0]), bf16hi(w[0]), bf16lo(w[1]), bf16hi(w[1])};
+  }
+  return a.grad_scale ? v * gs : v;
+}
 __device__ __forceinline__ float load_g(const MuonArgs& a, const void* g, size_t i, float gs) {
   const float v = a.g_f32 ? ((const float*)g)[i] : bf16_to_f32(((const uint16_t*)g)[i]);
   return a.grad_scale ? v * gs : v;
 }
 
 // m = mu m + g', and the sum of u^2 of this workgroup's part of a matrix, u = g' + mu m (Nesterov), m or g'. Sums are
-// in 64 bits: no gradient overflows or vanishes in them. Part p of MUON_SUMS, always the same elements: the same bits
-// on every run.
+// in 64 bits: no gradient overflows or vanishes in them. A part is always the same elements: the same bits on every run.
+// Bound by memory: 10 bytes an element with a bf16 gradient.
 __global__ void __launch_bounds__(THR) momentum_kernel(const MuonArgs a) {
   const int b = blockIdx.y, part = blockIdx.x;
   const MuonStack& s = muon_stack(a, a.first + b);
-  const size_t n = (size_t)a.M * a.N, base = (size_t)(a.first + b - s.first) * n;
+  const size_t n = (size_t)a.M * a.N, base = (size_t)(a.first + b - s.first) * n, from = (size_t)part * PART;
+  const size_t to = from + PART < n ? from + PART : n;
   const float gs = a.grad_scale ? *a.grad_scale : 1.f;
   double sum = 0.0;
-  for (size_t i = (size_t)part * THR + threadIdx.x; i < n; i += (size_t)MUON_SUMS * THR) {
-    float u = load_g(a, s.g, base + i, gs);
-    if (s.m) {
-      const float m = a.momentum * s.m[base + i] + u;
-      s.m[base + i] = m;
-      u = a.nesterov ? u + a.momentum * m : m;
+  if (n % 4 == 0) {
+#pragma unroll 4
+    for (size_t i = from + 4 * threadIdx.x; i < to; i += 4 * THR) {
+      f32x4 u = load_g4(a, s.g, base + i, gs);
+      if (s.m) {
+        f32x4 m = *(const f32x4*)(s.m + base + i);
+        m = a.momentum * m + u;
+        *(f32x4*)(s.m + base + i) = m;
+        u = a.nesterov ? u + a.momentum * m : m;
+      }
+#pragma unroll
+      for (int z = 0; z < 4; ++z) sum += (double)u[z] * u[z];
     }
-    sum += (double)u * u;
+  } else {
+    for (size_t i = from + threadIdx.x; i < to; i += THR) {
+      float u = load_g(a, s.g, base + i, gs);
+      if (s.m) {
+        const float m = a.momentum * s.m[base + i] + u;
+        s.m[base + i] = m;
+        u = a.nesterov ? u + a.momentum * m : m;
+      }
+      sum += (double)u * u;
+    }
   }
   __shared__ double part_sum[THR / 64];
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
   if ((threadIdx.x & 63) == 0) part_sum[threadIdx.x >> 6] = sum;
   __syncthreads();
-  if (threadIdx.x == 0) a.sums[b * MUON_SUMS + part] = part_sum[0] + part_sum[1] + part_sum[2] + part_sum[3];
+  if (threadIdx.x == 0) a.sums[(size_t)b * a.parts + part] = part_sum[0] + part_sum[1] + part_sum[2] + part_sum[3];
 }
 
-// A tile of 64 x 64 of X; matrices with the long side first are transposed through LDS.
+// A tile of X, 64 of the short side x 64 of the long one, through LDS: the user's rows are read 16 bytes a lane, X's written so.
+// Bound by memory: 10 bytes an element with a bf16 gradient.
 __global__ void __launch_bounds__(THR) normalize_kernel(const MuonArgs a) {
   __shared__ float tile[64][65];
   const int b = blockIdx.z, n0 = blockIdx.x * 64, j0 = blockIdx.y * 64;
   const MuonStack& s = muon_stack(a, a.first + b);
   const size_t base = (size_t)(a.first + b - s.first) * a.M * a.N;
-  double sum = a.sums[b * MUON_SUMS + (threadIdx.x & 63)];
+  double sum = 0.0;
+  for (int i = threadIdx.x & 63; i < a.parts; i += 64) sum += a.sums[(size_t)b * a.parts + i];
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
   const double norm = sqrt(sum) + a.eps;
   // a matrix of zeros stays one without an eps, too
   const double f = norm == 0.0 ? 0.0 : (double)MUON_SCALE / norm;
   const float gs = a.grad_scale ? *a.grad_scale : 1.f;
-  const int c = threadIdx.x & 63, r0 = threadIdx.x >> 6;
-  for (int r = r0; r < 64; r += 4) {
-    // n: place on the long side, j: on the short one; lanes run along the user's rows
-    const int n = n0 + (s.wide ? c : r), j = j0 + (s.wide ? r : c);
-    float v = 0.f;
-    if (n < a.N && j < a.M) {
-      const size_t i = base + (s.wide ? (size_t)j * a.N + n : (size_t)n * a.M + j);
-      float u = load_g(a, s.g, i, gs);
-      if (s.m) u = a.nesterov ? u + a.momentum * s.m[i] : s.m[i];
-      v = (float)(u * f);
+  const int cols = s.wide ? a.N : a.M, rows = s.wide ? a.M : a.N, c0 = s.wide ? n0 : j0, r0 = s.wide ? j0 : n0;
+  const int c = 4 * (threadIdx.x & 15);
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int r = it * 16 + (threadIdx.x >> 4);
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    const size_t at = base + (size_t)(r0 + r) * cols + c0 + c;
+    if (cols % 4 == 0) {
+      if (r0 + r < rows && c0 + c < cols) {
+        f32x4 u = load_g4(a, s.g, at, gs);
+        if (s.m) {
+          const f32x4 m = *(const f32x4*)(s.m + at);
+          u = a.nesterov ? u + a.momentum * m : m;
+        }
+#pragma unroll
+        for (int z = 0; z < 4; ++z) v[z] = (float)(u[z] * f);
+      }
+    } else if (r0 + r < rows) {
+#pragma unroll
+      for (int z = 0; z < 4; ++z)
+        if (c0 + c + z < cols) {
+          float u = load_g(a, s.g, at + z, gs);
+          if (s.m) u = a.nesterov ? u + a.momentum * s.m[at + z] : s.m[at + z];
+          v[z] = (float)(u * f);
+        }
     }
-    if (s.wide) tile[r][c] = v;
-    else tile[c][r] = v;
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+      if (s.wide) tile[r][c + z] = v[z];
+      else tile[c + z][r] = v[z];
+    }
   }
   __syncthreads();
   const size_t at = (size_t)b * a.Mp * a.Np;
-  for (int r = r0; r < 64; r += 4) {
-    const float v = tile[r][c];
-    const _Float16 hi = (_Float16)v, lo = (_Float16)(v - (float)hi);
-    const size_t i = at + (size_t)(j0 + r) * a.Np + n0 + c;
-    a.x[i] = __builtin_bit_cast(uint16_t, hi);
-    a.x_lo[i] = __builtin_bit_cast(uint16_t, lo);
+  const int n = 8 * (threadIdx.x & 7);
+#pragma unroll
+  for (int it = 0; it < 2; ++it) {
+    const int j = it * 32 + (threadIdx.x >> 3);
+    typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
+    f16x8 hi, lo;
+#pragma unroll
+    for (int z = 0; z < 8; ++z) {
+      const float v = tile[j][n + z];
+      hi[z] = (_Float16)v;
+      lo[z] = (_Float16)(v - (float)hi[z]);
+    }
+    const size_t i = at + (size_t)(j0 + j) * a.Np + n0 + n;
+    *(u32x4*)(a.x + i) = __builtin_bit_cast(u32x4, hi);
+    *(u32x4*)(a.x_lo + i) = __builtin_bit_cast(u32x4, lo);
   }
 }
 
 }  // namespace
 
+int muon_parts(long long elements) { return (int)((elements + PART - 1) / PART); }
+
 hipError_t launch_muon_momentum(const MuonArgs& a, hipStream_t st) {
-  momentum_kernel<<<dim3(MUON_SUMS, a.count), THR, 0, st>>>(a);
+  momentum_kernel<<<dim3(a.parts, a.count), THR, 0, st>>>(a);
   return hipGetLastError();
 }
 
