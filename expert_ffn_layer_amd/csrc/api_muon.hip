@@ -18,7 +18,7 @@ size_t up(size_t x) { return (x + WS_ALIGN - 1) / WS_ALIGN * WS_ALIGN; }
 struct Class {
   int M, N, Mp, Np, chunk, parts;
   bool split;
-  size_t sums, x, x_lo, xo, xo_lo, A, A_lo, C, C_lo, da, dc, total;
+  size_t sums, q, x, x_lo, xo, xo_lo, A, A_lo, C, C_lo, da, dc, total;
 };
 
 Class class_of(int rows, int cols, long long count, bool split) {
@@ -28,6 +28,23 @@ Class class_of(int rows, int cols, long long count, bool split) {
   c.Mp = (c.M + MUON_PAD - 1) / MUON_PAD * MUON_PAD;
   c.Np = (c.N + MUON_PAD - 1) / MUON_PAD * MUON_PAD;
   c.split = split;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += up(bytes);
+    return at;
+  };
+  if (c.M <= THIN_MAX) {
+    // within 256 MiB, and a launch's grid
+    const int side = thin_side(c.M), part = thin_part(c.N);
+    c.parts = (c.N + part - 1) / part;
+    const size_t square = (size_t)side * side * 8, each = (c.parts + 1) * square;
+    c.chunk = (int)std::min<long long>(std::min<long long>(std::max<long long>((long long)((256ull << 20) / each), 1), 65535), count);
+    c.sums = take(c.chunk * c.parts * square);
+    c.q = take(c.chunk * (square + 8));
+    c.total = o;
+    return c;
+  }
   const size_t xb = (size_t)c.Np * c.Mp * 2, ab = (size_t)c.Mp * c.Mp * 2;
   // As many matrices at a time as give the symmetric products, which have the fewest tiles, about 4 rounds of the
   // card, within 4 GiB
@@ -37,12 +54,6 @@ Class class_of(int rows, int cols, long long count, bool split) {
   n = std::min<long long>(n, std::max<long long>((long long)((4ull << 30) / each), 1));
   c.chunk = (int)std::min(n, count);
   const size_t k = c.chunk;
-  size_t o = 0;
-  auto take = [&](size_t bytes) {
-    const size_t at = o;
-    o += up(bytes);
-    return at;
-  };
   c.parts = muon_parts((long long)c.M * c.N);
   c.sums = take(k * c.parts * 8);
   c.da = take(k * c.Mp * 4);
@@ -105,9 +116,9 @@ hipError_t run_class(MuonArgs a, const Class& c, const moe_newton_schulz& ns, in
   a.split = c.split;
   a.parts = c.parts;
   a.eps = ns.eps;
-  a.a = (float)ns.a;
-  a.b = (float)ns.b;
-  a.c = (float)ns.c;
+  a.a = ns.a;
+  a.b = ns.b;
+  a.c = ns.c;
   a.sums = (double*)(w + c.sums);
   a.da = (float*)(w + c.da);
   a.dc = (float*)(w + c.dc);
@@ -115,11 +126,21 @@ hipError_t run_class(MuonArgs a, const Class& c, const moe_newton_schulz& ns, in
   a.A_lo = (uint16_t*)(w + c.A_lo);
   a.C = (uint16_t*)(w + c.C);
   a.C_lo = (uint16_t*)(w + c.C_lo);
+  hipError_t e = hipSuccess;
+  if (c.M <= THIN_MAX) {
+    a.q = (double*)(w + c.q);
+    a.part = thin_part(c.N);
+    for (int first = 0; first < total && e == hipSuccess; first += c.chunk) {
+      a.first = first;
+      a.count = std::min(c.chunk, total - first);
+      e = launch_muon_thin(a, ns.steps, st);
+    }
+    return e;
+  }
   if (muon_small(c.M, c.N)) {
     a.count = total;
     return launch_muon_small(a, ns.steps, st);
   }
-  hipError_t e = hipSuccess;
   for (int first = 0; first < total && e == hipSuccess; first += c.chunk) {
     a.first = first;
     a.count = std::min(c.chunk, total - first);

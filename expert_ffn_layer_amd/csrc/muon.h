@@ -39,13 +39,15 @@ struct MuonArgs {
   float momentum, lr, wd;
   const float *lr_dev, *grad_scale;
   double eps;
-  float a, b, c;           // the polynomial of this step
+  double a, b, c;          // the polynomial of a step
   // workspace
   int parts;               // partial sums of squares of a matrix
+  int part;                // thin matrices: columns of a part
   double* sums;            // [count][parts]
   uint16_t *x, *x_lo;      // in
   uint16_t *xo, *xo_lo;    // out; xo_lo may be x_lo without split, or NULL
   uint16_t *A, *A_lo, *C, *C_lo;
+  double* q;               // thin matrices
   float *da, *dc;          // [count][Mp]: the diagonals of A and of a I + C, which are zero in A, and in C but for whole_c and split
 };
 
@@ -60,7 +62,14 @@ enum MuonForm {
 };
 hipError_t launch_muon_product(MuonForm form, const MuonArgs& a, hipStream_t st);
 
-// All of it for small matrices, without a workspace
+// All of it for matrices with a short side of at most THIN_MAX; a.part = thin_part(N) and a.parts of them, a.sums
+// [count][parts][MB][MB], a.q [count][MB * MB + 1], MB the short side's 32 or 64
+constexpr int THIN_MAX = 64;
+inline int thin_side(int M) { return M <= 32 ? 32 : 64; }
+int thin_part(int N);
+hipError_t launch_muon_thin(const MuonArgs& a, int steps, hipStream_t st);
+
+// All of it for other small matrices, without a workspace
 bool muon_small(int M, int N);
 hipError_t launch_muon_small(const MuonArgs& a, int steps, hipStream_t st);
 

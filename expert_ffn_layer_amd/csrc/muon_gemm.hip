@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const
   static_assert((FOUR ? PART : PART / 2) >= 8192, "a part of the ring per wave");
   lds_byte* const ep = !FOUR ? (lds_byte*)(wave & 2 ? q1 : q0) + (wave & 1) * (PART / 2) : (lds_byte*)(wave == 0 ? q0 : wave == 1 ? q1 : wave == 2 ? q2 : q3);
   lds_byte* const mirror = !FOUR ? (lds_byte*)(wave & 2 ? p1 : p0) + (wave & 1) * (PART / 2) : (lds_byte*)(wave == 0 ? p0 : wave == 1 ? p1 : wave == 2 ? p2 : p3);
-  const float inv = 1.f / MUON_SCALE;
+  const float inv = 1.f / MUON_SCALE, pa = (float)a.a, pb = (float)a.b, pc = (float)a.c;
   const int wrow = m0 + wr * MT * 32, wcol = n0 + wc * NT * 32, r32 = lane & 31, hi4 = lane >> 5, c8 = lane & 7, r8 = lane >> 3;
   // The lanes of a wave exchange data through LDS: its accesses run in the order in which they are issued, and this keeps
   // the compiler from changing that order.
@@ -423,13 +423,13 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const
         Eight q = r;
         if constexpr (FORM == MF_POLY) {
 #pragma unroll
-          for (int z = 0; z < 8; ++z) q.v[z] = a.b * x.v[z] + a.c * ((dm + dn.v[z]) * x.v[z] + r.v[z]);
+          for (int z = 0; z < 8; ++z) q.v[z] = pb * x.v[z] + pc * ((dm + dn.v[z]) * x.v[z] + r.v[z]);
         }
         if (tm == tn) {
 #pragma unroll
           for (int z = 0; z < 8; ++z)
             if (m == n + z) {
-              const float d = FORM == MF_GRAM ? r.v[z] * inv : a.a + a.b * dm + a.c * (dm * dm + r.v[z] * inv);
+              const float d = FORM == MF_GRAM ? r.v[z] * inv : pa + pb * dm + pc * (dm * dm + r.v[z] * inv);
               if (inside) (FORM == MF_GRAM ? a.da : a.dc)[(size_t)b * a.Mp + m] = d;
               // C keeps its diagonal where the product that reads it adds nothing to it
               q.v[z] = FORM == MF_POLY && (SPLIT || a.whole_c) ? d * MUON_SCALE : 0.f;

@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(64 * waves_of(MB)) small_kernel(const MuonArgs
   const MuonStack s = muon_stack(a, a.first + blockIdx.x);
   const int M = a.M, N = a.N;
   const bool g_f32 = a.g_f32, out_f32 = a.out_f32, nesterov = a.nesterov, rescale = a.grad_scale != nullptr;
-  const float mu = a.momentum, pa = a.a, pb = a.b, pc = a.c;
+  const float mu = a.momentum, pa = (float)a.a, pb = (float)a.b, pc = (float)a.c;
   const size_t base = (size_t)(a.first + blockIdx.x - s.first) * M * N;
   f32x16 x[TILES];
 #pragma unroll
@@ -340,20 +340,12 @@ void launch(const MuonArgs& a, int steps, hipStream_t st) {
 
 }  // namespace
 
-bool muon_small(int M, int N) { return M <= 128 && N <= (M > 32 && M <= 64 ? 512 : 256); }
+bool muon_small(int M, int N) { return M <= 128 && N <= 256; }
 
 hipError_t launch_muon_small(const MuonArgs& a, int steps, hipStream_t st) {
   if (!muon_small(a.M, a.N)) return hipErrorInvalidValue;
-  if (a.M <= 32) {
-    if (a.N <= 64) launch<32, 2>(a, steps, st);
-    else launch<32, 8>(a, steps, st);
-  } else if (a.M <= 64) {
-    if (a.N <= 128) launch<64, 2>(a, steps, st);
-    else launch<64, 8>(a, steps, st);
-  } else {
-    if (a.N <= 128) launch<128, 2>(a, steps, st);
-    else launch<128, 4>(a, steps, st);
-  }
+  if (a.N <= 128) launch<128, 2>(a, steps, st);
+  else launch<128, 4>(a, steps, st);
   return hipGetLastError();
 }
 

@@ -1,0 +1,274 @@
+// Orthogonalisation and Muon step of matrices whose short side is at most 64, in 64 bits (v_mfma_f64_16x16x4_f64).
+//
+// With A_0 = X_0 X_0^T every step's polynomial is one in A_0, so the steps need X only before and after them:
+//   B_i = a I + b A_i + c A_i^2,  A_{i+1} = B_i A_i B_i,  Q = B_last ... B_0,  O = Q X_0
+// and the long side is read twice, whatever the number of steps: once for A_0 (gram), once for Q X_0 (apply). The steps
+// themselves (steps) are a few products of at most 64 x 64 by one workgroup. A step multiplies what rounding adds to small
+// eigenvalues by a^2 = 12, and Q's large entries cancel on large singular values: in 64 bits both stay far below fp32.
+//
+// What bounds them is latency: three launches, and in `steps` 17 products one after the other.
+#include "muon.h"
+
+namespace moe {
+
+namespace {
+
+typedef __attribute__((ext_vector_type(4))) double f64x4;
+
+constexpr int THR = 256, COLS = 64, LD = COLS + 4;  // columns of the long side at a time, and floats of a row of them in LDS
+
+// v_mfma_f64_16x16x4_f64: lane l gives row l % 16 of the first operand and column l % 16 of the second at reduction element
+// l / 16, and gets rows l / 16 + 4 r of column l % 16.
+__device__ __forceinline__ f64x4 product(double a, double b, f64x4 c) { return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0); }
+
+// The user's elements of columns n0.. + 64 of the long side, 4 of a row of theirs at a time: f(place, row and column of X,
+// how many there are, step of X's column per element or 0 where its row runs)
+template <int MB, typename F>
+__device__ __forceinline__ void user_elements(const MuonArgs& a, const MuonStack& s, size_t base, int n0, F f) {
+  const int w = s.wide ? COLS : MB, per_row = w / 4, rows = s.wide ? MB : COLS;
+  const int c = 4 * (threadIdx.x % per_row);
+  for (int r = threadIdx.x / per_row; r < rows; r += THR / per_row) {
+    const int j = s.wide ? r : c, n = n0 + (s.wide ? c : r);
+    if (j >= a.M || n >= a.N) continue;
+    const int left = s.wide ? a.N - n : a.M - j;
+    f(base + (s.wide ? (size_t)j * a.N + n : (size_t)n * a.M + j), j, n - n0, left < 4 ? left : 4);
+  }
+}
+
+// u at `n` consecutive places; with `update` m is stepped first, else it has been
+__device__ __forceinline__ f32x4 read_u(const MuonArgs& a, const MuonStack& s, size_t at, int n, bool whole, float gs, bool update) {
+  f32x4 u = {0.f, 0.f, 0.f, 0.f}, m = u;
+  if (whole) {
+    if (a.g_f32) {
+      u = *(const f32x4*)((const float*)s.g + at);
+    } else {
+      const u32x2 w = *(const u32x2*)((const uint16_t*)s.g + at);
+      u = f32x4{bf16lo(w[0]), bf16hi(w[0]), bf16lo(w[1]), bf16hi(w[1])};
+    }
+    if (s.m) m = *(const f32x4*)(s.m + at);
+  } else {
+#pragma unroll
+    for (int z = 0; z < 4; ++z)
+      if (z < n) {
+        u[z] = a.g_f32 ? ((const float*)s.g)[at + z] : bf16_to_f32(((const uint16_t*)s.g)[at + z]);
+        if (s.m) m[z] = s.m[at + z];
+      }
+  }
+  if (a.grad_scale) u = u * gs;
+  if (!s.m) return u;
+  if (update) {
+    m = a.momentum * m + u;
+    if (whole) {
+      *(f32x4*)(s.m + at) = m;
+    } else {
+#pragma unroll
+      for (int z = 0; z < 4; ++z)
+        if (z < n) s.m[at + z] = m[z];
+    }
+  }
+  return a.nesterov ? u + a.momentum * m : m;
+}
+
+// Partial sums of u u^T over a part's columns, and the new momentum. Parts are always the same columns: the same bits on every run.
+template <int MB>
+__global__ void __launch_bounds__(THR) gram_kernel(const MuonArgs a) {
+  constexpr int T = MB / 16, EACH = T * T / 4;  // tiles of 16 a side, and of each of 4 waves
+  __shared__ __align__(16) float u[MB * LD];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, k4 = lane >> 4, b = blockIdx.y;
+  const int ti = wave * EACH / T, tj = wave * EACH % T;
+  const MuonStack& s = muon_stack(a, a.first + b);
+  const size_t base = (size_t)(a.first + b - s.first) * a.M * a.N;
+  const bool whole = (s.wide ? a.N : a.M) % 4 == 0;
+  const float gs = a.grad_scale ? *a.grad_scale : 1.f;
+  f64x4 acc[EACH];
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) acc[i] = f64x4{0.0, 0.0, 0.0, 0.0};
+  const int from = blockIdx.x * a.part, to = from + a.part < a.N ? from + a.part : a.N;
+  for (int n0 = from; n0 < to; n0 += COLS) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < MB * LD / 4; i += THR) *(f32x4*)(u + 4 * i) = f32x4{0.f, 0.f, 0.f, 0.f};
+    __syncthreads();
+    user_elements<MB>(a, s, base, n0, [&](size_t at, int j, int n, int left) {
+      const f32x4 v = read_u(a, s, at, left, whole, gs, true);
+#pragma unroll
+      for (int z = 0; z < 4; ++z)
+        if (z < left) u[s.wide ? j * LD + n + z : (j + z) * LD + n] = v[z];
+    });
+    __syncthreads();
+    for (int k = 0; k < COLS; k += 4) {
+      const double p = u[(ti * 16 + l16) * LD + k + k4];
+#pragma unroll
+      for (int i = 0; i < EACH; ++i) acc[i] = product(p, (double)u[((tj + i) * 16 + l16) * LD + k + k4], acc[i]);
+    }
+  }
+  double* const out = a.sums + ((size_t)b * a.parts + blockIdx.x) * MB * MB;
+#pragma unroll
+  for (int i = 0; i < EACH; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) out[((ti * T + tj + i) * 4 + r) * 64 + lane] = acc[i][r];
+}
+
+// Q and 1 / (|u| + eps) of a matrix; wave w of (MB / 16)^2 holds tile w of every matrix here
+template <int MB>
+__global__ void __launch_bounds__(MB* MB / 4) steps_kernel(const MuonArgs a, int steps) {
+  constexpr int T = MB / 16, LQ = MB + 4;
+  __shared__ double A[MB * LQ], B[MB * LQ], Q[MB * LQ], W[MB * LQ], traces[T * T];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, k4 = lane >> 4, ti = wave / T, tj = wave % T, b = blockIdx.x;
+  const double* const in = a.sums + (size_t)b * a.parts * MB * MB;
+  double mine[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 4
+  for (int p = 0; p < a.parts; ++p)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) mine[r] += in[(size_t)p * MB * MB + (wave * 4 + r) * 64 + lane];
+  // the place of element r
+  auto at = [&](int r) { return (ti * 16 + k4 + 4 * r) * LQ + tj * 16 + l16; };
+  auto diagonal = [&](int r) { return ti == tj && k4 + 4 * r == l16; };
+  double trace = 0.0;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) trace += diagonal(r) ? mine[r] : 0.0;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) trace += __shfl_xor(trace, d);
+  if (lane == 0) traces[wave] = trace;
+  __syncthreads();
+  trace = 0.0;
+  for (int i = 0; i < T * T; ++i) trace += traces[i];
+  const double norm = sqrt(trace) + a.eps, f = norm == 0.0 ? 0.0 : 1.0 / norm;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) A[at(r)] = mine[r] * f * f;
+  // rows of p times rows of q: all matrices here are symmetric
+  auto multiply = [&](const double* p, const double* q) {
+    f64x4 acc = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 4
+    for (int k = 0; k < MB; k += 4) acc = product(p[(ti * 16 + l16) * LQ + k + k4], q[(tj * 16 + l16) * LQ + k + k4], acc);
+    return acc;
+  };
+  const double ca = a.a, cb = a.b, cc = a.c;
+  for (int step = 0; step < steps; ++step) {
+    __syncthreads();
+    const f64x4 square = multiply(A, A);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) B[at(r)] = cb * A[at(r)] + cc * square[r] + (diagonal(r) ? ca : 0.0);
+    __syncthreads();
+    f64x4 q, w;
+    if (step == 0) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) q[r] = B[at(r)];
+    } else {
+      q = multiply(B, Q);
+    }
+    if (step + 1 < steps) {
+      w = multiply(B, A);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) W[at(r)] = w[r];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 4; ++r) Q[at(r)] = q[r];
+    if (step + 1 < steps) {
+      w = multiply(W, B);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) A[at(r)] = w[r];
+    }
+  }
+  __syncthreads();
+  double* const out = a.q + (size_t)b * (MB * MB + 1);
+  for (int i = threadIdx.x; i < MB * MB; i += MB * MB / 4) out[i] = Q[i / MB * LQ + i % MB];
+  if (threadIdx.x == 0) out[MB * MB] = f;
+}
+
+// O = Q u / (|u| + eps) of 64 columns, or the parameters' step by it
+template <int MB>
+__global__ void __launch_bounds__(THR) apply_kernel(const MuonArgs a) {
+  constexpr int T = MB / 16, LQ = MB + 4;
+  __shared__ __align__(16) float u[MB * LD];
+  __shared__ double Q[MB * LQ];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, k4 = lane >> 4, b = blockIdx.y, n0 = blockIdx.x * COLS;
+  const MuonStack& s = muon_stack(a, a.first + b);
+  const size_t base = (size_t)(a.first + b - s.first) * a.M * a.N;
+  const bool whole = (s.wide ? a.N : a.M) % 4 == 0;
+  const float gs = a.grad_scale ? *a.grad_scale : 1.f;
+  const double* const in = a.q + (size_t)b * (MB * MB + 1);
+  for (int i = threadIdx.x; i < MB * LD / 4; i += THR) *(f32x4*)(u + 4 * i) = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i = threadIdx.x; i < MB * MB; i += THR) Q[i / MB * LQ + i % MB] = in[i];
+  const double f = in[MB * MB];
+  __syncthreads();
+  user_elements<MB>(a, s, base, n0, [&](size_t at, int j, int n, int left) {
+    const f32x4 v = read_u(a, s, at, left, whole, gs, false);
+#pragma unroll
+    for (int z = 0; z < 4; ++z)
+      if (z < left) u[s.wide ? j * LD + n + z : (j + z) * LD + n] = v[z];
+  });
+  __syncthreads();
+  f64x4 acc[T];  // all rows of 16 columns
+#pragma unroll
+  for (int i = 0; i < T; ++i) acc[i] = f64x4{0.0, 0.0, 0.0, 0.0};
+  for (int k = 0; k < MB; k += 4) {
+    const double x = u[(k + k4) * LD + wave * 16 + l16] * f;
+#pragma unroll
+    for (int i = 0; i < T; ++i) acc[i] = product(Q[(i * 16 + l16) * LQ + k + k4], x, acc[i]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < T; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) u[(i * 16 + k4 + 4 * r) * LD + wave * 16 + l16] = (float)acc[i][r];
+  __syncthreads();
+  const float lr = a.lr_dev ? *a.lr_dev : a.lr, keep = 1.f - lr * a.wd, by = lr * s.scale;
+  user_elements<MB>(a, s, base, n0, [&](size_t at, int j, int n, int left) {
+    f32x4 v;
+#pragma unroll
+    for (int z = 0; z < 4; ++z) v[z] = z < left ? u[s.wide ? j * LD + n + z : (j + z) * LD + n] : 0.f;
+    if (whole) {
+      if (s.m) {
+        f32x4 old;
+        if (s.master || a.out_f32) {
+          old = *(const f32x4*)((s.master ? s.master : (const float*)s.out) + at);
+        } else {
+          const u32x2 w = *(const u32x2*)((const uint16_t*)s.out + at);
+          old = f32x4{bf16lo(w[0]), bf16hi(w[0]), bf16lo(w[1]), bf16hi(w[1])};
+        }
+        v = old * keep - by * v;
+        if (s.master) *(f32x4*)(s.master + at) = v;
+      }
+      if (a.out_f32) *(f32x4*)((float*)s.out + at) = v;
+      else *(u32x2*)((uint16_t*)s.out + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+      return;
+    }
+#pragma unroll
+    for (int z = 0; z < 4; ++z)
+      if (z < left) {
+        float w = v[z];
+        if (s.m) {
+          const float old = s.master ? s.master[at + z] : a.out_f32 ? ((const float*)s.out)[at + z] : bf16_to_f32(((const uint16_t*)s.out)[at + z]);
+          w = old * keep - by * w;
+          if (s.master) s.master[at + z] = w;
+        }
+        if (a.out_f32) ((float*)s.out)[at + z] = w;
+        else ((uint16_t*)s.out)[at + z] = __builtin_bit_cast(uint16_t, (__bf16)w);
+      }
+  });
+}
+
+template <int MB>
+void launch(const MuonArgs& a, int steps, hipStream_t st) {
+  gram_kernel<MB><<<dim3(a.parts, a.count), THR, 0, st>>>(a);
+  steps_kernel<MB><<<a.count, MB * MB / 4, 0, st>>>(a, steps);
+  apply_kernel<MB><<<dim3((a.N + COLS - 1) / COLS, a.count), THR, 0, st>>>(a);
+}
+
+}  // namespace
+
+// Columns of a part: enough parts to spread a long matrix over the card, no more than 64 to be added up one after the other
+int thin_part(int N) {
+  const int p = (N + 63) / 64;
+  return (p < 4 * COLS ? 4 * COLS : (p + COLS - 1) / COLS * COLS);
+}
+
+hipError_t launch_muon_thin(const MuonArgs& a, int steps, hipStream_t st) {
+  if (a.M > THIN_MAX) return hipErrorInvalidValue;
+  if (a.M <= 32) launch<32>(a, steps, st);
+  else launch<64>(a, steps, st);
+  return hipGetLastError();
+}
+
+}  // namespace moe
