@@ -18,7 +18,7 @@ size_t up(size_t x) { return (x + WS_ALIGN - 1) / WS_ALIGN * WS_ALIGN; }
 struct Class {
   int M, N, Mp, Np, chunk, parts;
   bool split;
-  size_t sums, q, x, x_lo, xo, xo_lo, A, A_lo, C, C_lo, da, dc, total;
+  size_t sums, q, x, x_lo, xo, xo_lo, A, A_lo, C, C_lo, da, dc, partial, total;
 };
 
 Class class_of(int rows, int cols, long long count, bool split) {
@@ -28,6 +28,10 @@ Class class_of(int rows, int cols, long long count, bool split) {
   c.Mp = (c.M + MUON_PAD - 1) / MUON_PAD * MUON_PAD;
   c.Np = (c.N + MUON_PAD - 1) / MUON_PAD * MUON_PAD;
   c.split = split;
+  if (c.M > THIN_MAX && muon_small(c.M, c.N)) {
+    c.chunk = (int)std::min<long long>(count, 65535);  // a launch's grid
+    return c;
+  }
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -66,6 +70,9 @@ Class class_of(int rows, int cols, long long count, bool split) {
   c.C = take(k * ab);
   c.A_lo = split ? take(k * ab) : c.A;
   c.C_lo = split ? take(k * ab) : c.C;
+  // of a whole chunk and of the last
+  const int last = (int)(count % c.chunk);
+  c.partial = take(2 * (size_t)std::max(muon_runs(c.Mp, c.Np, c.chunk, split), last ? muon_runs(c.Mp, c.Np, last, split) : 0) * 128 * 128 * 4);
   c.total = o;
   return c;
 }
@@ -126,28 +133,34 @@ hipError_t run_class(MuonArgs a, const Class& c, const moe_newton_schulz& ns, in
   a.A_lo = (uint16_t*)(w + c.A_lo);
   a.C = (uint16_t*)(w + c.C);
   a.C_lo = (uint16_t*)(w + c.C_lo);
+  a.partial = (float*)(w + c.partial);
   hipError_t e = hipSuccess;
   if (c.M <= THIN_MAX) {
     a.q = (double*)(w + c.q);
     a.part = thin_part(c.N);
-    for (int first = 0; first < total && e == hipSuccess; first += c.chunk) {
-      a.first = first;
-      a.count = std::min(c.chunk, total - first);
+    for (long long first = 0; first < total && e == hipSuccess; first += c.chunk) {
+      a.first = (int)first;
+      a.count = (int)std::min<long long>(c.chunk, total - first);
       e = launch_muon_thin(a, ns.steps, st);
     }
     return e;
   }
   if (muon_small(c.M, c.N)) {
-    a.count = total;
-    return launch_muon_small(a, ns.steps, st);
+    for (long long first = 0; first < total && e == hipSuccess; first += c.chunk) {
+      a.first = (int)first;
+      a.count = (int)std::min<long long>(c.chunk, total - first);
+      e = launch_muon_small(a, ns.steps, st);
+    }
+    return e;
   }
-  for (int first = 0; first < total && e == hipSuccess; first += c.chunk) {
-    a.first = first;
-    a.count = std::min(c.chunk, total - first);
+  for (long long first = 0; first < total && e == hipSuccess; first += c.chunk) {
+    a.first = (int)first;
+    a.count = (int)std::min<long long>(c.chunk, total - first);
     a.x = (uint16_t*)(w + c.x);
     a.x_lo = (uint16_t*)(w + c.x_lo);
     a.xo = (uint16_t*)(w + c.xo);
     a.xo_lo = (uint16_t*)(w + c.xo_lo);
+    a.runs = muon_runs(c.Mp, c.Np, a.count, c.split);
     e = launch_muon_momentum(a, st);
     if (e == hipSuccess) e = launch_muon_normalize(a, st);
     for (int i = 0; i < ns.steps && e == hipSuccess; ++i) {
@@ -163,7 +176,7 @@ hipError_t run_class(MuonArgs a, const Class& c, const moe_newton_schulz& ns, in
       std::swap(a.x_lo, a.xo_lo);
     }
     // the matrices that are wide, then the others
-    const int n = std::min(std::max(wide - first, 0), a.count), all = a.count;
+    const int n = (int)std::min<long long>(std::max<long long>(wide - first, 0), a.count), all = a.count;
     for (int turned = 0; turned < 2 && e == hipSuccess; ++turned) {
       a.turned = turned;
       a.skip = turned ? n : 0;

@@ -48,6 +48,8 @@ struct MuonArgs {
   uint16_t *xo, *xo_lo;    // out; xo_lo may be x_lo without split, or NULL
   uint16_t *A, *A_lo, *C, *C_lo;
   double* q;               // thin matrices
+  int runs;                // workgroups that share Gram's matrix by parts of the reduction; 0: a tile is one workgroup's
+  float* partial;          // [2 runs][128 * 128]
   float *da, *dc;          // [count][Mp]: the diagonals of A and of a I + C, which are zero in A, and in C but for whole_c and split
 };
 
@@ -60,6 +62,8 @@ enum MuonForm {
   MF_STEP,  // X' = a X + C X
   MF_LAST   // the same into the user's matrices
 };
+// How many runs Gram's matrices of a chunk of `count` take, or 0
+int muon_runs(int Mp, int Np, long long count, bool split);
 hipError_t launch_muon_product(MuonForm form, const MuonArgs& a, hipStream_t st);
 
 // All of it for matrices with a short side of at most THIN_MAX; a.part = thin_part(N) and a.parts of them, a.sums

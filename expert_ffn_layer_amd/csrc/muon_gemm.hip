@@ -12,6 +12,7 @@
 // directions that X lacks would grow by a = 3.4 in every step. The last step has none after it: it takes x alone, and C's
 // diagonal as the fp16 that stands in C, so that it has X to read in the product only (with SPLIT every step does: the pairs
 // hold all of both).
+#include <algorithm>
 #include <type_traits>
 
 #include "muon.h"
@@ -52,8 +53,8 @@ __device__ __forceinline__ u32x4 to_rest(const Eight& r, const u32x4& hi) {
   return to_halves(d);
 }
 
-// Where the last product goes. O in the matrices' type; parameters of that type; bf16 parameters with fp32 copies
-enum Out { OUT_NONE, OUT_O, OUT_P, OUT_MASTER };
+// Where a product goes that is not whole in the workspace: sums over a part of the reduction; O in the matrices' type; parameters of that type; bf16 parameters with fp32 copies
+enum Out { OUT_NONE, OUT_PART, OUT_O, OUT_P, OUT_MASTER };
 
 // 8 consecutive fp32 (8 words) or bf16 (4 words) of a row
 template <bool F32>
@@ -89,8 +90,10 @@ __device__ __forceinline__ void store_bf16(uint16_t* p, size_t at, const Eight& 
   *(u32x4*)(p + at) = u32x4{pack_bf16x2(v.v[0], v.v[1]), pack_bf16x2(v.v[2], v.v[3]), pack_bf16x2(v.v[4], v.v[5]), pack_bf16x2(v.v[6], v.v[7])};
 }
 
+// The tile (tm, tn) of matrix b, over `once` steps of 64 reduction elements, an even number, from step `from`. OUT_PART: the
+// sums to `part`, a 4 KiB block for each 32 x 32, which has lane l's elements 4 q + j at (64 q + l) 4 + j.
 template <int FORM, int WR, int WC, int MT, int NT, int D, bool SPLIT, int OUT>
-__global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const MuonArgs a) {
+__device__ __forceinline__ void product_tile(const MuonArgs& a, const int b, const int tm, const int tn, const int from, const int once, float* part) {
   constexpr bool SYM = FORM == MF_GRAM || FORM == MF_POLY, KC = FORM == MF_GRAM;
   constexpr int BM = WR * MT * 32, BN = WC * NT * 32;
   static_assert(BM == BN, "square tiles");
@@ -109,35 +112,10 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const
   // the user's matrices have their long side first: the last product's tiles lie as they do, with X as P
   const bool turned = FORM == MF_LAST && a.turned;
 
-  // --- the tile. Workgroup b runs on XCD b % 8: each XCD gets an equal run of the chunk's tiles, matrix by matrix, so that
-  // what it runs at a time shares operands in its L2.
-  const int short_tiles = (a.Mp + BM - 1) / BM, long_tiles = (a.Np + BM - 1) / BM;
-  const int tiles = SYM ? short_tiles * (short_tiles + 1) / 2 : short_tiles * long_tiles;
-  const long long all = (long long)a.count * tiles, run = (all + NXCD - 1) / NXCD;
-  const long long id = (blockIdx.x % NXCD) * run + blockIdx.x / NXCD;
-  if (blockIdx.x / NXCD >= run || id >= all) return;
-  const int b = a.skip + (int)(id / tiles);
-  int tm, tn, rest = (int)(id % tiles);
-  if constexpr (SYM) {
-    tm = 0;
-    while (rest > tm) rest -= ++tm;
-    tn = rest;
-  } else {
-    // 4 tiles of the long side x all of the short one after each other
-    const int g = rest / (4 * short_tiles), wide = min(4, long_tiles - 4 * g);
-    rest -= g * 4 * short_tiles;
-    tn = 4 * g + rest % wide;
-    tm = rest / wide;
-    if (turned) {
-      const int t = tm;
-      tm = tn;
-      tn = t;
-    }
-  }
   const int m0 = tm * BM, n0 = tn * BM;
   const int mend = turned ? a.Np : a.Mp, nend = SYM || turned ? a.Mp : a.Np;
   const size_t xat = (size_t)b * a.Mp * a.Np, aat = (size_t)b * a.Mp * a.Mp;
-  const int K = KC ? a.Np : a.Mp, once = K / BK, nsteps = SPLIT ? 3 * once : once;
+  const int nsteps = SPLIT ? 3 * once : once;
 
   // --- loads: this wave's units of both operands; the lower halves of pairs lie `p_lo`, `q_lo` bytes behind the upper
   const uint8_t *psrc[U], *qsrc[U];
@@ -145,7 +123,7 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const
   int pld, qld;
   ptrdiff_t p_lo = 0, q_lo = 0;
   if constexpr (FORM == MF_GRAM) {
-    p = q = a.x + xat;
+    p = q = a.x + xat + from * BK;
     pld = qld = a.Np;
     if (SPLIT) p_lo = q_lo = (const uint8_t*)a.x_lo - (const uint8_t*)a.x;
   } else if constexpr (FORM == MF_POLY) {
@@ -333,6 +311,17 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const
   // 16-byte chunk c of a row sits at c ^ (row % 16), which keeps both directions free of bank conflicts. Mirrored blocks pass
   // through another 4.5 KiB as 64 rows of 32, 72 bytes apart. The parts of the ring serve for both.
   __builtin_amdgcn_s_barrier();
+  if constexpr (OUT == OUT_PART) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *(f32x4*)(part + ((wr * MT + i) * (WC * NT) + wc * NT + t) * 1024 + (64 * j + lane) * 4) =
+              f32x4{acc[t][i][4 * j], acc[t][i][4 * j + 1], acc[t][i][4 * j + 2], acc[t][i][4 * j + 3]};
+    return;
+  }
   constexpr bool FOUR = HV || D == 4;  // parts of an operand
   static_assert((FOUR ? PART : PART / 2) >= 8192, "a part of the ring per wave");
   lds_byte* const ep = !FOUR ? (lds_byte*)(wave & 2 ? q1 : q0) + (wave & 1) * (PART / 2) : (lds_byte*)(wave == 0 ? q0 : wave == 1 ? q1 : wave == 2 ? q2 : q3);
@@ -511,6 +500,118 @@ __global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const
   }
 }
 
+// Row and column of a symmetric product's tile `rest`
+__device__ __forceinline__ void lower_tile(int rest, int& tm, int& tn) {
+  tm = 0;
+  while (rest > tm) rest -= ++tm;
+  tn = rest;
+}
+
+// Workgroup b runs on XCD b % 8: each XCD gets an equal run of the chunk's tiles, matrix by matrix, so that what it runs at a
+// time shares operands in its L2.
+template <int FORM, int WR, int WC, int MT, int NT, int D, bool SPLIT, int OUT>
+__global__ void __launch_bounds__(THR, MT * NT > 8 ? 1 : 2) product_kernel(const MuonArgs a) {
+  constexpr bool SYM = FORM == MF_GRAM || FORM == MF_POLY;
+  constexpr int BM = WR * MT * 32;
+  const int short_tiles = (a.Mp + BM - 1) / BM, long_tiles = (a.Np + BM - 1) / BM;
+  const int tiles = SYM ? short_tiles * (short_tiles + 1) / 2 : short_tiles * long_tiles;
+  const long long all = (long long)a.count * tiles, run = (all + NXCD - 1) / NXCD;
+  const long long id = (blockIdx.x % NXCD) * run + blockIdx.x / NXCD;
+  if (blockIdx.x / NXCD >= run || id >= all) return;
+  int tm, tn, rest = (int)(id % tiles);
+  if constexpr (SYM) {
+    lower_tile(rest, tm, tn);
+  } else {
+    // 4 tiles of the long side x all of the short one after each other
+    const int g = rest / (4 * short_tiles), wide = min(4, long_tiles - 4 * g);
+    rest -= g * 4 * short_tiles;
+    tn = 4 * g + rest % wide;
+    tm = rest / wide;
+    // the user's matrices have their long side first: the last product's tiles lie as they do, with X as P
+    if (FORM == MF_LAST && a.turned) {
+      const int t = tm;
+      tm = tn;
+      tn = t;
+    }
+  }
+  product_tile<FORM, WR, WC, MT, NT, D, SPLIT, OUT>(a, a.skip + (int)(id / tiles), tm, tn, 0, (FORM == MF_GRAM ? a.Np : a.Mp) / BK, nullptr);
+}
+
+// Gram's matrix of few tiles of 128 x 128 with a long reduction: the pairs of steps of all tiles, one tile's after the other's,
+// go in equal runs to a.runs workgroups, at least as many as tiles, so that a run touches two tiles at most. The sums over
+// its part of each go to the workspace and are added up by joined_kernel, in order.
+struct Runs {
+  int each, work, runs;  // pairs of steps of a tile, of all
+  __device__ int start(int g) const { return (int)((unsigned)g * (unsigned)work / (unsigned)runs); }  // at most 256 * 128 * 8192
+};
+__device__ __forceinline__ Runs runs_of(const MuonArgs& a, int tiles) { return Runs{a.Np / 128, a.Np / 128 * tiles * a.count, a.runs}; }
+
+template <bool SPLIT>
+__global__ void __launch_bounds__(THR, 2) runs_kernel(const MuonArgs a) {
+  const int side = a.Mp / 128, tiles = side * (side + 1) / 2, of_xcd = (a.runs + NXCD - 1) / NXCD;
+  const int g = blockIdx.x % NXCD * of_xcd + blockIdx.x / NXCD;
+  if (blockIdx.x / NXCD >= of_xcd || g >= a.runs) return;
+  const Runs r = runs_of(a, tiles);
+  const int end = r.start(g + 1);
+  int part = 2 * g;
+#pragma nounroll
+  for (int at = r.start(g); at < end;) {
+    const int tile = at / r.each, from = at - tile * r.each, n = min(end - at, r.each - from);
+    int tm, tn;
+    lower_tile(tile % tiles, tm, tn);
+    product_tile<MF_GRAM, 2, 2, 2, 2, 4, SPLIT, OUT_PART>(a, tile / tiles, tm, tn, 2 * from, 2 * n, a.partial + (size_t)part++ * (128 * 128));
+    at += n;
+  }
+}
+
+// A workgroup adds up 32 x 32 elements, a lane four of a row, and writes them to both places of A
+template <bool SPLIT>
+__global__ void __launch_bounds__(256) joined_kernel(const MuonArgs a) {
+  __shared__ float v[32][33];
+  const int side = a.Mp / 128, tiles = side * (side + 1) / 2, tile = blockIdx.x >> 4, sub = blockIdx.x & 15;
+  const Runs r = runs_of(a, tiles);
+  // the runs g that meet the tile; only the first may have another tile before it
+  const int begin = tile * r.each, end = begin + r.each;
+  int g = (int)((unsigned)begin * (unsigned)r.runs / (unsigned)r.work), last = min((int)((unsigned)end * (unsigned)r.runs / (unsigned)r.work), r.runs - 1);
+  while (r.start(g + 1) <= begin) ++g;
+  while (r.start(last) >= end) --last;
+  const float* from = a.partial + sub * 1024 + threadIdx.x * 4;
+  f32x4 sum = *(const f32x4*)(from + (size_t)(2 * g + (r.start(g) < begin)) * (128 * 128));
+  from += (size_t)(2 * g) * (128 * 128);
+#pragma unroll 8
+  for (++g; g <= last; ++g) sum += *(const f32x4*)(from += 2 * 128 * 128);
+  int tm, tn;
+  lower_tile(tile % tiles, tm, tn);
+  const int b = tile / tiles, lane = threadIdx.x & 63;
+  const int row = lane & 31, col = (threadIdx.x >> 6) * 8 + (lane >> 5) * 4;
+  const int m0 = tm * 128 + (sub >> 2) * 32, n0 = tn * 128 + (sub & 3) * 32;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float w = sum[j] * (1.f / MUON_SCALE);
+    if (m0 + row == n0 + col + j) {
+      a.da[(size_t)b * a.Mp + m0 + row] = w * (1.f / MUON_SCALE);
+      w = 0.f;
+    }
+    v[row][col + j] = w;
+  }
+  __syncthreads();
+  const int at = threadIdx.x >> 3, c = threadIdx.x & 7;
+  auto write = [&](size_t to, const f32x4& w) {
+    typedef __attribute__((ext_vector_type(4))) _Float16 f16x4;
+    f16x4 hi, lo;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      hi[j] = (_Float16)w[j];
+      lo[j] = (_Float16)(w[j] - (float)hi[j]);
+    }
+    *(f16x4*)(a.A + to) = hi;
+    if (SPLIT) *(f16x4*)(a.A_lo + to) = lo;
+  };
+  const size_t aat = (size_t)b * a.Mp * a.Mp;
+  write(aat + (size_t)(m0 + at) * a.Mp + n0 + c * 4, f32x4{v[at][c * 4], v[at][c * 4 + 1], v[at][c * 4 + 2], v[at][c * 4 + 3]});
+  if (tm != tn) write(aat + (size_t)(n0 + at) * a.Mp + m0 + c * 4, f32x4{v[c * 4][at], v[c * 4 + 1][at], v[c * 4 + 2][at], v[c * 4 + 3][at]});
+}
+
 template <int FORM, int WR, int WC, int MT, int NT, int D>
 hipError_t launch(const MuonArgs& a, hipStream_t st) {
   constexpr int B = WR * MT * 32;
@@ -538,6 +639,8 @@ hipError_t launch(const MuonArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+constexpr long long CUS = 256;
+
 template <int FORM>
 hipError_t choose(const MuonArgs& a, hipStream_t st) {
   auto tiles = [&](int b) {
@@ -550,9 +653,34 @@ hipError_t choose(const MuonArgs& a, hipStream_t st) {
 
 }  // namespace
 
+// Runs are worth it where the tiles leave most CUs idle: bf16, 1 of 1024 x 4096 (36 tiles) takes 29.6 us by tiles and 13.8 + 5.6
+// by runs and sums, 2 of 1024 x 2048 (72) 18.5 and 13.5 + 5.8; fp32, 2 of 79 x 4042 (2) 74 and 7.9 + 6.1, 8 of 1000 x 500 (80) 28
+// and 16.2 + 6.3. With more tiles a step waits for its operands: tiles that go through the reduction together share them in
+// their XCD's L2, runs do not (1 of 2048 x 7168, 136 tiles: 64 and 58 + 11). A run has two pairs of steps at least, and saves six
+// (f32: a pair counts for three): 1 of 200 x 1000 (3 tiles of 8 pairs) takes 11.5 us by tiles and 5.9 + 3.4 by runs.
+int muon_runs(int Mp, int Np, long long count, bool split) {
+  const long long side = Mp / 128, tiles = side * (side + 1) / 2 * count, each = Np / 128, pair = split ? 3 : 1;
+  if (tiles > (split ? CUS / 2 : CUS / 4)) return 0;
+  const long long work = tiles * each, runs = std::max(std::min({CUS, work, work * pair / 2}), tiles);
+  return (each - work / runs) * pair >= 6 ? (int)runs : 0;
+}
+
 hipError_t launch_muon_product(MuonForm form, const MuonArgs& a, hipStream_t st) {
   switch (form) {
-    case MF_GRAM: return choose<MF_GRAM>(a, st);
+    case MF_GRAM:
+      if (a.runs) {
+        const int side = a.Mp / 128, tiles = side * (side + 1) / 2 * a.count;
+        const unsigned grid = (unsigned)((a.runs + NXCD - 1) / NXCD * NXCD);
+        if (a.split) {
+          runs_kernel<true><<<grid, THR, 0, st>>>(a);
+          joined_kernel<true><<<tiles * 16, 256, 0, st>>>(a);
+        } else {
+          runs_kernel<false><<<grid, THR, 0, st>>>(a);
+          joined_kernel<false><<<tiles * 16, 256, 0, st>>>(a);
+        }
+        return hipGetLastError();
+      }
+      return choose<MF_GRAM>(a, st);
     case MF_POLY: return choose<MF_POLY>(a, st);
     case MF_STEP: return choose<MF_STEP>(a, st);
     case MF_LAST: return choose<MF_LAST>(a, st);

@@ -68,6 +68,16 @@ def test_many_tiles(kind):
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("count,rows,cols", [(1, 70, 900), (2, 79, 4042), (1, 6100, 150), (1, 400, 9000), (5, 380, 1100)])
+def test_few_tiles_with_a_long_reduction(count, rows, cols, kind):
+    say("orthogonalize", count, rows, cols, kind)
+    g = matrices(count, rows, cols, kind, seed=rows)
+    o = orthogonalize(g, kind)
+    verify(g, o, kind)
+    assert torch.equal(o, orthogonalize(g, kind))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
 def test_long_stack(kind):
     """More matrices than are worked on at a time."""
     g = matrices(2500, 8, 11, kind, seed=3, rank=2)
