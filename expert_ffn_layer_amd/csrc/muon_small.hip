@@ -79,73 +79,90 @@ __global__ void __launch_bounds__(64 * WAVES) small_kernel(const MuonArgs a, int
   const int row = wm * 32 + (lane & 31), hi4 = 4 * (lane >> 5);
   const MuonStack s = muon_stack(a, a.first + blockIdx.x);
   const int M = a.M, N = a.N;
-  const bool g_f32 = a.g_f32, out_f32 = a.out_f32, nesterov = a.nesterov, rescale = a.grad_scale != nullptr;
+  const bool g_f32 = a.g_f32, out_f32 = a.out_f32, nesterov = a.nesterov;
   const float mu = a.momentum, pa = (float)a.a, pb = (float)a.b, pc = (float)a.c;
   const size_t base = (size_t)(a.first + blockIdx.x - s.first) * M * N;
-  f32x16 x[TILES];
-#pragma unroll
-  for (int i = 0; i < TILES; ++i)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) x[i][e] = 0.f;
-  // the user's elements: f(X's tile, element of it, place), 4 at a time where they lie together
+  // A tile of the user's elements, 4 at a time where they lie together. No load waits for another: what lies outside reads the
+  // matrix's first element, and counts as 0.
   const bool fours = s.wide && N % 4 == 0;
-  auto each = [&](auto f4, auto f1) __attribute__((always_inline)) {
-    each_of<TILES>([&](auto tile) __attribute__((always_inline)) {
-      constexpr int i = decltype(tile)::value;
-      __asm__ volatile("" ::: "memory");  // a tile at a time: all at once need more registers than there are
-      const int n0 = (wn + i * WN) * 32 + hi4;
-      if (fours) {
+  const int row_step = s.wide ? N : 1, col_step = s.wide ? 1 : M;
+  auto column = [&](int i, int e) { return (wn + i * WN) * 32 + hi4 + 8 * (e >> 2) + (e & 3); };
+  auto load = [&](const void* from, bool f32, int i) __attribute__((always_inline)) {
+    f32x16 t;
+    if (fours) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (row < M && n0 + 8 * q < N) f4(x[i], 4 * q, base + (size_t)row * N + n0 + 8 * q);
-      } else {
+      for (int q = 0; q < 4; ++q) {
+        const int n = column(i, 4 * q);
+        const size_t at = base + (row < M && n < N ? row * N + n : 0);
+        f32x4 v;
+        if (f32) {
+          v = *(const f32x4*)((const float*)from + at);
+        } else {
+          const u32x2 w = *(const u32x2*)((const uint16_t*)from + at);
+          v = f32x4{bf16lo(w[0]), bf16hi(w[0]), bf16lo(w[1]), bf16hi(w[1])};
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t[4 * q + j] = row < M && n < N ? v[j] : 0.f;
+      }
+    } else {
+      auto all = [&](auto one) __attribute__((always_inline)) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const int n = n0 + 8 * (e >> 2) + (e & 3);
-          if (row < M && n < N) f1(x[i], e, base + (s.wide ? (size_t)row * N + n : (size_t)n * M + row));
+          const int n = column(i, e);
+          t[e] = one(base + (row < M && n < N ? row * row_step + n * col_step : 0));
         }
+      };
+      if (f32) all([&](size_t at) __attribute__((always_inline)) { return ((const float*)from)[at]; });
+      else all([&](size_t at) __attribute__((always_inline)) { return bf16_to_f32(((const uint16_t*)from)[at]); });
+#pragma unroll
+      for (int e = 0; e < 16; ++e) t[e] = row < M && column(i, e) < N ? t[e] : 0.f;
+    }
+    return t;
+  };
+  auto store = [&](void* to, bool f32, int i, const f32x16& t) __attribute__((always_inline)) {
+    if (fours) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int n = column(i, 4 * q);
+        if (row >= M || n >= N) continue;
+        const size_t at = base + row * N + n;
+        if (f32) *(f32x4*)((float*)to + at) = f32x4{t[4 * q], t[4 * q + 1], t[4 * q + 2], t[4 * q + 3]};
+        else *(u32x2*)((uint16_t*)to + at) = u32x2{pack_bf16x2(t[4 * q], t[4 * q + 1]), pack_bf16x2(t[4 * q + 2], t[4 * q + 3])};
       }
-    });
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int n = column(i, e);
+        if (row >= M || n >= N) continue;
+        const size_t at = base + row * row_step + n * col_step;
+        if (f32) ((float*)to)[at] = t[e];
+        else ((uint16_t*)to)[at] = __builtin_bit_cast(uint16_t, (__bf16)t[e]);
+      }
+    }
   };
 
   // --- u, the new momentum and the norm
-  const float gs = a.grad_scale ? *a.grad_scale : 1.f;
-  auto scaled = [&](float g) { return rescale ? g * gs : g; };
-  auto momentum = [&](float g, float& m) {
-    m = mu * m + g;
-    return nesterov ? g + mu * m : m;
-  };
-  each(
-      [&](f32x16& t, int e, size_t at) __attribute__((always_inline)) {
-        f32x4 u, m;
-        if (g_f32) {
-          u = *(const f32x4*)((const float*)s.g + at);
-        } else {
-          const u32x2 w = *(const u32x2*)((const uint16_t*)s.g + at);
-          u = f32x4{bf16lo(w[0]), bf16hi(w[0]), bf16lo(w[1]), bf16hi(w[1])};
-        }
-        if (s.m) m = *(const f32x4*)(s.m + at);
+  f32x16 x[TILES];
+  each_of<TILES>([&](auto tile) __attribute__((always_inline)) { x[decltype(tile)::value] = load(s.g, g_f32, decltype(tile)::value); });
+  if (a.grad_scale) {
+    const float gs = *a.grad_scale;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          u[j] = scaled(u[j]);
-          if (s.m) {
-            float mj = m[j];
-            u[j] = momentum(u[j], mj);
-            m[j] = mj;
-          }
-          t[e + j] = u[j];
-        }
-        if (s.m) *(f32x4*)(s.m + at) = m;
-      },
-      [&](f32x16& t, int e, size_t at) __attribute__((always_inline)) {
-        float u = scaled(g_f32 ? ((const float*)s.g)[at] : bf16_to_f32(((const uint16_t*)s.g)[at]));
-        if (s.m) {
-          float m = s.m[at];
-          u = momentum(u, m);
-          s.m[at] = m;
-        }
-        t[e] = u;
-      });
+    for (int i = 0; i < TILES; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[i][e] *= gs;
+  }
+  if (s.m) {
+    each_of<TILES>([&](auto tile) __attribute__((always_inline)) {
+      constexpr int i = decltype(tile)::value;
+      f32x16 m = load(s.m, true, i);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        m[e] = mu * m[e] + x[i][e];
+        x[i][e] = nesterov ? x[i][e] + mu * m[e] : m[e];
+      }
+      store(s.m, true, i, m);
+    });
+  }
   double sum = 0.0;
 #pragma unroll
   for (int i = 0; i < TILES; ++i)
@@ -321,36 +338,19 @@ __global__ void __launch_bounds__(64 * WAVES) small_kernel(const MuonArgs a, int
 
   // --- O, or the parameters' step
   const float lr = a.lr_dev ? *a.lr_dev : a.lr, keep = 1.f - lr * a.wd, by = lr * s.scale;
-  each(
-      [&](f32x16& t, int e, size_t at) __attribute__((always_inline)) {
-        f32x4 v;
+  each_of<TILES>([&](auto tile) __attribute__((always_inline)) {
+    constexpr int i = decltype(tile)::value;
+    f32x16 v;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = t[e + j] * inv;
-        if (s.m) {
-          f32x4 old;
-          if (s.master || out_f32) {
-            old = *(const f32x4*)((s.master ? s.master : (const float*)s.out) + at);
-          } else {
-            const u32x2 w = *(const u32x2*)((const uint16_t*)s.out + at);
-            old = f32x4{bf16lo(w[0]), bf16hi(w[0]), bf16lo(w[1]), bf16hi(w[1])};
-          }
+    for (int e = 0; e < 16; ++e) v[e] = x[i][e] * inv;
+    if (s.m) {
+      const f32x16 old = load(s.master ? s.master : s.out, s.master || out_f32, i);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = old[j] * keep - by * v[j];
-          if (s.master) *(f32x4*)(s.master + at) = v;
-        }
-        if (out_f32) *(f32x4*)((float*)s.out + at) = v;
-        else *(u32x2*)((uint16_t*)s.out + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-      },
-      [&](f32x16& t, int e, size_t at) __attribute__((always_inline)) {
-        float v = t[e] * inv;
-        if (s.m) {
-          const float old = s.master ? s.master[at] : out_f32 ? ((const float*)s.out)[at] : bf16_to_f32(((const uint16_t*)s.out)[at]);
-          v = old * keep - by * v;
-          if (s.master) s.master[at] = v;
-        }
-        if (out_f32) ((float*)s.out)[at] = v;
-        else ((uint16_t*)s.out)[at] = __builtin_bit_cast(uint16_t, (__bf16)v);
-      });
+      for (int e = 0; e < 16; ++e) v[e] = old[e] * keep - by * v[e];
+      if (s.master) store(s.master, true, i, v);
+    }
+    store(s.out, out_f32, i, v);
+  });
 }
 
 template <int TILES>
