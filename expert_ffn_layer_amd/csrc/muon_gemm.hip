@@ -177,6 +177,59 @@ __device__ __forceinline__ void product_tile(const MuonArgs& a, const int b, con
     load_one(qsrc[u], Q_PART(decltype(slot)::value, u >= U / 2) + (HV ? un % (T::UNITS / 2) : un) * 1024, step, qstride, q_lo, -q_lo);
   };
 
+  // --- for the results
+  const float inv = 1.f / MUON_SCALE, pa = (float)a.a, pb = (float)a.b, pc = (float)a.c;
+  const int wrow = m0 + wr * MT * 32, wcol = n0 + wc * NT * 32, r32 = lane & 31, hi4 = lane >> 5, c8 = lane & 7, r8 = lane >> 3;
+  constexpr int BLOCKS = NT / 2, ALL = MT * BLOCKS;
+  const float* const diagonal = FORM == MF_GRAM ? nullptr : (FORM == MF_POLY ? a.da : a.dc) + (size_t)b * a.Mp;
+  // What a block's results are formed with, the elements themselves of A or X and the diagonal, or the user's parameters, is
+  // fetched AHEAD - 1 blocks before: a block takes about 1 us, a load from memory 2 to 3 while all CUs write. Where there are
+  // few tiles, all of it before the reduction.
+  constexpr bool OLD_HI = FORM == MF_POLY || (FORM == MF_STEP && !SPLIT), OLD_LO = (FORM == MF_POLY && SPLIT) || (FORM == MF_STEP && !SPLIT);
+  constexpr bool OLD_P = OUT == OUT_P || OUT == OUT_MASTER, P_F32 = SPLIT || OUT == OUT_MASTER;
+  constexpr int AHEAD = ALL < 3 ? ALL : 3;
+  const uint16_t* const old_hi = FORM == MF_POLY ? a.A + aat : a.x + xat;
+  const uint16_t* const old_lo = FORM == MF_POLY ? a.A_lo + aat : a.x_lo + xat;
+  const int ld = FORM == MF_POLY ? a.Mp : a.Np;
+  const MuonStack* const user = FORM == MF_LAST ? &muon_stack(a, a.first + b) : nullptr;
+  const int rows = turned ? a.N : a.M, cols = turned ? a.M : a.N;  // of the user's matrix
+  const size_t uat = FORM == MF_LAST ? (size_t)(a.first + b - user->first) * a.M * a.N : 0;
+  const bool whole = cols % 8 == 0;  // rows and matrices begin on 16 bytes, and no 8 columns pass their end
+  void* const params = FORM == MF_LAST ? (OUT == OUT_MASTER ? (void*)user->master : user->out) : nullptr;
+  float keep = 0.f, step = 0.f;
+  if constexpr (OLD_P) {
+    const float lr = a.lr_dev ? *a.lr_dev : a.lr;
+    keep = 1.f - lr * a.wd;
+    step = lr * user->scale;
+  }
+  float dm[AHEAD][OLD_HI ? 4 : 1];
+  f32x4 dn[AHEAD][FORM == MF_POLY ? 2 : 1];  // at this lane's columns
+  u32x4 hw[AHEAD][OLD_HI ? 4 : 1], lw[AHEAD][OLD_LO ? 4 : 1];
+  Row8<P_F32> pw[AHEAD][OLD_P ? 4 : 1];
+  auto fetch = [&](int blk) __attribute__((always_inline)) {
+    const int n = wcol + blk % BLOCKS * 64 + c8 * 8, set = blk % AHEAD;
+    if constexpr (FORM == MF_POLY) {
+#pragma unroll
+      for (int z = 0; z < 2; ++z) dn[set][z] = *(const f32x4*)(diagonal + (n < nend ? n : 0) + 4 * z);
+    }
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int m = wrow + blk / BLOCKS * 32 + it * 8 + r8;
+      // past the end an element that exists, which is not used
+      const size_t at = m < mend && n < nend ? (size_t)m * ld + n : 0;
+      if constexpr (OLD_HI) dm[set][it] = diagonal[m < mend ? m : 0];
+      if constexpr (OLD_HI) hw[set][it] = *(const u32x4*)(old_hi + at);
+      if constexpr (OLD_LO) lw[set][it] = *(const u32x4*)(old_lo + at);
+      if constexpr (OLD_P)
+        if (whole) pw[set][it] = load8<P_F32>(params, uat + (m < rows && n < cols ? (size_t)m * cols + n : 0));
+    }
+  };
+  constexpr bool EARLY = D == 4 && ALL <= AHEAD;
+  if constexpr (EARLY) {
+#pragma unroll
+    for (int blk = 0; blk < ALL; ++blk) fetch(blk);
+  }
+
   f32x16 acc[NT][MT];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -326,52 +379,16 @@ __device__ __forceinline__ void product_tile(const MuonArgs& a, const int b, con
   static_assert((FOUR ? PART : PART / 2) >= 8192, "a part of the ring per wave");
   lds_byte* const ep = !FOUR ? (lds_byte*)(wave & 2 ? q1 : q0) + (wave & 1) * (PART / 2) : (lds_byte*)(wave == 0 ? q0 : wave == 1 ? q1 : wave == 2 ? q2 : q3);
   lds_byte* const mirror = !FOUR ? (lds_byte*)(wave & 2 ? p1 : p0) + (wave & 1) * (PART / 2) : (lds_byte*)(wave == 0 ? p0 : wave == 1 ? p1 : wave == 2 ? p2 : p3);
-  const float inv = 1.f / MUON_SCALE, pa = (float)a.a, pb = (float)a.b, pc = (float)a.c;
-  const int wrow = m0 + wr * MT * 32, wcol = n0 + wc * NT * 32, r32 = lane & 31, hi4 = lane >> 5, c8 = lane & 7, r8 = lane >> 3;
   // The lanes of a wave exchange data through LDS: its accesses run in the order in which they are issued, and this keeps
   // the compiler from changing that order.
   auto in_order = [] { __asm__ volatile("" ::: "memory"); };
-  constexpr int BLOCKS = NT / 2, ALL = MT * BLOCKS;
-  const float* const diagonal = FORM == MF_GRAM ? nullptr : (FORM == MF_POLY ? a.da : a.dc) + (size_t)b * a.Mp;
-  // What a block's results are formed with is fetched AHEAD blocks before: the elements themselves of A or X, or the
-  // user's parameters. A block takes about 1 us, a load from memory 2 to 3 while all CUs write.
-  constexpr bool OLD_HI = FORM == MF_POLY || (FORM == MF_STEP && !SPLIT), OLD_LO = (FORM == MF_POLY && SPLIT) || (FORM == MF_STEP && !SPLIT);
-  constexpr bool OLD_P = OUT == OUT_P || OUT == OUT_MASTER, P_F32 = SPLIT || OUT == OUT_MASTER;
-  constexpr int AHEAD = ALL < 3 ? ALL : 3;
-  const uint16_t* const old_hi = FORM == MF_POLY ? a.A + aat : a.x + xat;
-  const uint16_t* const old_lo = FORM == MF_POLY ? a.A_lo + aat : a.x_lo + xat;
-  const int ld = FORM == MF_POLY ? a.Mp : a.Np;
-  const MuonStack* const user = FORM == MF_LAST ? &muon_stack(a, a.first + b) : nullptr;
-  const int rows = turned ? a.N : a.M, cols = turned ? a.M : a.N;  // of the user's matrix
-  const size_t uat = FORM == MF_LAST ? (size_t)(a.first + b - user->first) * a.M * a.N : 0;
-  const bool whole = cols % 8 == 0;  // rows and matrices begin on 16 bytes, and no 8 columns pass their end
-  void* const params = FORM == MF_LAST ? (OUT == OUT_MASTER ? (void*)user->master : user->out) : nullptr;
-  float keep = 0.f, step = 0.f;
-  if constexpr (OLD_P) {
-    const float lr = a.lr_dev ? *a.lr_dev : a.lr;
-    keep = 1.f - lr * a.wd;
-    step = lr * user->scale;
+  if constexpr (!EARLY) {
+#pragma unroll
+    for (int blk = 0; blk < AHEAD - 1; ++blk) fetch(blk);
   }
-  u32x4 hw[AHEAD][OLD_HI ? 4 : 1], lw[AHEAD][OLD_LO ? 4 : 1];
-  Row8<P_F32> pw[AHEAD][OLD_P ? 4 : 1];
-  auto fetch = [&](int blk) __attribute__((always_inline)) {
-    const int n = wcol + blk % BLOCKS * 64 + c8 * 8, set = blk % AHEAD;
-#pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const int m = wrow + blk / BLOCKS * 32 + it * 8 + r8;
-      // past the end an element that exists, which is not used
-      const size_t at = m < mend && n < nend ? (size_t)m * ld + n : 0;
-      if constexpr (OLD_HI) hw[set][it] = *(const u32x4*)(old_hi + at);
-      if constexpr (OLD_LO) lw[set][it] = *(const u32x4*)(old_lo + at);
-      if constexpr (OLD_P)
-        if (whole) pw[set][it] = load8<P_F32>(params, uat + (m < rows && n < cols ? (size_t)m * cols + n : 0));
-    }
-  };
-#pragma unroll
-  for (int blk = 0; blk < AHEAD - 1; ++blk) fetch(blk);
 #pragma unroll
   for (int blk = 0; blk < ALL; ++blk) {
-    if (blk + AHEAD - 1 < ALL) fetch(blk + AHEAD - 1);
+    if (!EARLY && blk + AHEAD - 1 < ALL) fetch(blk + AHEAD - 1);
     const int i = blk / BLOCKS, n = wcol + blk % BLOCKS * 64 + c8 * 8, set = blk % AHEAD;
     in_order();
 #pragma unroll
@@ -382,11 +399,6 @@ __device__ __forceinline__ void product_tile(const MuonArgs& a, const int b, con
         *(lds_f32x4*)(ep + r32 * 256 + (((z * 8 + 2 * j + hi4) ^ (r32 & 15)) << 4)) = f32x4{v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
     }
     in_order();
-    Eight dn;  // the diagonal at this lane's columns
-    if constexpr (FORM == MF_POLY) {
-#pragma unroll
-      for (int z = 0; z < 8; ++z) dn.v[z] = diagonal[n < nend ? n + z : z];
-    }
     u32x4 low[4];
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
@@ -408,17 +420,17 @@ __device__ __forceinline__ void product_tile(const MuonArgs& a, const int b, con
         for (int z = 0; z < 8; ++z) x.v[z] += lo.v[z];
       }
       if constexpr (SYM) {
-        const float dm = FORM == MF_POLY ? diagonal[m < mend ? m : 0] : 0.f;
         Eight q = r;
         if constexpr (FORM == MF_POLY) {
 #pragma unroll
-          for (int z = 0; z < 8; ++z) q.v[z] = pb * x.v[z] + pc * ((dm + dn.v[z]) * x.v[z] + r.v[z]);
+          for (int z = 0; z < 8; ++z) q.v[z] = pb * x.v[z] + pc * ((dm[set][it] + dn[set][z >> 2][z & 3]) * x.v[z] + r.v[z]);
         }
         if (tm == tn) {
 #pragma unroll
           for (int z = 0; z < 8; ++z)
             if (m == n + z) {
-              const float d = FORM == MF_GRAM ? r.v[z] * inv : pa + pb * dm + pc * (dm * dm + r.v[z] * inv);
+              float d = r.v[z] * inv;
+              if constexpr (FORM == MF_POLY) d = pa + pb * dm[set][it] + pc * (dm[set][it] * dm[set][it] + d);
               if (inside) (FORM == MF_GRAM ? a.da : a.dc)[(size_t)b * a.Mp + m] = d;
               // C keeps its diagonal where the product that reads it adds nothing to it
               q.v[z] = FORM == MF_POLY && (SPLIT || a.whole_c) ? d * MUON_SCALE : 0.f;
@@ -438,9 +450,8 @@ __device__ __forceinline__ void product_tile(const MuonArgs& a, const int b, con
         }
       } else if constexpr (FORM == MF_STEP) {
         if constexpr (!SPLIT) {
-          const float f = diagonal[m < mend ? m : 0];
 #pragma unroll
-          for (int z = 0; z < 8; ++z) r.v[z] += f * x.v[z];
+          for (int z = 0; z < 8; ++z) r.v[z] += dm[set][it] * x.v[z];
         }
         const u32x4 hi = to_halves(r);
         if (inside) *(u32x4*)(a.xo + xat + (size_t)m * a.Np + n) = hi;
