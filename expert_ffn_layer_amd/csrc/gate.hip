@@ -94,8 +94,20 @@ __device__ __forceinline__ double reduce64(double v, int lanes, F f) {
   if (lanes > 2) both([](uint32_t x) { return dpp<0x4E>(x); });
   if (lanes > 4) both([](uint32_t x) { return dpp<0x141>(x); });
   if (lanes > 8) both([](uint32_t x) { return dpp<0x140>(x); });
-  for (int d = 16; d < lanes; d <<= 1) both([&](uint32_t x) { return (uint32_t)__shfl_xor((int)x, d); });
+  auto halves = [&](auto swap) {
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    const auto lo = swap((uint32_t)u), hi = swap((uint32_t)(u >> 32));
+    v = f(__longlong_as_double((long long)((uint64_t)hi[0] << 32 | lo[0])), __longlong_as_double((long long)((uint64_t)hi[1] << 32 | lo[1])));
+  };
+  if (lanes > 16) halves([](uint32_t x) { return __builtin_amdgcn_permlane16_swap(x, x, false, false); });
+  if (lanes > 32) halves([](uint32_t x) { return __builtin_amdgcn_permlane32_swap(x, x, false, false); });
   return v;
+}
+// v of a lane that is the same for all
+__device__ __forceinline__ double of_lane(double v, int lane) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane), hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+  return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
 }
 __device__ __forceinline__ double larger64(double a, double b) { return a > b ? a : b; }
 __device__ __forceinline__ double sum64(double a, double b) { return a + b; }
@@ -324,6 +336,7 @@ __device__ __forceinline__ Place place_of(const GateArgs& a, int q, bool on) {
 template <int LN>
 __device__ __forceinline__ bool group_stays(const GateArgs& a, const Place& p, float worth, int first_lane) {
   int rank = 0;
+#pragma unroll 4
   for (int o = 0; o < a.groups; ++o) {
     const float w = __shfl(worth, first_lane + o * p.lanes);
     rank += w > worth || (w == worth && o < p.g);
@@ -412,16 +425,20 @@ __device__ __forceinline__ void exact_token(const GateArgs& a, long long t, Row 
   const int lane = threadIdx.x & 63;
   const Place p = place_of<64>(a, lane, true);
   double c[PL], inv = 1.0, z = 0.0;
+  float l[PL], b[PL];
 #pragma unroll
   for (int j = 0; j < PL; ++j) {
-    const double l = j < p.n ? row(p.e0 + j) : -INFINITY;
-    c[j] = a.sigmoid ? sigmoid64(l) : exp(l - (double)m);
+    l[j] = j < p.n ? row(p.e0 + j) : -INFINITY;
+    b[j] = a.bias ? a.bias[j < p.n ? p.e0 + j : 0] : 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < PL; ++j) {
+    c[j] = exp(a.sigmoid ? -(double)l[j] : (double)l[j] - (double)m);
     z += c[j];
   }
   if (!a.sigmoid) inv = 1.0 / reduce64(z, 64, sum64);
 #pragma unroll
-  for (int j = 0; j < PL; ++j)
-    c[j] = j < p.n && row(p.e0 + j) > -INFINITY ? c[j] * inv + (a.bias ? (double)a.bias[p.e0 + j] : 0.0) : -INFINITY;
+  for (int j = 0; j < PL; ++j) c[j] = l[j] > -INFINITY ? (a.sigmoid ? 1.0 / (1.0 + c[j]) : c[j] * inv) + (double)b[j] : -INFINITY;
   if (a.groups > 1) {
     // the largest of the group, and the largest of the others: all but the first place that has it
     double here = c[0];
@@ -444,13 +461,13 @@ __device__ __forceinline__ void exact_token(const GateArgs& a, long long t, Row 
     }
     int rank = 0;
     for (int o = 0; o < a.groups; ++o) {
-      const double w = __shfl(worth, o * p.lanes);
+      const double w = of_lane(worth, o * p.lanes);
       rank += w > worth || (w == worth && o < p.g);
     }
 #pragma unroll
     for (int j = 0; j < PL; ++j) {
       if (rank >= a.top_groups) c[j] = -INFINITY;
-      else if (!a.bias && c[j] > -INFINITY) c[j] = row(p.e0 + j);  // the logits order the experts
+      else if (!a.bias && c[j] > -INFINITY) c[j] = l[j];  // the logits order the experts
     }
   }
   uint32_t taken = 0;
