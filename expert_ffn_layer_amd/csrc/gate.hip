@@ -397,6 +397,50 @@ __device__ __forceinline__ Rounds take_largest(float (&v)[PL], int k) {
   return r;
 }
 
+// Of a token of sigmoids and a bias the experts that fp32 cannot tell apart from the last that was taken, by choices in 64 bits:
+// those more than `tol` above `last` stay taken, of those within tol the largest fill the k. False where that does not settle
+// it: equal choices hid the border, or more than 16 are near it. Lanes of other tokens have doubt = false.
+template <int LN, int PL, typename Row>
+__device__ __forceinline__ bool settle_border(const GateArgs& a, const Place& p, const float (&v)[PL], float last, float tol, bool doubt, int q,
+                                              int first_lane, Row row, uint32_t& taken) {
+  uint32_t near = 0, sure = taken;
+#pragma unroll
+  for (int j = 0; j < PL; ++j) near |= v[j] > -INFINITY && v[j] >= last - tol ? 1u << j : 0u;
+  for (uint32_t left = taken; doubt && left; left &= left - 1) {
+    const int e = p.e0 + __ffs((int)left) - 1;
+    const float c = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-row(e) * 1.4426950408889634f)) + a.bias[e];
+    if (c <= last + tol) {
+      near |= left & -left;
+      sure &= ~(left & -left);
+    }
+  }
+  const int counts = (int)run_sum<LN>((float)(__popc(sure) + 1024 * __popc(near)));  // at most 1024 experts of either
+  int need = a.k - counts % 1024;
+  const bool settled = doubt && need >= 0 && counts / 1024 <= 16;
+  if (!settled) need = 0;
+  near = settled ? near : 0;
+  const uint64_t token = (~0ull >> (64 - LN)) << first_lane;
+  while (__any(need > 0)) {
+    double best = -INFINITY;
+    uint32_t which = 0;
+    for (uint32_t left = need > 0 ? near : 0; left; left &= left - 1) {
+      const int e = p.e0 + __ffs((int)left) - 1;
+      const double c = sigmoid64(row(e)) + (double)a.bias[e];
+      which = c > best ? left & -left : which;
+      best = larger64(best, c);
+    }
+    const double most = reduce64(best, LN, larger64);
+    const uint64_t has = __ballot(need > 0 && best == most && which) & token;
+    if (has && __ffsll((long long)has) - 1 == first_lane + q) {
+      sure |= which;
+      near &= ~which;
+    }
+    --need;
+  }
+  if (settled) taken = sure;
+  return settled;
+}
+
 // The taken experts of a token to its list, in ascending order
 // (at most LIST of them); returns how many there are
 template <int LN, typename Row>
@@ -583,8 +627,15 @@ __global__ void __launch_bounds__(64 * WAVES) gate_kernel(const GateArgs a) {
 #pragma unroll
     for (int j = 0; j < PL; ++j) v[j] = !stays || v[j] == -INFINITY ? -INFINITY : pairs && !a.bias ? l[j] : v[j];
   }
-  const Rounds r = take_largest<LN, PL>(v, a.k);
-  if (a.bias) unsure |= r.got == a.k && r.left > -INFINITY && r.last - r.left <= tol(r.last);
+  Rounds r = take_largest<LN, PL>(v, a.k);
+  if (a.bias) {
+    const bool border = r.got == a.k && r.left > -INFINITY && r.last - r.left <= tol(r.last);
+    bool settled = false;
+    if (a.sigmoid && __any(border && !unsure))
+      settled = settle_border<LN>(a, p, v, r.last, tol(r.last), border && !unsure, q, first_lane,
+                                  [&](int e) { return tile[place(mine * a.ldl + e)]; }, r.taken);
+    unsure |= border && !settled;
+  }
   // infinite choices have no differences, and an infinite logit makes its softmax's weights NaN
   strange |= r.top == INFINITY && (!a.sigmoid || a.bias);
   Chosen* const list = lists + mine * LIST;

@@ -131,6 +131,23 @@ def test_a_border_that_32_bits_do_not_see():
     verify(logits, torch.zeros(E), k, rule("softmax", groups=4, top_groups=1, group_top=2))
 
 
+@pytest.mark.parametrize("E,k,groups,top_groups", [(64, 6, 1, 1), (256, 8, 8, 4), (300, 8, 4, 2), (768, 16, 1, 1)])
+def test_many_tokens_with_borders_that_32_bits_do_not_see(E, k, groups, top_groups):
+    """Some tokens have 2 to 24 experts within 2e-8 of each other around the last chosen, some of them equal."""
+    g = torch.Generator().manual_seed(E)
+    T = 2300
+    logits = torch.randn(T, E, generator=g)
+    bias = torch.rand(E, generator=g) * 2.0 ** -30  # keeps the order of the sigmoids below in doubt, not what is far
+    steps = torch.tensor([6.0 + i * 2.0 ** -21 for i in range(6)])
+    for t in range(0, T, 3):
+        n = int(torch.randint(2, 25, (1,), generator=g))
+        few = torch.randperm(E, generator=g)[:n + k // 2]
+        logits[t, few[:n]] = steps[torch.randint(0, 6, (n,), generator=g)]
+        logits[t, few[n:]] = 8.0 + torch.rand(len(few) - n, generator=g)
+    for b in (bias, torch.zeros(E)):
+        verify(logits, b, k, rule(groups=groups, top_groups=top_groups, group_top=2, scale=1.5))
+
+
 def test_far_logits():
     """Weights that are renormalised keep their ratios where the scores themselves vanish."""
     logits = torch.tensor([[-200.0, -201.0, -300.0, -1e30], [90.0, 91.0, 100.0, 1e30], [-90.0, 80.0, 0.0, -100.0],
