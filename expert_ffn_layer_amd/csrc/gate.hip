@@ -399,7 +399,7 @@ __device__ __forceinline__ Rounds take_largest(float (&v)[PL], int k) {
 
 // Of a token of sigmoids and a bias the experts that fp32 cannot tell apart from the last that was taken, by choices in 64 bits:
 // those more than `tol` above `last` stay taken, of those within tol the largest fill the k. False where that does not settle
-// it: equal choices hid the border, or more than 16 are near it. Lanes of other tokens have doubt = false.
+// it: equal choices hid more than k that are above, or more than 16 are near. Lanes of other tokens have doubt = false.
 template <int LN, int PL, typename Row>
 __device__ __forceinline__ bool settle_border(const GateArgs& a, const Place& p, const float (&v)[PL], float last, float tol, bool doubt, int q,
                                               int first_lane, Row row, uint32_t& taken) {
@@ -629,7 +629,9 @@ __global__ void __launch_bounds__(64 * WAVES) gate_kernel(const GateArgs a) {
   }
   Rounds r = take_largest<LN, PL>(v, a.k);
   if (a.bias) {
-    const bool border = r.got == a.k && r.left > -INFINITY && r.last - r.left <= tol(r.last);
+    // equal choices that went in one round leave more than k
+    const bool more = run_sum<LN>((float)__popc(r.taken)) > (float)r.got;
+    const bool border = r.got == a.k && (more || (r.left > -INFINITY && r.last - r.left <= tol(r.last)));
     bool settled = false;
     if (a.sigmoid && __any(border && !unsure))
       settled = settle_border<LN>(a, p, v, r.last, tol(r.last), border && !unsure, q, first_lane,
