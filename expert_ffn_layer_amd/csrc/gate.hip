@@ -602,18 +602,23 @@ __global__ void __launch_bounds__(64 * WAVES) gate_kernel(const GateArgs a) {
   // s (1 - s) times that, 0.42 2^-23 at most; a softmax's e^x likewise, with e^x |x| < 0.37, and 1 / sum 2^-23.
   auto tol = [&](float c) { return 0x1.8p-21f * top + 0x1.8p-23f * __builtin_fabsf(c); };
   bool nan = false;
+  auto scores = [&](auto score) __attribute__((always_inline)) {
 #pragma unroll
-  for (int j = 0; j < PL; ++j) {
-    float c = l[j];
-    if (scored) {
-      const float x = __builtin_amdgcn_exp2f((a.sigmoid ? -l[j] : l[j] - m) * inv_log2);
-      const float s = a.sigmoid ? __builtin_amdgcn_rcpf(1.f + x) : x * top;
-      c = s + v[j];
-      c = l[j] == -INFINITY ? -INFINITY : c;
+    for (int j = 0; j < PL; ++j) {
+      const float c = score(l[j]) + v[j];
+      v[j] = l[j] == -INFINITY ? -INFINITY : c;
     }
-    nan |= c != c;
-    v[j] = c;
+  };
+  if (!scored) {
+#pragma unroll
+    for (int j = 0; j < PL; ++j) v[j] = l[j];
+  } else if (a.sigmoid) {
+    scores([&](float x) { return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-x * inv_log2)); });
+  } else {
+    scores([&](float x) { return __builtin_amdgcn_exp2f((x - m) * inv_log2) * top; });
   }
+#pragma unroll
+  for (int j = 0; j < PL; ++j) nan |= v[j] != v[j];
   strange |= run_max<LN>(nan ? 1.f : 0.f) > 0.f;
   if (a.groups > 1) {
     float first, second;
