@@ -183,8 +183,8 @@ __device__ __forceinline__ void product_tile(const MuonArgs& a, const int b, con
   constexpr int BLOCKS = NT / 2, ALL = MT * BLOCKS;
   const float* const diagonal = FORM == MF_GRAM ? nullptr : (FORM == MF_POLY ? a.da : a.dc) + (size_t)b * a.Mp;
   // What a block's results are formed with, the elements themselves of A or X and the diagonal, or the user's parameters, is
-  // fetched AHEAD - 1 blocks before: a block takes about 1 us, a load from memory 2 to 3 while all CUs write. Where there are
-  // few tiles, all of it before the reduction.
+  // fetched AHEAD - 1 blocks before: a block takes about 1 us, a load from memory 2 to 3 while all CUs write. With tiles of
+  // 128 x 128 all of it comes before the reduction.
   constexpr bool OLD_HI = FORM == MF_POLY || (FORM == MF_STEP && !SPLIT), OLD_LO = (FORM == MF_POLY && SPLIT) || (FORM == MF_STEP && !SPLIT);
   constexpr bool OLD_P = OUT == OUT_P || OUT == OUT_MASTER, P_F32 = SPLIT || OUT == OUT_MASTER;
   constexpr int AHEAD = ALL < 3 ? ALL : 3;
@@ -224,7 +224,7 @@ __device__ __forceinline__ void product_tile(const MuonArgs& a, const int b, con
         if (whole) pw[set][it] = load8<P_F32>(params, uat + (m < rows && n < cols ? (size_t)m * cols + n : 0));
     }
   };
-  constexpr bool EARLY = D == 4 && ALL <= AHEAD;
+  constexpr bool EARLY = ALL <= AHEAD;
   if constexpr (EARLY) {
 #pragma unroll
     for (int blk = 0; blk < ALL; ++blk) fetch(blk);
@@ -652,14 +652,22 @@ hipError_t launch(const MuonArgs& a, hipStream_t st) {
 
 constexpr long long CUS = 256;
 
+// Tiles of 256 x 256 read least, one workgroup a CU; of 128 x 128, two a CU, they take a round of 256 tiles as long as 680 of
+// theirs: one X of 2048 x 5632 (176 tiles, or 704) takes 67 us either way, of 2048 x 4096 (128, 512) 58 and 48, of 2048 x 7168
+// (224, 896) 72 and 79; five of 2048 x 2048 (320, 1280) two rounds of 64, or 118. Where every 128 x 128 tile has a CU for
+// itself, Gram's matrix, whose reduction is the long side, takes a ring of four slots: three of 771 x 1000 (84 tiles)
+// 13.1 us, with two slots 15.4; one of 2048 x 7168 (136) 60 and 82. The others' operands come by halves of slots, which does
+// as much: 14.6 and 15.0.
 template <int FORM>
 hipError_t choose(const MuonArgs& a, hipStream_t st) {
   auto tiles = [&](int b) {
     const long long m = (a.Mp + b - 1) / b, n = (a.Np + b - 1) / b;
     return (FORM == MF_GRAM || FORM == MF_POLY ? m * (m + 1) / 2 : m * n) * a.count;
   };
-  if (tiles(256) >= 224) return launch<FORM, 2, 2, 4, 4, 2>(a, st);
-  return tiles(128) <= 256 ? launch<FORM, 2, 2, 2, 2, 4>(a, st) : launch<FORM, 2, 2, 2, 2, 2>(a, st);
+  if (tiles(128) >= 680 * ((tiles(256) + CUS - 1) / CUS)) return launch<FORM, 2, 2, 4, 4, 2>(a, st);
+  if constexpr (FORM == MF_GRAM)
+    if (tiles(128) <= CUS) return launch<FORM, 2, 2, 2, 2, 4>(a, st);
+  return launch<FORM, 2, 2, 2, 2, 2>(a, st);
 }
 
 }  // namespace
