@@ -6,7 +6,9 @@
 // themselves (steps) are a few products of at most 64 x 64 by one workgroup. A step multiplies what rounding adds to small
 // eigenvalues by a^2 = 12, and Q's large entries cancel on large singular values: in 64 bits both stay far below fp32.
 //
-// What bounds them is latency: three launches, and in `steps` 17 products one after the other.
+// What bounds them is latency: three launches, and in `steps` 17 products one after the other. One of 256 x 8: 10 + 13 + 6 us; in
+// `steps` a short side of up to 32 takes 13 us, of 64 64 to 70. By the products of 16-bit operands, for which the short side is
+// padded to 128, two of 24 x 1577 took 333 us, here 30.
 #include "muon.h"
 
 namespace moe {

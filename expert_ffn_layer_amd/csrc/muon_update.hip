@@ -27,7 +27,7 @@ __device__ __forceinline__ float load_g(const MuonArgs& a, const void* g, size_t
 
 // m = mu m + g', and the sum of u^2 of this workgroup's part of a matrix, u = g' + mu m (Nesterov), m or g'. Sums are
 // in 64 bits: no gradient overflows or vanishes in them. A part is always the same elements: the same bits on every run.
-// Bound by memory: 10 bytes an element with a bf16 gradient.
+// Bound by memory: 10 bytes an element with a bf16 gradient, 32 matrices of 7168 x 2048 in 917 us, 5.1 TB/s.
 __global__ void __launch_bounds__(THR) momentum_kernel(const MuonArgs a) {
   const int b = blockIdx.y, part = blockIdx.x;
   const MuonStack& s = muon_stack(a, a.first + b);
@@ -49,15 +49,31 @@ __global__ void __launch_bounds__(THR) momentum_kernel(const MuonArgs a) {
       for (int z = 0; z < 4; ++z) sum += (double)u[z] * u[z];
     }
   } else {
-    for (size_t i = from + threadIdx.x; i < to; i += THR) {
-      float u = load_g(a, s.g, base + i, gs);
-      if (s.m) {
-        const float m = a.momentum * s.m[base + i] + u;
-        s.m[base + i] = m;
-        u = a.nesterov ? u + a.momentum * m : m;
+    // eight loads of each at a time; behind the end the first of them, which does not count
+    auto all = [&](auto get) __attribute__((always_inline)) {
+      for (size_t i = from + threadIdx.x; i < to; i += 8 * THR) {
+        float u[8], m[8];
+#pragma unroll
+        for (int z = 0; z < 8; ++z) {
+          const size_t at = base + (i + z * THR < to ? i + z * THR : i);
+          u[z] = get(at);
+          if (s.m) m[z] = s.m[at];
+        }
+#pragma unroll
+        for (int z = 0; z < 8; ++z) {
+          if (i + z * THR >= to) break;
+          if (a.grad_scale) u[z] *= gs;
+          if (s.m) {
+            m[z] = a.momentum * m[z] + u[z];
+            s.m[base + i + z * THR] = m[z];
+            u[z] = a.nesterov ? u[z] + a.momentum * m[z] : m[z];
+          }
+          sum += (double)u[z] * u[z];
+        }
       }
-      sum += (double)u * u;
-    }
+    };
+    if (a.g_f32) all([&](size_t at) { return ((const float*)s.g)[at]; });
+    else all([&](size_t at) { return bf16_to_f32(((const uint16_t*)s.g)[at]); });
   }
   __shared__ double part_sum[THR / 64];
 #pragma unroll
@@ -68,46 +84,55 @@ __global__ void __launch_bounds__(THR) momentum_kernel(const MuonArgs a) {
 }
 
 // A tile of X, 64 of the short side x 64 of the long one, through LDS: the user's rows are read 16 bytes a lane, X's written so.
-// Bound by memory: 10 bytes an element with a bf16 gradient.
+// Bound by memory: 10 bytes an element with a bf16 gradient and momentum; of 32 matrices of 7168 x 2048 without, 6 bytes in
+// 0.70 ms, 4.0 TB/s (0.94 with loads that waited for the sums and for each other).
 __global__ void __launch_bounds__(THR) normalize_kernel(const MuonArgs a) {
   __shared__ float tile[64][65];
   const int b = blockIdx.z, n0 = blockIdx.x * 64, j0 = blockIdx.y * 64;
   const MuonStack& s = muon_stack(a, a.first + b);
   const size_t base = (size_t)(a.first + b - s.first) * a.M * a.N;
-  double sum = 0.0;
-  for (int i = threadIdx.x & 63; i < a.parts; i += 64) sum += a.sums[(size_t)b * a.parts + i];
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-  const double norm = sqrt(sum) + a.eps;
-  // a matrix of zeros stays one without an eps, too
-  const double f = norm == 0.0 ? 0.0 : (double)MUON_SCALE / norm;
   const float gs = a.grad_scale ? *a.grad_scale : 1.f;
   const int cols = s.wide ? a.N : a.M, rows = s.wide ? a.M : a.N, c0 = s.wide ? n0 : j0, r0 = s.wide ? j0 : n0;
   const int c = 4 * (threadIdx.x & 15);
+  // the elements, all loads before the first use; what lies outside reads the matrix's first
+  f32x4 u[4], m[4];
+  auto inside = [&](int it) { return r0 + it * 16 + (int)(threadIdx.x >> 4) < rows && c0 + c < cols; };
+  auto place = [&](int it) { return base + (inside(it) ? (size_t)(r0 + it * 16 + (threadIdx.x >> 4)) * cols + c0 + c : 0); };
+  if (cols % 4 == 0) {
+#pragma unroll
+    for (int it = 0; it < 4; ++it) u[it] = load_g4(a, s.g, place(it), gs);
+    if (s.m) {
+#pragma unroll
+      for (int it = 0; it < 4; ++it) m[it] = *(const f32x4*)(s.m + place(it));
+    }
+  } else {
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        const size_t at = place(it) + (inside(it) && c0 + c + z < cols ? z : 0);
+        u[it][z] = load_g(a, s.g, at, gs);
+        if (s.m) m[it][z] = s.m[at];
+      }
+  }
+  __shared__ double part_sum[THR / 64];
+  double sum = 0.0;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < a.parts; i += THR) sum += a.sums[(size_t)b * a.parts + i];
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+  if ((threadIdx.x & 63) == 0) part_sum[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  const double norm = sqrt(part_sum[0] + part_sum[1] + part_sum[2] + part_sum[3]) + a.eps;
+  // a matrix of zeros stays one without an eps, too
+  const double f = norm == 0.0 ? 0.0 : (double)MUON_SCALE / norm;
 #pragma unroll
   for (int it = 0; it < 4; ++it) {
     const int r = it * 16 + (threadIdx.x >> 4);
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    const size_t at = base + (size_t)(r0 + r) * cols + c0 + c;
-    if (cols % 4 == 0) {
-      if (r0 + r < rows && c0 + c < cols) {
-        f32x4 u = load_g4(a, s.g, at, gs);
-        if (s.m) {
-          const f32x4 m = *(const f32x4*)(s.m + at);
-          u = a.nesterov ? u + a.momentum * m : m;
-        }
+    f32x4 v = u[it];
+    if (s.m) v = a.nesterov ? u[it] + a.momentum * m[it] : m[it];
 #pragma unroll
-        for (int z = 0; z < 4; ++z) v[z] = (float)(u[z] * f);
-      }
-    } else if (r0 + r < rows) {
-#pragma unroll
-      for (int z = 0; z < 4; ++z)
-        if (c0 + c + z < cols) {
-          float u = load_g(a, s.g, at + z, gs);
-          if (s.m) u = a.nesterov ? u + a.momentum * s.m[at + z] : s.m[at + z];
-          v[z] = (float)(u * f);
-        }
-    }
+    for (int z = 0; z < 4; ++z) v[z] = inside(it) && c0 + c + z < cols ? (float)(v[z] * f) : 0.f;
 #pragma unroll
     for (int z = 0; z < 4; ++z) {
       if (s.wide) tile[r][c + z] = v[z];
