@@ -257,3 +257,43 @@ def test_many_tokens_and_no_tokens():
     none = torch.empty(0, E, device=DEV)
     N.moe_gate(shape(0, E, k), N.make_gate(), none, None, torch.empty(0, k, dtype=torch.int32, device=DEV), torch.empty(0, k, device=DEV))
     N.moe_gate_backward(shape(0, E, k), N.make_gate(), none, torch.empty(0, k, dtype=torch.int32, device=DEV), torch.empty(0, k, device=DEV), none.clone())
+
+
+def test_captured_gate_and_gradient():
+    """Replays follow the logits, with eager calls of other sizes between them."""
+    T, E, k = 2500, 96, 6
+    r = N.make_gate(**rule(groups=8, top_groups=3, group_top=2, scale=2.0))
+    s = shape(T, E, k)
+    logits, bias = (t.to(DEV) for t in inputs(T, E, 5))
+    dw = torch.randn(T, k, device=DEV)
+    idx, w, d = (torch.empty(n, dtype=t, device=DEV) for n, t in (((T, k), torch.int32), ((T, k), torch.float32), ((T, E), torch.float32)))
+
+    def both(l, i, w, d):
+        N.moe_gate(s, r, l, bias, i, w)
+        N.moe_gate_backward(s, r, l, i, dw, d)
+    both(logits, idx, w, d)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both(logits, idx, w, d)
+    for i in range(4):
+        logits.copy_(torch.randn(T, E, device=DEV) * 2)
+        graph.replay()
+        other = [torch.empty_like(t) for t in (idx, w, d)]
+        both(logits.clone(), *other)
+        run(*inputs(7, 40, i), 4, rule())
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip((idx, w, d), other)), "replay %d" % i
+
+
+def test_gradient_in_the_logits_memory():
+    for name in RULES:
+        T, E, k = 1000, 200, 5
+        r, s = N.make_gate(**RULES[name]), shape(T, E, k)
+        logits, b = inputs(T, E, 9)
+        idx, _ = run(logits, b, k, RULES[name])
+        l, i, dw = logits.to(DEV), idx.to(DEV), torch.randn(T, k, device=DEV)
+        d = torch.empty_like(l)
+        N.moe_gate_backward(s, r, l, i, dw, d)
+        N.moe_gate_backward(s, r, l, i, dw, l)
+        assert torch.equal(d, l), name

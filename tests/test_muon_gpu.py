@@ -256,3 +256,67 @@ def test_captured_step():
         b.run(lr=float(lr))
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(a.arrays(), b.arrays())), "replay %d" % i
+
+
+KINDS_OF_WORK = [(3, 40, 700), (2, 100, 200), (1, 300, 4000), (2, 640, 700)]  # in 64 bits, one workgroup, shared reductions, products
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_captured_orthogonalize(kind):
+    gs = [matrices(*z, kind, seed=i) for i, z in enumerate(KINDS_OF_WORK)]
+    os, ws = [torch.empty_like(g) for g in gs], [workspace(kind, *z) for z in KINDS_OF_WORK]
+
+    def all_of(os, ws):
+        for g, o, w in zip(gs, os, ws):
+            N.moe_orthogonalize(g, o, w)
+    all_of(os, ws)
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    outs = [[torch.empty_like(g) for g in gs] for _ in graphs]
+    for graph, o in zip(graphs, outs):  # two graphs that share workspaces, replayed one after the other
+        with torch.cuda.graph(graph):
+            all_of(o, ws)
+    for i in range(4):
+        for g in gs:
+            g.copy_(torch.randn(g.shape, device=DEV))
+        for graph in graphs:
+            graph.replay()
+        all_of(os, [workspace(kind, *z) for z in KINDS_OF_WORK])
+        torch.cuda.synchronize()
+        for o in outs:
+            assert all(torch.equal(x, y) for x, y in zip(o, os)), "replay %d" % i
+
+
+def test_two_calls_at_once():
+    """On two streams, with a workspace each."""
+    for z in KINDS_OF_WORK:
+        gs = [matrices(*z, "bf16", seed=i) for i in range(2)]
+        want = [orthogonalize(g, "bf16") for g in gs]
+        os, ws, streams = [torch.empty_like(g) for g in gs], [workspace("bf16", *z) for _ in gs], [torch.cuda.Stream() for _ in gs]
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for g, o, w, s in zip(gs, os, ws, streams):
+                N.moe_orthogonalize(g, o, w, stream=s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(os, want)), z
+
+
+@pytest.mark.parametrize("p,master", [("f32", False), ("bf16", True)])
+def test_step_of_every_kind_of_work(p, master):
+    """Matrices of each kernel's sizes in one step, both ways round and at lengths that are not multiples of 4 or 8."""
+    s = Step([(2, 33, 1001), (1, 1001, 33), (2, 127, 255), (1, 255, 127), (1, 129, 3001), (1, 2051, 130), (1, 515, 770)], p, master=master)
+    for lr, momentum, nesterov in ((0.02, 0.95, True), (0.1, 0.5, False)):
+        want = s.want(lr, momentum, nesterov, 0.1)
+        s.run(lr, momentum, nesterov, 0.1)
+        s.verify(want)
+
+
+def test_nothing_is_written_past_the_end():
+    for kind in ("f32", "bf16"):
+        for z in ((3, 7, 9), (2, 101, 203), (1, 301, 333), (1, 130, 2501)):
+            n = z[0] * z[1] * z[2]
+            need = N.moe_orthogonalize_workspace_size(kind, *z)
+            buf = torch.full((n + 64,), 5.0, dtype=DT[kind], device=DEV)
+            ws = torch.full((need + 4096,), 0xAB, dtype=torch.uint8, device=DEV)
+            N.moe_orthogonalize(matrices(*z, kind), buf[:n].reshape(z), ws[:need])
+            assert (buf[n:] == 5.0).all() and (ws[need:] == 0xAB).all(), (kind, z)
