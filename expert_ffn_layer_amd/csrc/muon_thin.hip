@@ -6,8 +6,9 @@
 // themselves (steps) are a few products of at most 64 x 64 by one workgroup. A step multiplies what rounding adds to small
 // eigenvalues by a^2 = 12, and Q's large entries cancel on large singular values: in 64 bits both stay far below fp32.
 //
-// What bounds them is latency: three launches, and in `steps` 17 products one after the other. One of 256 x 8: 10 + 13 + 6 us; in
-// `steps` a short side of up to 32 takes 13 us, of 64 64 to 70. By the products of 16-bit operands, for which the short side is
+// What bounds them is latency: three launches, and in `steps` 17 products one after the other. One of 256 x 8: 9 + 12 + 6 us, by
+// one workgroup in one launch 33; in `steps` a short side of up to 32 takes 12 to 13 us, of 64 61, of which the matrix
+// instructions of one CU need 31. By the products of 16-bit operands, for which the short side is
 // padded to 128, two of 24 x 1577 took 333 us, here 30.
 #include "muon.h"
 
@@ -139,10 +140,14 @@ __global__ void __launch_bounds__(MB* MB / 4) steps_kernel(const MuonArgs a, int
   for (int r = 0; r < 4; ++r) A[at(r)] = mine[r] * f * f;
   // rows of p times rows of q: all matrices here are symmetric
   auto multiply = [&](const double* p, const double* q) {
-    f64x4 acc = {0.0, 0.0, 0.0, 0.0};
+    // two sums: a product takes twice as long to end as to start
+    f64x4 even = {0.0, 0.0, 0.0, 0.0}, odd = even;
 #pragma unroll 4
-    for (int k = 0; k < MB; k += 4) acc = product(p[(ti * 16 + l16) * LQ + k + k4], q[(tj * 16 + l16) * LQ + k + k4], acc);
-    return acc;
+    for (int k = 0; k < MB; k += 8) {
+      even = product(p[(ti * 16 + l16) * LQ + k + k4], q[(tj * 16 + l16) * LQ + k + k4], even);
+      odd = product(p[(ti * 16 + l16) * LQ + k + 4 + k4], q[(tj * 16 + l16) * LQ + k + 4 + k4], odd);
+    }
+    return even + odd;
   };
   const double ca = a.a, cb = a.b, cc = a.c;
   for (int step = 0; step < steps; ++step) {
