@@ -28,7 +28,7 @@ Class class_of(int rows, int cols, long long count, bool split) {
   c.Mp = (c.M + MUON_PAD - 1) / MUON_PAD * MUON_PAD;
   c.Np = (c.N + MUON_PAD - 1) / MUON_PAD * MUON_PAD;
   c.split = split;
-  if (c.M > THIN_MAX && muon_small(c.M, c.N)) {
+  if (!muon_thin(c.M, c.N) && muon_small(c.M, c.N)) {
     c.chunk = (int)std::min<long long>(count, 65535);  // a launch's grid
     return c;
   }
@@ -38,7 +38,7 @@ Class class_of(int rows, int cols, long long count, bool split) {
     o += up(bytes);
     return at;
   };
-  if (c.M <= THIN_MAX) {
+  if (muon_thin(c.M, c.N)) {
     // within 256 MiB, and a launch's grid
     const int side = thin_side(c.M), part = thin_part(c.N);
     c.parts = (c.N + part - 1) / part;
@@ -135,7 +135,7 @@ hipError_t run_class(MuonArgs a, const Class& c, const moe_newton_schulz& ns, in
   a.C_lo = (uint16_t*)(w + c.C_lo);
   a.partial = (float*)(w + c.partial);
   hipError_t e = hipSuccess;
-  if (c.M <= THIN_MAX) {
+  if (muon_thin(c.M, c.N)) {
     a.q = (double*)(w + c.q);
     a.part = thin_part(c.N);
     for (long long first = 0; first < total && e == hipSuccess; first += c.chunk) {

@@ -66,11 +66,12 @@ enum MuonForm {
 int muon_runs(int Mp, int Np, long long count, bool split);
 hipError_t launch_muon_product(MuonForm form, const MuonArgs& a, hipStream_t st);
 
-// All of it for matrices with a short side of at most THIN_MAX; a.part = thin_part(N) and a.parts of them, a.sums
+// All of it for matrices with a short side of at most THIN_MAX that muon_thin() names; a.part = thin_part(N) and a.parts of them, a.sums
 // [count][parts][MB][MB], a.q [count][MB * MB + 1], MB the short side's 32 or 64
 constexpr int THIN_MAX = 64;
 inline int thin_side(int M) { return M <= 32 ? 32 : 64; }
 int thin_part(int N);
+bool muon_thin(int M, int N);
 hipError_t launch_muon_thin(const MuonArgs& a, int steps, hipStream_t st);
 
 // All of it for other small matrices, without a workspace

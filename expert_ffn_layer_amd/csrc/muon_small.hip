@@ -361,6 +361,7 @@ void launch(const MuonArgs& a, int steps, hipStream_t st) {
 
 }  // namespace
 
+// Of 2048 matrices, too: of 128 x 256 375 us in bf16 and 715 in fp32, by launches of products 1172 and 1956.
 bool muon_small(int M, int N) { return M <= MB && N <= 256; }
 
 hipError_t launch_muon_small(const MuonArgs& a, int steps, hipStream_t st) {

@@ -1,4 +1,4 @@
-// Orthogonalisation and Muon step of matrices whose short side is at most 64, in 64 bits (v_mfma_f64_16x16x4_f64).
+// Orthogonalisation and Muon step of matrices whose short side is at most 32, or 64 beside a long one, in 64 bits (v_mfma_f64_16x16x4_f64).
 //
 // With A_0 = X_0 X_0^T every step's polynomial is one in A_0, so the steps need X only before and after them:
 //   B_i = a I + b A_i + c A_i^2,  A_{i+1} = B_i A_i B_i,  Q = B_last ... B_0,  O = Q X_0
@@ -271,8 +271,13 @@ int thin_part(int N) {
   return (p < 4 * COLS ? 4 * COLS : (p + COLS - 1) / COLS * COLS);
 }
 
+// Short sides from 33 on with a long one of up to 256 are quicker by one workgroup a matrix and 16-bit operands, although it pads
+// them to 128: 2 of 60 x 60 take 28 us in bf16 and 48 in fp32, of 60 x 200 37 and 70, here 75 to 80, 60 of them in `steps`.
+// With a short side of up to 32 these take 28 (2 of 60 x 300: 90).
+bool muon_thin(int M, int N) { return M <= 32 || (M <= THIN_MAX && !muon_small(M, N)); }
+
 hipError_t launch_muon_thin(const MuonArgs& a, int steps, hipStream_t st) {
-  if (a.M > THIN_MAX) return hipErrorInvalidValue;
+  if (!muon_thin(a.M, a.N)) return hipErrorInvalidValue;
   if (a.M <= 32) launch<32>(a, steps, st);
   else launch<64>(a, steps, st);
   return hipGetLastError();

@@ -581,7 +581,7 @@ moe_status moe_layer_forward_gated(const moe_shape* shape, const moe_gate_rule* 
  * Precision by type: MOE_F32 forms the products of pairs of 16-bit numbers with fp32 sums (about 22 bits); MOE_BF16 those
  * of fp16 numbers with fp32 sums, X itself (but in the last step) and the diagonals of A and its polynomial wider: off by
  * about 0.0007 of its norm before it is rounded to bf16, which is 0.0017, up to 0.003 where the rank is a few. A shorter side
- * of up to 64 is worked on in 64 bits. The same bits on every run: no atomics.
+ * of up to 32 (64 where the longer exceeds 256) is worked on in 64 bits. The same bits on every run: no atomics.
  */
 typedef struct {
   int32_t steps;  /* 1..32 */

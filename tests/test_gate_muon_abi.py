@@ -208,10 +208,10 @@ def test_muon_workspace_counts_a_class_together():
         arr, b = (N.MoeMuonTensor * len(t))(*t), ctypes.c_size_t()
         assert N.load().moe_muon_workspace_size(1, arr, len(t), ctypes.byref(b)) == 0
         return b.value
-    one, both = need(tensor(rows=64, cols=128)), need(tensor(rows=64, cols=128), tensor(rows=128, cols=64))
-    assert both > one and need(tensor(rows=64, cols=128, count=4)) == both
-    assert need(tensor(rows=64, cols=128), tensor(rows=8, cols=8)) == one  # one class after the other
-    assert need(tensor(count=0)) == 0
+    one, both = need(tensor(rows=300, cols=400)), need(tensor(rows=300, cols=400), tensor(rows=400, cols=300))
+    assert both > one and need(tensor(rows=300, cols=400, count=4)) == both
+    assert need(tensor(rows=300, cols=400), tensor(rows=8, cols=8)) == one  # one class after the other
+    assert need(tensor(count=0)) == 0 and need(tensor(rows=64, cols=128)) == 0  # a workgroup each needs none
 
 
 def test_muon_binding():
