@@ -475,14 +475,23 @@ __device__ __forceinline__ void exact_token(const GateArgs& a, long long t, Row 
     l[j] = j < p.n ? row(p.e0 + j) : -INFINITY;
     b[j] = a.bias ? a.bias[j < p.n ? p.e0 + j : 0] : 0.f;
   }
+  // Without a bias and sums of two the logits are the order, also where scores are 1 or 0 in 64 bits. m is there where the
+  // exponentials are.
+  const bool scored = a.bias || (a.groups > 1 && a.group_top == 2);
+  if (scored || (!a.sigmoid && !a.renormalize)) {
 #pragma unroll
-  for (int j = 0; j < PL; ++j) {
-    c[j] = exp(a.sigmoid ? -(double)l[j] : (double)l[j] - (double)m);
-    z += c[j];
+    for (int j = 0; j < PL; ++j) {
+      c[j] = exp(a.sigmoid ? -(double)l[j] : (double)l[j] - (double)m);
+      z += c[j];
+    }
+    if (!a.sigmoid) inv = 1.0 / reduce64(z, 64, sum64);
+#pragma unroll
+    for (int j = 0; j < PL; ++j) c[j] = l[j] > -INFINITY ? (a.sigmoid ? 1.0 / (1.0 + c[j]) : c[j] * inv) + (double)b[j] : -INFINITY;
   }
-  if (!a.sigmoid) inv = 1.0 / reduce64(z, 64, sum64);
+  if (!scored) {
 #pragma unroll
-  for (int j = 0; j < PL; ++j) c[j] = l[j] > -INFINITY ? (a.sigmoid ? 1.0 / (1.0 + c[j]) : c[j] * inv) + (double)b[j] : -INFINITY;
+    for (int j = 0; j < PL; ++j) c[j] = l[j];
+  }
   if (a.groups > 1) {
     // the largest of the group, and the largest of the others: all but the first place that has it
     double here = c[0];

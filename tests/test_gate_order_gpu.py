@@ -1,0 +1,95 @@
+"""The order in which the gate takes experts, where it is hard to tell, and the rounding of its numbers, on the GPU."""
+import math
+
+import pytest
+import torch
+
+from expert_ffn_layer_amd import native as N
+
+from _gpu import say
+from _muon import F
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+INF = math.inf
+
+
+def shape(T, E, k):
+    return N.make_shape(T, 128, E, k, 128)
+
+
+def gate(logits, bias, k, rule):
+    T, E = logits.shape
+    idx = torch.full((T, k), -7, dtype=torch.int32, device=DEV)
+    w = torch.full((T, k), 99.0, device=DEV)
+    N.moe_gate(shape(T, E, k), rule, logits.to(DEV), None if bias is None else bias.to(DEV), idx, w)
+    return idx.cpu().long(), w.cpu()
+
+
+def by_logits(logits, k, groups, top_groups):
+    """[T, k] experts in ascending order, E where there are fewer: groups by their largest logit, equal ones to the lower index."""
+    T, E = logits.shape
+    order = logits.double()
+    if groups > 1:
+        worth = order.reshape(T, groups, -1).amax(2)
+        kept = worth.sort(dim=1, descending=True, stable=True).indices[:, :top_groups]
+        stays = torch.zeros(T, groups, dtype=torch.bool).scatter_(1, kept, True)
+        order = order.masked_fill(~stays.repeat_interleave(E // groups, 1), -INF)
+    top = order.sort(dim=1, descending=True, stable=True)
+    return torch.where(top.values[:, :k] > -INF, top.indices[:, :k], E).sort(1).values
+
+
+def weights(logits, idx, score, renormalize, scale):
+    """In 64 bits; a score that vanishes keeps its ratio to the others."""
+    l = logits.double()
+    here = idx < l.shape[1]
+    v = torch.where(here, l.gather(1, idx.clamp(max=l.shape[1] - 1)), -INF)
+    x = v.clamp(max=0.0) if score == "sigmoid" else v
+    most = torch.zeros(len(l), 1, dtype=torch.float64)
+    if renormalize:
+        most = x.amax(1, keepdim=True)
+    elif score == "softmax":
+        most = l.amax(1, keepdim=True)
+    most = torch.where(most > -INF, most, 0.0)
+    s = torch.exp(x - most)
+    if score == "sigmoid":
+        s = s / (1.0 + torch.exp(-v.abs()))
+    s = torch.where(here, s, 0.0)
+    if renormalize:
+        s = s / s.sum(1, keepdim=True).clamp(min=1e-300)
+    elif score == "softmax":
+        s = s / torch.exp(l - most).sum(1, keepdim=True).clamp(min=1e-300)
+    return scale * s
+
+
+LEVELS = [0.0, 40.0, 60.0, 800.0, -40.0, -790.0]
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("E,k,groups,top_groups", [(3, 1, 1, 1), (4, 2, 1, 1), (40, 8, 1, 1), (256, 8, 1, 1), (256, 8, 8, 3), (300, 5, 4, 2),
+                                                   (600, 16, 1, 1), (1024, 3, 64, 2), (60, 5, 3, 2)])
+@pytest.mark.parametrize("T", [40, 2300])
+def test_equal_logits_where_scores_saturate(T, E, k, groups, top_groups, score, renormalize):
+    """Without a bias the logits are the order, whatever becomes of the scores: 1 or 0 in any number of bits, or past the
+    exponential's range."""
+    say("equal logits", T, E, k, groups, top_groups, score, renormalize)
+    g = torch.Generator().manual_seed(E + T)
+    logits = torch.randint(0, 6, (T, E), generator=g).float() + torch.tensor(LEVELS)[torch.arange(T) % len(LEVELS)][:, None]
+    logits[::5][torch.rand(len(logits[::5]), E, generator=g) < 0.5] = -INF
+    rule = N.make_gate(score, groups, top_groups, 1, renormalize, 1.5)
+    idx, w = gate(logits, None, k, rule)
+    want = by_logits(logits, k, groups, top_groups)
+    assert torch.equal(torch.where(want < E, want, -1), idx)
+    exact = weights(logits, want, score, renormalize, 1.5)
+    assert ((w.double() - exact).abs() <= F * exact + 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("l,k,experts", [([50.0, 60, 60], 1, [1]), ([38.0, 40, 40, 39], 2, [1, 2]), ([-800.0, -790, -790], 1, [1]), ([40.0, 41, 41], 1, [1]),
+                                         ([50.0, 50, 40, 45], 3, [0, 1, 3])])
+def test_a_few_equal_logits(l, k, experts):
+    for score in ("sigmoid", "softmax"):
+        idx, _ = gate(torch.tensor([l]), None, k, N.make_gate(score))
+        assert idx.tolist() == [experts]
+    idx, w = gate(torch.tensor([[800.0, 800, 1, 2], [-800.0, -800, -801, -900]]), None, 2, N.make_gate())
+    assert idx.tolist() == [[0, 1], [0, 1]] and w.tolist() == [[0.5, 0.5]] * 2
