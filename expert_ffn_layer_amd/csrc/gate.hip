@@ -397,22 +397,43 @@ __device__ __forceinline__ Rounds take_largest(float (&v)[PL], int k) {
   return r;
 }
 
-// Of a token of sigmoids and a bias the experts that fp32 cannot tell apart from the last that was taken, by choices in 64 bits:
-// those more than `tol` above `last` stay taken, of those within tol the largest fill the k. False where that does not settle
-// it: equal choices hid more than k that are above, or more than 16 are near. Lanes of other tokens have doubt = false.
-template <int LN, int PL, typename Row>
-__device__ __forceinline__ bool settle_border(const GateArgs& a, const Place& p, const float (&v)[PL], float last, float tol, bool doubt, int q,
+// Of a token of sigmoids and a bias, of which at least k were taken, the experts that fp32 cannot tell apart from the k-th
+// largest, by choices in 64 bits: those more than tol above it stay taken, of those within tol the largest fill the k. A choice
+// is off by less than tol / 3 and fewer than k are above the k-th, so that no k experts can be above one that stays for sure.
+// False where that does not settle it: more than 16 are near. Lanes of other tokens have doubt = false.
+template <int LN, int PL, typename Row, typename Tol>
+__device__ __forceinline__ bool settle_border(const GateArgs& a, const Place& p, const float (&v)[PL], float last, Tol tol_of, bool more, bool doubt, int q,
                                               int first_lane, Row row, uint32_t& taken) {
-  uint32_t near = 0, sure = taken;
+  // choices of the taken, as they were
+  float c[PL];
 #pragma unroll
-  for (int j = 0; j < PL; ++j) near |= v[j] > -INFINITY && v[j] >= last - tol ? 1u << j : 0u;
-  for (uint32_t left = taken; doubt && left; left &= left - 1) {
-    const int e = p.e0 + __ffs((int)left) - 1;
-    const float c = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-row(e) * 1.4426950408889634f)) + a.bias[e];
-    if (c <= last + tol) {
-      near |= left & -left;
-      sure &= ~(left & -left);
-    }
+  for (int j = 0; j < PL; ++j) {
+    const int e = j < p.n ? p.e0 + j : 0;
+    const float x = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-row(e) * 1.4426950408889634f)) + a.bias[e];
+    c[j] = (taken >> j) & 1 ? x : -INFINITY;
+  }
+  // Equal ones went in one round: with more than k of them the k-th largest is above the last round's, unless these are what
+  // was equal. A round each of its levels, at most k.
+  float level = INFINITY;
+  int left = doubt && more ? a.k : 0;
+  for (int i = 0; i < a.k && __any(left > 0); ++i) {
+    float next = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < PL; ++j) next = larger(next, c[j] < level ? c[j] : -INFINITY);
+    level = run_max<LN>(next);
+    int equal = 0;
+#pragma unroll
+    for (int j = 0; j < PL; ++j) equal += c[j] == level;
+    if (left > 0) last = level;
+    left -= (int)run_sum<LN>((float)equal);
+  }
+  const float tol = tol_of(last);
+  uint32_t near = 0, sure = 0;
+#pragma unroll
+  for (int j = 0; j < PL; ++j) {
+    const float x = larger(c[j], v[j]);  // v is -inf where taken
+    near |= x > -INFINITY && x >= last - tol && x <= last + tol ? 1u << j : 0u;
+    sure |= x > last + tol ? 1u << j : 0u;
   }
   const int counts = (int)run_sum<LN>((float)(__popc(sure) + 1024 * __popc(near)));  // at most 1024 experts of either
   int need = a.k - counts % 1024;
@@ -642,18 +663,18 @@ __global__ void __launch_bounds__(64 * WAVES) gate_kernel(const GateArgs a) {
     for (int j = 0; j < PL; ++j) v[j] = !stays || v[j] == -INFINITY ? -INFINITY : pairs && !a.bias ? l[j] : v[j];
   }
   Rounds r = take_largest<LN, PL>(v, a.k);
+  // infinite choices have no differences, and an infinite logit makes its softmax's weights NaN
+  strange |= r.top == INFINITY && (!a.sigmoid || a.bias);
   if (a.bias) {
     // equal choices that went in one round leave more than k
     const bool more = run_sum<LN>((float)__popc(r.taken)) > (float)r.got;
     const bool border = r.got == a.k && (more || (r.left > -INFINITY && r.last - r.left <= tol(r.last)));
+    const bool doubt = border && !unsure && !strange;
     bool settled = false;
-    if (a.sigmoid && __any(border && !unsure))
-      settled = settle_border<LN>(a, p, v, r.last, tol(r.last), border && !unsure, q, first_lane,
-                                  [&](int e) { return tile[place(mine * a.ldl + e)]; }, r.taken);
+    if (a.sigmoid && __any(doubt))
+      settled = settle_border<LN>(a, p, v, r.last, tol, more, doubt, q, first_lane, [&](int e) { return tile[place(mine * a.ldl + e)]; }, r.taken);
     unsure |= border && !settled;
   }
-  // infinite choices have no differences, and an infinite logit makes its softmax's weights NaN
-  strange |= r.top == INFINITY && (!a.sigmoid || a.bias);
   Chosen* const list = lists + mine * LIST;
   unsure |= write_list<LN>(r.taken, q, p.e0, [&](int e) { return tile[place(mine * a.ldl + e)]; }, list) > r.got;
   write_weights<LN>(a, list, r.got, t0 + mine, q, on && !unsure && !strange, m, inv);

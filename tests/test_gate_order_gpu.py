@@ -93,3 +93,43 @@ def test_a_few_equal_logits(l, k, experts):
         assert idx.tolist() == [experts]
     idx, w = gate(torch.tensor([[800.0, 800, 1, 2], [-800.0, -800, -801, -900]]), None, 2, N.make_gate())
     assert idx.tolist() == [[0, 1], [0, 1]] and w.tolist() == [[0.5, 0.5]] * 2
+
+
+def by_choices(logits, bias, k):
+    """[T, k] experts in ascending order by sigmoid and bias in 64 bits, equal ones to the lower index."""
+    c = 1.0 / (1.0 + torch.exp(-logits.double())) + bias.double()
+    return c.sort(dim=1, descending=True, stable=True).indices[:, :k].sort(1).values
+
+
+@pytest.mark.parametrize("T", [500, 2300])
+@pytest.mark.parametrize("E,k", [(24, 3), (64, 6), (256, 8), (300, 16), (768, 6)])
+def test_borders_among_equal_choices(T, E, k):
+    """Choices spread over one to four times what fp32 tells apart, so that some are equal in fp32, above the border, on it and
+    below, while others end just outside of what is looked at again."""
+    say("borders", T, E, k)
+    g = torch.Generator().manual_seed(E + T)
+    bias = torch.randn(E, generator=g) * 0.2
+    logits = torch.randn(T, E, generator=g) - 4.0
+    for t in range(T):
+        n = int(torch.randint(2, min(E, 25), (1,), generator=g))
+        few = torch.randperm(E, generator=g)[:n + k // 3]
+        width = 2.0 ** -float(torch.randint(19, 25, (1,), generator=g))
+        want = 0.6 + width * torch.rand(len(few), generator=g, dtype=torch.float64)
+        want[n:] += 0.1
+        s = (want - bias[few].double()).clamp(0.01, 0.99)
+        logits[t, few] = torch.log(s / (1.0 - s)).float()
+    want = by_choices(logits, bias, k)
+    idx, _ = gate(logits, bias, k, N.make_gate("sigmoid"))
+    bad = (idx != want).any(1).nonzero().flatten().tolist()
+    assert not bad, "%d tokens, the first %d: %s, not %s" % (len(bad), bad[0], idx[bad[0]].tolist(), want[bad[0]].tolist())
+
+
+def test_a_border_two_equal_choices_deep():
+    """The three equal choices went in one round, so that the border looked for lay below the fourth."""
+    logits = torch.tensor([[0.0, 0.0, 0.0, 1.5563236, -30.0, -3.0]])
+    bias = torch.tensor([-0.4, -0.4, -0.4, -0.7258252, 0.09999926, -1.0])
+    want = by_choices(logits, bias, 3)
+    assert want.tolist() == [[0, 1, 3]]
+    for T in (1, 2500):
+        idx, _ = gate(logits.expand(T, -1).contiguous(), bias, 3, N.make_gate("sigmoid"))
+        assert (idx == want).all()
