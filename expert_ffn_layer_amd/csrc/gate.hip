@@ -656,8 +656,11 @@ __global__ void __launch_bounds__(64 * WAVES) gate_kernel(const GateArgs a) {
     const float worth = pairs && second > -INFINITY ? first + second : first;
     const bool stays = group_stays<LN>(a, p, worth, first_lane);
     if (scored) {
-      const float low = run_min<LN>(stays ? worth : INFINITY), high = run_max<LN>(stays ? -INFINITY : worth);
-      unsure |= high > -INFINITY && low - high <= 2.f * tol(low);
+      // A sum of two is off by what both are, however much of them cancels, and by its own rounding: less than 2/3 of this.
+      // Where no difference can be formed the order is open, too.
+      const float off = pairs && second > -INFINITY ? 0x1.8p-21f * top + 0x1.8p-23f * (__builtin_fabsf(first) + __builtin_fabsf(second)) : tol(first);
+      const float low = run_min<LN>(stays && worth > -INFINITY ? worth - off : INFINITY), high = run_max<LN>(stays || worth == -INFINITY ? -INFINITY : worth + off);
+      unsure |= high > -INFINITY && !(low > high);
     }
 #pragma unroll
     for (int j = 0; j < PL; ++j) v[j] = !stays || v[j] == -INFINITY ? -INFINITY : pairs && !a.bias ? l[j] : v[j];

@@ -133,3 +133,32 @@ def test_a_border_two_equal_choices_deep():
     for T in (1, 2500):
         idx, _ = gate(logits.expand(T, -1).contiguous(), bias, 3, N.make_gate("sigmoid"))
         assert (idx == want).all()
+
+
+def by_groups(scores, bias, k, groups, top_groups):
+    """The definition with sums of two in 64 bits, for groups of at least two that may all be chosen."""
+    c = scores.double() + bias.double()
+    worth = c.reshape(len(c), groups, -1).topk(2, dim=2).values.sum(2)
+    kept = worth.sort(dim=1, descending=True, stable=True).indices[:, :top_groups]
+    stays = torch.zeros(len(c), groups, dtype=torch.bool).scatter_(1, kept, True).repeat_interleave(c.shape[1] // groups, 1)
+    return c.masked_fill(~stays, -INF).sort(dim=1, descending=True, stable=True).indices[:, :k].sort(1).values
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("size", [10.0, 100.0, 1000.0, 2e38])
+@pytest.mark.parametrize("E,groups,top_groups,k", [(64, 8, 3, 5), (256, 8, 4, 8), (24, 2, 1, 3), (1024, 16, 7, 6), (120, 4, 2, 4)])
+@pytest.mark.parametrize("T", [300, 2300])
+def test_group_values_that_cancel(T, E, groups, top_groups, k, size, score):
+    """Biases of one size and both signs in each group: its value is the small rest of two large numbers."""
+    say("groups that cancel", T, E, groups, top_groups, k, size, score)
+    g = torch.Generator().manual_seed(E)
+    n = E // groups
+    bias = torch.full((E,), -size)
+    bias[torch.arange(groups) * n + torch.randint(0, n, (groups,), generator=g)] = size
+    logits = torch.randn(T, E, generator=g) * 10.0 ** -torch.randint(0, 5, (T, 1), generator=g).float()
+    logits = logits + torch.randn(T, 1, generator=g)
+    s = torch.sigmoid(logits.double()) if score == "sigmoid" else torch.softmax(logits.double(), 1)
+    want = by_groups(s, bias, k, groups, top_groups)
+    idx, _ = gate(logits, bias, k, N.make_gate(score, groups, top_groups, 2))
+    bad = (idx != want).any(1).nonzero().flatten().tolist()
+    assert not bad, "%d tokens, the first %d: %s, not %s" % (len(bad), bad[0], idx[bad[0]].tolist(), want[bad[0]].tolist())
