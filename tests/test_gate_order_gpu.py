@@ -162,3 +162,26 @@ def test_group_values_that_cancel(T, E, groups, top_groups, k, size, score):
     idx, _ = gate(logits, bias, k, N.make_gate(score, groups, top_groups, 2))
     bad = (idx != want).any(1).nonzero().flatten().tolist()
     assert not bad, "%d tokens, the first %d: %s, not %s" % (len(bad), bad[0], idx[bad[0]].tolist(), want[bad[0]].tolist())
+
+
+# Of a number formed in 64 bits by some ten operations, 2^-52 each at most and 2^-48 in all, and rounded once: half a step, and
+# where it moves across the middle of one as much more.
+ONE_ROUNDING, SMALLEST = 2.0 ** -24 + 2.0 ** -44, 0.51 * 2.0 ** -149
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (9, 63, 5), (300, 256, 8), (5000, 40, 4), (3000, 256, 8), (2500, 500, 16), (2500, 1000, 3)])
+@pytest.mark.parametrize("size", [2.0, 30.0, 400.0])
+def test_weights_are_rounded_once(T, E, k, score, renormalize, size):
+    say("weights", T, E, k, score, renormalize, size)
+    g = torch.Generator().manual_seed(E + k)
+    logits = torch.randn(T, E, generator=g) * size
+    logits[::3] -= 2 * size  # scores that vanish
+    logits[::4][torch.rand(len(logits[::4]), E, generator=g) < 0.3] = -INF
+    rule = N.make_gate(score, renormalize=renormalize, scale=1.7)
+    for bias in (None, torch.randn(E, generator=g) * 0.1):
+        idx, w = gate(logits, bias, k, rule)
+        want = weights(logits, torch.where(idx >= 0, idx, E), score, renormalize, 1.7)
+        off = (w.double() - want).abs() - ONE_ROUNDING * want - SMALLEST
+        assert (off <= 0).all(), "%d, one %s" % ((off > 0).sum(), (w[off > 0][0].item(), want[off > 0][0].item()))
