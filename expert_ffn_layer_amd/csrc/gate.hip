@@ -134,17 +134,24 @@ struct Chosen {
   float l;
 };
 
-// e^(a - b); the rounding of the difference is made up for, so that the result is off by 2^-23 of itself or little more
-__device__ __forceinline__ float exp_diff(float a, float b) {
-  const float d = a - b, z = d - a, rest = (a - (d - z)) - (b + z);
-  const float e = expf(d);
-  return d == d && rest == rest ? __builtin_fmaf(e, rest, e) : e;
+// A chosen expert's score of logit v, or its ratio to e^most: e^x / (1 + e^-|v|) for a sigmoid with x = min(v, 0), e^v for a
+// softmax; rest: 1 - s for a sigmoid, else 1. In 64 bits a sigmoid needs no most but where all are below e^-600.
+struct Score {
+  double s, rest;
+};
+__device__ __forceinline__ float most_of(bool sigmoid, float top) { return top == -INFINITY || (sigmoid && top > -600.f) ? 0.f : top; }
+__device__ __forceinline__ Score score_of(bool sigmoid, float v, float most) {
+  const double e = exp(sigmoid ? -(double)__builtin_fabsf(v) : (double)v - (double)most);
+  if (!sigmoid) return Score{e, 1.0};
+  const double f = 1.0 / (1.0 + e);
+  double s = v > 0.f ? 1.0 : e;
+  if (__any(most != 0.f)) s = exp((double)(v > 0.f ? 0.f : v) - (double)most);
+  return Score{s * f, (v > 0.f ? e : 1.0) * f};
 }
 
 // Weights of one token by the LN lanes q = 0.. that belong to it: list holds its n chosen in ascending order. m, inv: a
-// softmax's largest logit and 1 / sum (NaN for one of NaN or infinity).
-//   e^x / (1 + e^-|l|) for a sigmoid with x = min(l, 0), e^(l - m) for a softmax; where weights are renormalised only the ratio
-//   to the sum is taken, with the largest exponent as 0 in a softmax, and for sigmoids that 64 bits would lose
+// softmax's largest logit and 1 / sum (NaN for one of NaN or infinity). Where weights are renormalised only the ratio to the
+// sum is taken, so that scores that vanish keep their ratios.
 // In 64 bits, rounded once: of 16384 tokens with 8 of 256 experts 15.7 us as called, in fp32 with about ten roundings 15.3.
 template <int LN>
 __device__ __forceinline__ void write_weights(const GateArgs& a, const Chosen* list, int n, long long t, int q, bool on, float m, double inv) {
@@ -161,20 +168,13 @@ __device__ __forceinline__ void write_weights(const GateArgs& a, const Chosen* l
   float most = a.sigmoid ? 0.f : m;
   if (a.renormalize) {
     top = reduce<LN>(top, nan_max);
-    most = top == -INFINITY || (a.sigmoid && top > -600.f) ? 0.f : top;
+    most = most_of(a.sigmoid, top);
   }
-  const bool far = a.sigmoid && __any(most != 0.f);
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const float v = mine[i].l;
-    const double e = exp(a.sigmoid ? -(double)__builtin_fabsf(v) : (double)v - (double)most);
-    s[i] = e;
-    if (a.sigmoid) {
-      s[i] = v > 0.f ? 1.0 : e;
-      if (far) s[i] = exp((double)(v > 0.f ? 0.f : v) - (double)most);
-      s[i] /= 1.0 + e;
-    }
-    s[i] = v == -INFINITY ? 0.0 : s[i];
+    const double score = score_of(a.sigmoid, v, most).s;
+    s[i] = v == -INFINITY ? 0.0 : score;
     sum += s[i];
   }
   const double factor = a.scale * (a.renormalize ? (inv != inv ? inv : 1.0 / reduce64(sum, LN, sum64)) : inv);
@@ -309,7 +309,7 @@ __device__ __forceinline__ void stage(const GateArgs& a, long long t0, int token
 }
 
 __host__ __device__ __forceinline__ int backward_wave_bytes(const GateArgs& a) {
-  return (64 / LIST * a.E + 3) / 4 * 16 + 64 * (int)sizeof(Chosen);
+  return (64 / LIST * a.E + 3) / 4 * 16 + 64 * 16;  // rows, and an Entry a lane
 }
 
 __global__ void __launch_bounds__(64 * WAVES) gate_exact_kernel(const GateArgs a) {
@@ -713,12 +713,13 @@ __global__ void __launch_bounds__(64 * WAVES) gate_kernel(const GateArgs a) {
 // The gradient, for r_j = s_j / (sum of the chosen s):
 //   sigmoid, renormalised  dl_j = scale r_j (1 - s_j) (dw_j - sum_i r_i dw_i)    else  scale s_j (1 - s_j) dw_j
 //   softmax, renormalised  dl_j = scale r_j (dw_j - sum_i r_i dw_i)              else  scale p_e ([e chosen] dw_e - sum_i p_i dw_i)
-// 0 elsewhere in the first three, which read the chosen logits only and are bound by writing zeros.
+// 0 elsewhere in the first three, which read the chosen logits only and are bound by writing zeros. Formed in 64 bits and
+// rounded once.
 
 // An entry of a token: its expert (negative: it takes no part) and gradient
 struct Entry {
+  double d;
   int e;
-  float d;
 };
 
 // The forms with zeros: 16 lanes a token. Rows are put together in LDS and written 16 bytes a lane.
@@ -732,47 +733,43 @@ __global__ void __launch_bounds__(64 * WAVES) gate_backward_kernel(const GateArg
   float* const tile = (float*)(lds + (size_t)wave * backward_wave_bytes(a));
   Entry* const list = (Entry*)(tile + (TOKENS * E + 3) / 4 * 4) + mine * LIST;
   int e = -1;
-  float dw = 0.f, l = -INFINITY;
+  float g = 0.f, l = -INFINITY;
   if (t < a.T && q < k) {
     e = a.chosen[t * k + q];
-    dw = a.dw[t * k + q];
+    g = a.dw[t * k + q];
   }
   for (int i = 4 * lane; i < TOKENS * E; i += 256) *(f32x4*)(tile + i) = f32x4{0.f, 0.f, 0.f, 0.f};
   if (e >= 0 && e < E) l = a.logits[t * E + e];
   const bool here = l != -INFINITY;  // takes part
-  dw = here ? dw : 0.f;
-  // r, and 1 - s for a sigmoid, both to a few roundings however far the logit is
+  const double dw = here ? (double)g : 0.0;
+  // r, and 1 - s for a sigmoid, however far the logit is
   const float x = a.sigmoid && l > 0.f ? 0.f : l;
   float most = 0.f;
   if (a.renormalize) {
     const float top = reduce<LN>(here ? x : -INFINITY, nan_max);
-    most = top == -INFINITY ? 0.f : top;
+    most = most_of(a.sigmoid, top);
   }
-  float r = here ? exp_diff(x, most) : 0.f, rest = 1.f;
-  if (a.sigmoid && here) {
-    const float small = expf(-__builtin_fabsf(l)), f = 1.f / (1.f + small);
-    r *= f;
-    rest = (l > 0.f ? small : 1.f) * f;
-  }
-  float d = dw;
+  const Score score = score_of(a.sigmoid, l, most);
+  double r = here ? score.s : 0.0;
+  const double rest = score.rest;
+  double d = dw;
   if (a.renormalize) {
-    r *= 1.f / run_sum<LN>(r);
-    r = here ? r : 0.f;
-    // dw less its mean: products and sum in 64 bits, since the two may nearly be the same
-    d = (float)((double)dw - reduce64((double)r * dw, LN, sum64));
+    r *= 1.0 / reduce64(r, LN, sum64);
+    r = here ? r : 0.0;
+    d = dw - reduce64(r * dw, LN, sum64);
   }
-  d = here ? (float)a.scale * r * rest * d : 0.f;
-  list[q] = Entry{here ? e : -1 - q, d};
+  d = here ? a.scale * r * rest * d : 0.0;
+  list[q] = Entry{d, here ? e : -1 - q};
   in_order();
   if (here) {
-    float sum = 0.f;
+    double sum = 0.0;
     bool first = true;
     for (int i = 0; i < k; ++i) {
       const Entry o = list[i];
-      sum += o.e == e ? o.d : 0.f;
+      sum += o.e == e ? o.d : 0.0;
       first = first && (o.e != e || i >= q);
     }
-    if (first) tile[mine * E + e] = sum;
+    if (first) tile[mine * E + e] = (float)sum;
   }
   in_order();
   float* const to = a.dlogits + t0 * E;
@@ -792,7 +789,8 @@ __global__ void __launch_bounds__(64 * WAVES) gate_backward_dense_kernel(const G
   if (t >= a.T) return;  // no barrier below: a wave works alone
   const float* const row = a.logits + t * E;
   int e = -1;
-  float dw = 0.f, l[PL], p[PL], top = -INFINITY;
+  float dw = 0.f, l[PL], top = -INFINITY;
+  double p[PL];
   if (lane < k) {
     e = a.chosen[t * k + lane];
     dw = a.dw[t * k + lane];
@@ -806,23 +804,23 @@ __global__ void __launch_bounds__(64 * WAVES) gate_backward_dense_kernel(const G
   const bool here = at != -INFINITY;
   top = reduce<64>(top, nan_max);
   const float m = top == -INFINITY ? 0.f : top;
-  float z = 0.f;
+  double z = 0.0;
 #pragma unroll
   for (int j = 0; j < PL; ++j) {
-    p[j] = l[j] == -INFINITY ? 0.f : exp_diff(l[j], m);
+    p[j] = l[j] == -INFINITY ? 0.0 : exp((double)l[j] - (double)m);
     z += p[j];
   }
-  const float inv = 1.f / run_sum<64>(z);
-  const double mean = reduce64(here ? (double)dw * exp_diff(at, m) * inv : 0.0, 64, sum64);
+  const double inv = 1.0 / reduce64(z, 64, sum64);
+  const double mean = reduce64(here ? (double)dw * exp((double)at - (double)m) * inv : 0.0, 64, sum64);
   Entry* const list = lists[wave];
-  if (lane < LIST) list[lane] = Entry{here ? e : -1, dw};
+  if (lane < LIST) list[lane] = Entry{(double)dw, here ? e : -1};
   in_order();
 #pragma unroll
   for (int j = 0; j < PL; ++j) {
     const int i = lane + 64 * j;
-    float sum = 0.f;
-    for (int o = 0; o < k; ++o) sum += list[o].e == i ? list[o].d : 0.f;
-    if (i < E) a.dlogits[t * E + i] = l[j] == -INFINITY ? 0.f : (float)a.scale * (p[j] * inv) * (float)((double)sum - mean);
+    double sum = 0.0;
+    for (int o = 0; o < k; ++o) sum += list[o].e == i ? list[o].d : 0.0;
+    if (i < E) a.dlogits[t * E + i] = l[j] == -INFINITY ? 0.f : (float)(a.scale * (p[j] * inv) * (sum - mean));
   }
 }
 
@@ -863,7 +861,7 @@ hipError_t launch_gate_backward(const GateArgs& args, hipStream_t st) {
   if (a.T == 0) return hipSuccess;
   a.whole = a.E % 4 == 0 && (uintptr_t)a.dlogits % 16 == 0;
   if (a.sigmoid || a.renormalize) {
-    const int waves = a.E <= 512 ? WAVES : WAVES / 2, tokens = 64 / LIST * waves;  // at most 34 KiB of LDS
+    const int waves = a.E <= 512 ? WAVES : WAVES / 2, tokens = 64 / LIST * waves;  // at most 36 KiB of LDS
     gate_backward_kernel<<<dim3((unsigned)((a.T + tokens - 1) / tokens)), dim3(64 * waves), waves * backward_wave_bytes(a), st>>>(a);
     return hipGetLastError();
   }

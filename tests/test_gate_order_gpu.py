@@ -185,3 +185,41 @@ def test_weights_are_rounded_once(T, E, k, score, renormalize, size):
         want = weights(logits, torch.where(idx >= 0, idx, E), score, renormalize, 1.7)
         off = (w.double() - want).abs() - ONE_ROUNDING * want - SMALLEST
         assert (off <= 0).all(), "%d, one %s" % ((off > 0).sum(), (w[off > 0][0].item(), want[off > 0][0].item()))
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (9, 63, 5), (300, 256, 8), (3000, 257, 8), (2500, 600, 16), (50, 1000, 3)])
+@pytest.mark.parametrize("size", [2.0, 30.0, 300.0])
+def test_gradients_are_rounded_once(T, E, k, score, renormalize, size):
+    """An expert may be there twice; entries of experts that are off or out of range take no part."""
+    say("gradients", T, E, k, score, renormalize, size)
+    g = torch.Generator().manual_seed(E + k)
+    logits = torch.randn(T, E, generator=g) * size
+    logits[::3] -= 2 * size
+    logits[::4][torch.rand(len(logits[::4]), E, generator=g) < 0.3] = -INF
+    idx = torch.randint(-1, E + 1, (T, k), generator=g, dtype=torch.int32)
+    dw = torch.randn(T, k, generator=g)
+    got = torch.full((T, E), 77.0, device=DEV)
+    N.moe_gate_backward(shape(T, E, k), N.make_gate(score, renormalize=renormalize, scale=1.7), logits.to(DEV), idx.to(DEV), dw.to(DEV), got)
+    l, e = logits.double(), idx.long().clamp(0, E - 1)
+    v = l.gather(1, e)
+    here = (idx >= 0) & (idx < E) & (v > -INF)
+    d = torch.where(here, dw.double(), 0.0)
+    at = torch.where(here, e, E)
+    w = weights(logits, at, score, renormalize, 1.0)  # r, or the scores
+    sums = lambda t: torch.zeros(T, E + 1, dtype=torch.float64).scatter_add_(1, at, t)[:, :E]  # noqa: E731
+    if renormalize or score == "softmax":
+        mean, most = (w * d).sum(1, keepdim=True), (w * d.abs()).sum(1, keepdim=True)
+    else:
+        mean = most = torch.zeros(T, 1, dtype=torch.float64)
+    if score == "softmax" and not renormalize:
+        s = weights(logits, torch.arange(E).expand(T, E), score, False, 1.0)
+        s = torch.where(l > -INF, s, 0.0)
+        want, added = 1.7 * s * (sums(d) - mean), 1.7 * s * (sums(d.abs()) + most)
+    else:
+        f = 1.7 * torch.where(here, w * (torch.sigmoid(-v) if score == "sigmoid" else 1.0), 0.0)
+        want, added = sums(f * (d - mean)), sums(f * (d.abs() + most))
+    # of what is added and may cancel 2^-44 as well
+    off = (got.cpu().double() - want).abs() - ONE_ROUNDING * want.abs() - 2.0 ** -44 * added - SMALLEST
+    assert (off <= 0).all(), "%d, one %s" % ((off > 0).sum(), (got.cpu()[off > 0][0].item(), want[off > 0][0].item()))
