@@ -17,8 +17,9 @@ size_t up(size_t x) { return (x + WS_ALIGN - 1) / WS_ALIGN * WS_ALIGN; }
 // Matrices of one size class, and what the workspace holds of a chunk of them
 struct Class {
   int M, N, Mp, Np, chunk, parts;
+  int kept;  // thin matrices: those that there is room for in xs
   bool split;
-  size_t sums, q, x, x_lo, xo, xo_lo, A, A_lo, C, C_lo, da, dc, partial, total;
+  size_t sums, q, xs, x, x_lo, xo, xo_lo, A, A_lo, C, C_lo, da, dc, partial, total;
 };
 
 Class class_of(int rows, int cols, long long count, bool split) {
@@ -46,6 +47,10 @@ Class class_of(int rows, int cols, long long count, bool split) {
     c.chunk = (int)std::min<long long>(std::min<long long>(std::max<long long>((long long)((256ull << 20) / each), 1), 65535), count);
     c.sums = take(c.chunk * c.parts * square);
     c.q = take(c.chunk * (square + 8));
+    // X between runs of steps, which few calls have: within 256 MiB of its own, whatever the chunk
+    const size_t x = (size_t)c.M * c.N * 8;
+    c.kept = (int)std::min<long long>(std::max<long long>((long long)((256ull << 20) / x), 1), c.chunk);
+    c.xs = take(c.kept * x);
     c.total = o;
     return c;
   }
@@ -84,33 +89,56 @@ moe_status check_sizes(int32_t count, int32_t rows, int32_t cols) {
   return MOE_OK;
 }
 
-// The steps keep X, A and C within fp16 at MUON_SCALE: 15.99. From singular values up to 1; a step's rounding is
-// far below the 2% that each is given.
+// What a step makes of singular values up to `top`: the largest, and the polynomial's largest value
+struct StepRange {
+  double most, poly;
+};
+StepRange step_range(const moe_newton_schulz& ns, double top) {
+  const double a = ns.a, b = ns.b, c = ns.c, t1 = top * top;
+  auto f = [&](double t) { return t >= 0.0 && t <= t1 ? fabs(sqrt(t) * (a + t * (b + t * c))) : 0.0; };
+  auto g = [&](double t) { return t >= 0.0 && t <= t1 ? fabs(a + t * (b + t * c)) : 0.0; };
+  StepRange r{f(t1), std::max(std::max(g(0.0), g(t1)), c != 0.0 ? g(-b / (2.0 * c)) : 0.0)};
+  // where d/ds (a s + b s^3 + c s^5) = a + 3 b t + 5 c t^2 is 0
+  const double d = 9.0 * b * b - 20.0 * a * c;
+  if (c != 0.0 && d >= 0.0) {
+    r.most = std::max(r.most, std::max(f((-3.0 * b + sqrt(d)) / (10.0 * c)), f((-3.0 * b - sqrt(d)) / (10.0 * c))));
+  } else if (c == 0.0 && b != 0.0) {
+    r.most = std::max(r.most, f(-a / (3.0 * b)));
+  }
+  return r;
+}
+// The bound on the next step's singular values: a step's rounding is far below the 2% that each is given.
+double next_top(const StepRange& r) { return std::max(r.most * 1.02, 1e-3); }
+
+// The steps keep X, A and C within fp16 at MUON_SCALE: 15.99. From singular values up to 1.
 moe_status check_ns(const moe_newton_schulz* ns) {
   if (!ns) return fail(MOE_ERR_INVALID_ARG, "Newton-Schulz parameters are NULL");
   if (ns->steps < 1 || ns->steps > 32) return fail(MOE_ERR_INVALID_ARG, "steps=%d outside 1..32", ns->steps);
   if (!isfinite(ns->a) || !isfinite(ns->b) || !isfinite(ns->c)) return fail(MOE_ERR_INVALID_ARG, "coefficients must be finite");
   if (!(ns->eps >= 0.0) || !isfinite(ns->eps)) return fail(MOE_ERR_INVALID_ARG, "eps=%g must be finite and not negative", ns->eps);
-  const double a = ns->a, b = ns->b, c = ns->c;
   double top = 1.0;
   for (int i = 0; i < ns->steps; ++i) {
-    const double t1 = top * top;
-    auto f = [&](double t) { return t >= 0.0 && t <= t1 ? fabs(sqrt(t) * (a + t * (b + t * c))) : 0.0; };
-    auto g = [&](double t) { return t >= 0.0 && t <= t1 ? fabs(a + t * (b + t * c)) : 0.0; };
-    double most = f(t1), poly = std::max(std::max(g(0.0), g(t1)), c != 0.0 ? g(-b / (2.0 * c)) : 0.0);
-    // where d/ds (a s + b s^3 + c s^5) = a + 3 b t + 5 c t^2 is 0
-    const double d = 9.0 * b * b - 20.0 * a * c;
-    if (c != 0.0 && d >= 0.0) {
-      most = std::max(most, std::max(f((-3.0 * b + sqrt(d)) / (10.0 * c)), f((-3.0 * b - sqrt(d)) / (10.0 * c))));
-    } else if (c == 0.0 && b != 0.0) {
-      most = std::max(most, f(-a / (3.0 * b)));
-    }
-    if (!(poly <= 14.0) || !(most * 1.02 <= 3.7))
+    const StepRange r = step_range(*ns, top);
+    if (!(r.poly <= 14.0) || !(r.most * 1.02 <= 3.7))
       return fail(MOE_ERR_UNSUPPORTED, "coefficients %g, %g, %g take a singular value to %g and the polynomial to %g in step %d: "
-                  "3.7 and 14 are the most", a, b, c, most, poly, i + 1);
-    top = std::max(most * 1.02, 1e-3);
+                  "3.7 and 14 are the most", ns->a, ns->b, ns->c, r.most, r.poly, i + 1);
+    top = next_top(r);
   }
   return MOE_OK;
+}
+
+// Equal runs of steps that thin matrices take, each short enough that an eigenvalue's rounding, 2^-53, grows by 2^29 at most:
+// in a step by the derivative of t (a + b t + c t^2)^2 = (a + b t + c t^2) (a + 3 b t + 5 c t^2), here at 65 points of the range.
+int thin_runs(const moe_newton_schulz& ns) {
+  double top = 1.0, widest = 1.0, growth = 1.0;
+  for (int i = 1; i < ns.steps; ++i) widest = std::max(widest, top = next_top(step_range(ns, top)));
+  for (int i = 0; i <= 64; ++i) {
+    const double t = widest * widest * i / 64;
+    growth = std::max(growth, fabs((ns.a + t * (ns.b + t * ns.c)) * (ns.a + t * (3.0 * ns.b + t * 5.0 * ns.c))));
+  }
+  int most = 1;
+  for (double all = growth * growth; most < ns.steps && all <= 0x1p29; all *= growth) ++most;
+  return (ns.steps + most - 1) / most;
 }
 
 // All steps of the matrices of one class, `total` of them in the stacks of a, the first `wide` with their short side first.
@@ -138,10 +166,12 @@ hipError_t run_class(MuonArgs a, const Class& c, const moe_newton_schulz& ns, in
   if (muon_thin(c.M, c.N)) {
     a.q = (double*)(w + c.q);
     a.part = thin_part(c.N);
-    for (long long first = 0; first < total && e == hipSuccess; first += c.chunk) {
+    const int runs = thin_runs(ns), chunk = runs > 1 ? c.kept : c.chunk;
+    a.xs = (double*)(w + c.xs);
+    for (long long first = 0; first < total && e == hipSuccess; first += chunk) {
       a.first = (int)first;
-      a.count = (int)std::min<long long>(c.chunk, total - first);
-      e = launch_muon_thin(a, ns.steps, st);
+      a.count = (int)std::min<long long>(chunk, total - first);
+      e = launch_muon_thin(a, ns.steps, runs, st);
     }
     return e;
   }

@@ -48,6 +48,7 @@ struct MuonArgs {
   uint16_t *xo, *xo_lo;    // out; xo_lo may be x_lo without split, or NULL
   uint16_t *A, *A_lo, *C, *C_lo;
   double* q;               // thin matrices
+  double* xs;              // thin matrices: [count][M][N], X between two runs of steps, or NULL
   int runs;                // workgroups that share Gram's matrix by parts of the reduction; 0: a tile is one workgroup's
   float* partial;          // [2 runs][128 * 128]
   float *da, *dc;          // [count][Mp]: the diagonals of A and of a I + C, which are zero in A, and in C but for whole_c and split
@@ -72,7 +73,8 @@ constexpr int THIN_MAX = 64;
 inline int thin_side(int M) { return M <= 32 ? 32 : 64; }
 int thin_part(int N);
 bool muon_thin(int M, int N);
-hipError_t launch_muon_thin(const MuonArgs& a, int steps, hipStream_t st);
+// the steps in `runs` runs, Gram's matrix formed anew for each
+hipError_t launch_muon_thin(const MuonArgs& a, int steps, int runs, hipStream_t st);
 
 // All of it for other small matrices, without a workspace
 bool muon_small(int M, int N);

@@ -2,14 +2,20 @@
 //
 // With A_0 = X_0 X_0^T every step's polynomial is one in A_0, so the steps need X only before and after them:
 //   B_i = a I + b A_i + c A_i^2,  A_{i+1} = B_i A_i B_i,  Q = B_last ... B_0,  O = Q X_0
-// and the long side is read twice, whatever the number of steps: once for A_0 (gram), once for Q X_0 (apply). The steps
-// themselves (steps) are a few products of at most 64 x 64 by one workgroup. A step multiplies what rounding adds to small
-// eigenvalues by a^2 = 12, and Q's large entries cancel on large singular values: in 64 bits both stay far below fp32.
+// and the long side is read twice for several steps: once for A_0 (gram), once for Q X_0 (apply). The steps themselves (steps)
+// are a few products of at most 64 x 64 by one workgroup. But a step multiplies what rounding adds to A's small eigenvalues by
+// the derivative of lambda (a + b lambda + c lambda^2)^2, a^2 = 12 at 0, and one that rounding makes negative leaves the
+// polynomial's range in the end; and Q's large entries cancel on large singular values. So A is formed anew from X after as many
+// steps as multiply rounding by 2^29 at most (8 of the usual coefficients), from 2^-53 to below fp32's, with X kept in 64 bits
+// between: by A alone 16 steps were off by their norm and 20 infinite where the rank was below the short side. One of 256 x 8
+// takes 34 us for 8 steps, 67 for 16; 4096 of 32 x 2048 1.24 and 3.35 ms.
 //
 // What bounds them is latency: three launches, and in `steps` 17 products one after the other. One of 256 x 8: 9 + 12 + 6 us, by
 // one workgroup in one launch 33; in `steps` a short side of up to 32 takes 12 to 13 us, of 64 61, of which the matrix
 // instructions of one CU need 31. By the products of 16-bit operands, for which the short side is
 // padded to 128, two of 24 x 1577 took 333 us, here 30.
+#include <type_traits>
+
 #include "muon.h"
 
 namespace moe {
@@ -72,11 +78,26 @@ __device__ __forceinline__ f32x4 read_u(const MuonArgs& a, const MuonStack& s, s
   return a.nesterov ? u + a.momentum * m : m;
 }
 
-// Partial sums of u u^T over a part's columns, and the new momentum. Parts are always the same columns: the same bits on every run.
+// X between two runs of steps
+__device__ __forceinline__ double* kept_x(const MuonArgs& a, int b) { return a.xs + (size_t)b * a.M * a.N; }
+
+// 64 columns of it, zeros beyond its size
 template <int MB>
+__device__ __forceinline__ void read_x(const MuonArgs& a, int b, int n0, double* to) {
+  const double* const x = kept_x(a, b);
+  for (int i = threadIdx.x; i < MB * COLS; i += THR) {
+    const int j = i / COLS, n = i % COLS;
+    to[j * LD + n] = j < a.M && n0 + n < a.N ? x[(size_t)j * a.N + n0 + n] : 0.0;
+  }
+}
+
+// Partial sums of u u^T over a part's columns, and the new momentum, or of X X^T. Parts are always the same columns: the same
+// bits on every run.
+template <int MB, bool FROM_X>
 __global__ void __launch_bounds__(THR) gram_kernel(const MuonArgs a) {
   constexpr int T = MB / 16, EACH = T * T / 4;  // tiles of 16 a side, and of each of 4 waves
-  __shared__ __align__(16) float u[MB * LD];
+  using Element = std::conditional_t<FROM_X, double, float>;
+  __shared__ __align__(16) Element u[MB * LD];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, k4 = lane >> 4, b = blockIdx.y;
   const int ti = wave * EACH / T, tj = wave * EACH % T;
   const MuonStack& s = muon_stack(a, a.first + b);
@@ -89,14 +110,18 @@ __global__ void __launch_bounds__(THR) gram_kernel(const MuonArgs a) {
   const int from = blockIdx.x * a.part, to = from + a.part < a.N ? from + a.part : a.N;
   for (int n0 = from; n0 < to; n0 += COLS) {
     __syncthreads();
-    for (int i = threadIdx.x; i < MB * LD / 4; i += THR) *(f32x4*)(u + 4 * i) = f32x4{0.f, 0.f, 0.f, 0.f};
-    __syncthreads();
-    user_elements<MB>(a, s, base, n0, [&](size_t at, int j, int n, int left) {
-      const f32x4 v = read_u(a, s, at, left, whole, gs, true);
+    if constexpr (FROM_X) {
+      read_x<MB>(a, b, n0, u);
+    } else {
+      for (int i = threadIdx.x; i < MB * LD / 4; i += THR) *(f32x4*)(u + 4 * i) = f32x4{0.f, 0.f, 0.f, 0.f};
+      __syncthreads();
+      user_elements<MB>(a, s, base, n0, [&](size_t at, int j, int n, int left) {
+        const f32x4 v = read_u(a, s, at, left, whole, gs, true);
 #pragma unroll
-      for (int z = 0; z < 4; ++z)
-        if (z < left) u[s.wide ? j * LD + n + z : (j + z) * LD + n] = v[z];
-    });
+        for (int z = 0; z < 4; ++z)
+          if (z < left) u[s.wide ? j * LD + n + z : (j + z) * LD + n] = v[z];
+      });
+    }
     __syncthreads();
     for (int k = 0; k < COLS; k += 4) {
       const double p = u[(ti * 16 + l16) * LD + k + k4];
@@ -111,9 +136,9 @@ __global__ void __launch_bounds__(THR) gram_kernel(const MuonArgs a) {
     for (int r = 0; r < 4; ++r) out[((ti * T + tj + i) * 4 + r) * 64 + lane] = acc[i][r];
 }
 
-// Q and 1 / (|u| + eps) of a matrix; wave w of (MB / 16)^2 holds tile w of every matrix here
+// Q and 1 / (|u| + eps) of a matrix, 1 for sums over X itself; wave w of (MB / 16)^2 holds tile w of every matrix here
 template <int MB>
-__global__ void __launch_bounds__(MB* MB / 4) steps_kernel(const MuonArgs a, int steps) {
+__global__ void __launch_bounds__(MB* MB / 4) steps_kernel(const MuonArgs a, int steps, bool from_x) {
   constexpr int T = MB / 16, LQ = MB + 4;
   __shared__ double A[MB * LQ], B[MB * LQ], Q[MB * LQ], W[MB * LQ], traces[T * T];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, k4 = lane >> 4, ti = wave / T, tj = wave % T, b = blockIdx.x;
@@ -135,7 +160,7 @@ __global__ void __launch_bounds__(MB* MB / 4) steps_kernel(const MuonArgs a, int
   __syncthreads();
   trace = 0.0;
   for (int i = 0; i < T * T; ++i) trace += traces[i];
-  const double norm = sqrt(trace) + a.eps, f = norm == 0.0 ? 0.0 : 1.0 / norm;
+  const double norm = sqrt(trace) + a.eps, f = from_x ? 1.0 : norm == 0.0 ? 0.0 : 1.0 / norm;
 #pragma unroll
   for (int r = 0; r < 4; ++r) A[at(r)] = mine[r] * f * f;
   // rows of p times rows of q: all matrices here are symmetric
@@ -183,11 +208,12 @@ __global__ void __launch_bounds__(MB* MB / 4) steps_kernel(const MuonArgs a, int
   if (threadIdx.x == 0) out[MB * MB] = f;
 }
 
-// O = Q u / (|u| + eps) of 64 columns, or the parameters' step by it
-template <int MB>
+// O = Q u / (|u| + eps) or Q X of 64 columns: X, the user's result, or the parameters' step by it
+template <int MB, bool FROM_X, bool TO_X>
 __global__ void __launch_bounds__(THR) apply_kernel(const MuonArgs a) {
   constexpr int T = MB / 16, LQ = MB + 4;
-  __shared__ __align__(16) float u[MB * LD];
+  using Element = std::conditional_t<FROM_X, double, float>;
+  __shared__ __align__(16) Element u[MB * LD];
   __shared__ double Q[MB * LQ];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, k4 = lane >> 4, b = blockIdx.y, n0 = blockIdx.x * COLS;
   const MuonStack& s = muon_stack(a, a.first + b);
@@ -195,16 +221,20 @@ __global__ void __launch_bounds__(THR) apply_kernel(const MuonArgs a) {
   const bool whole = (s.wide ? a.N : a.M) % 4 == 0;
   const float gs = a.grad_scale ? *a.grad_scale : 1.f;
   const double* const in = a.q + (size_t)b * (MB * MB + 1);
-  for (int i = threadIdx.x; i < MB * LD / 4; i += THR) *(f32x4*)(u + 4 * i) = f32x4{0.f, 0.f, 0.f, 0.f};
   for (int i = threadIdx.x; i < MB * MB; i += THR) Q[i / MB * LQ + i % MB] = in[i];
   const double f = in[MB * MB];
-  __syncthreads();
-  user_elements<MB>(a, s, base, n0, [&](size_t at, int j, int n, int left) {
-    const f32x4 v = read_u(a, s, at, left, whole, gs, false);
+  if constexpr (FROM_X) {
+    read_x<MB>(a, b, n0, u);
+  } else {
+    for (int i = threadIdx.x; i < MB * LD / 4; i += THR) *(f32x4*)(u + 4 * i) = f32x4{0.f, 0.f, 0.f, 0.f};
+    __syncthreads();
+    user_elements<MB>(a, s, base, n0, [&](size_t at, int j, int n, int left) {
+      const f32x4 v = read_u(a, s, at, left, whole, gs, false);
 #pragma unroll
-    for (int z = 0; z < 4; ++z)
-      if (z < left) u[s.wide ? j * LD + n + z : (j + z) * LD + n] = v[z];
-  });
+      for (int z = 0; z < 4; ++z)
+        if (z < left) u[s.wide ? j * LD + n + z : (j + z) * LD + n] = v[z];
+    });
+  }
   __syncthreads();
   f64x4 acc[T];  // all rows of 16 columns
 #pragma unroll
@@ -213,6 +243,18 @@ __global__ void __launch_bounds__(THR) apply_kernel(const MuonArgs a) {
     const double x = u[(k + k4) * LD + wave * 16 + l16] * f;
 #pragma unroll
     for (int i = 0; i < T; ++i) acc[i] = product(Q[(i * 16 + l16) * LQ + k + k4], x, acc[i]);
+  }
+  if constexpr (TO_X) {  // in place: these columns are this workgroup's, and have been read
+    double* const x = kept_x(a, b);
+    const int n = n0 + wave * 16 + l16;
+#pragma unroll
+    for (int i = 0; i < T; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int j = i * 16 + k4 + 4 * r;
+        if (j < a.M && n < a.N) x[(size_t)j * a.N + n] = acc[i][r];
+      }
+    return;
   }
   __syncthreads();
 #pragma unroll
@@ -224,7 +266,7 @@ __global__ void __launch_bounds__(THR) apply_kernel(const MuonArgs a) {
   user_elements<MB>(a, s, base, n0, [&](size_t at, int j, int n, int left) {
     f32x4 v;
 #pragma unroll
-    for (int z = 0; z < 4; ++z) v[z] = z < left ? u[s.wide ? j * LD + n + z : (j + z) * LD + n] : 0.f;
+    for (int z = 0; z < 4; ++z) v[z] = z < left ? (float)u[s.wide ? j * LD + n + z : (j + z) * LD + n] : 0.f;
     if (whole) {
       if (s.m) {
         f32x4 old;
@@ -256,11 +298,23 @@ __global__ void __launch_bounds__(THR) apply_kernel(const MuonArgs a) {
   });
 }
 
-template <int MB>
+template <int MB, bool FROM_X, bool TO_X>
 void launch(const MuonArgs& a, int steps, hipStream_t st) {
-  gram_kernel<MB><<<dim3(a.parts, a.count), THR, 0, st>>>(a);
-  steps_kernel<MB><<<a.count, MB * MB / 4, 0, st>>>(a, steps);
-  apply_kernel<MB><<<dim3((a.N + COLS - 1) / COLS, a.count), THR, 0, st>>>(a);
+  gram_kernel<MB, FROM_X><<<dim3(a.parts, a.count), THR, 0, st>>>(a);
+  steps_kernel<MB><<<a.count, MB * MB / 4, 0, st>>>(a, steps, FROM_X);
+  apply_kernel<MB, FROM_X, TO_X><<<dim3((a.N + COLS - 1) / COLS, a.count), THR, 0, st>>>(a);
+}
+
+// `runs` equal runs of steps
+template <int MB>
+void launch_runs(const MuonArgs& a, int steps, int runs, hipStream_t st) {
+  if (runs == 1) return launch<MB, false, false>(a, steps, st);
+  for (int i = 0; i < runs; ++i) {
+    const int n = steps * (i + 1) / runs - steps * i / runs;
+    if (i == 0) launch<MB, false, true>(a, n, st);
+    else if (i + 1 < runs) launch<MB, true, true>(a, n, st);
+    else launch<MB, true, false>(a, n, st);
+  }
 }
 
 }  // namespace
@@ -276,10 +330,10 @@ int thin_part(int N) {
 // With a short side of up to 32 these take 28 (2 of 60 x 300: 90).
 bool muon_thin(int M, int N) { return M <= 32 || (M <= THIN_MAX && !muon_small(M, N)); }
 
-hipError_t launch_muon_thin(const MuonArgs& a, int steps, hipStream_t st) {
-  if (!muon_thin(a.M, a.N)) return hipErrorInvalidValue;
-  if (a.M <= 32) launch<32>(a, steps, st);
-  else launch<64>(a, steps, st);
+hipError_t launch_muon_thin(const MuonArgs& a, int steps, int runs, hipStream_t st) {
+  if (!muon_thin(a.M, a.N) || runs < 1 || runs > steps || (runs > 1 && !a.xs)) return hipErrorInvalidValue;
+  if (a.M <= 32) launch_runs<32>(a, steps, runs, st);
+  else launch_runs<64>(a, steps, runs, st);
   return hipGetLastError();
 }
 
