@@ -413,36 +413,45 @@ __device__ __forceinline__ Rounds take_largest(float (&v)[PL], int k) {
 template <int LN, int PL, typename Row, typename Tol>
 __device__ __forceinline__ bool settle_border(const GateArgs& a, const Place& p, const float (&v)[PL], float last, Tol tol_of, bool more, bool doubt, int q,
                                               int first_lane, Row row, uint32_t& taken) {
-  // choices of the taken, as they were
-  float c[PL];
+  auto choice = [&](int e) { return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-row(e) * 1.4426950408889634f)) + a.bias[e]; };
+  // Equal ones went in one round: where they leave more than k the k-th largest may be above the last round's. The lowest of
+  // the taken go until fewer than k would stay; they have k values at most.
+  if (__any(doubt && more)) {
+    float c[PL];
 #pragma unroll
-  for (int j = 0; j < PL; ++j) {
-    const int e = j < p.n ? p.e0 + j : 0;
-    const float x = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-row(e) * 1.4426950408889634f)) + a.bias[e];
-    c[j] = (taken >> j) & 1 ? x : -INFINITY;
-  }
-  // Equal ones went in one round: with more than k of them the k-th largest is above the last round's, unless these are what
-  // was equal. A round each of its levels, at most k.
-  float level = INFINITY;
-  int left = doubt && more ? a.k : 0;
-  for (int i = 0; i < a.k && __any(left > 0); ++i) {
-    float next = -INFINITY;
+    for (int j = 0; j < PL; ++j) {
+      const float x = choice(j < p.n ? p.e0 + j : 0);
+      c[j] = (taken >> j) & 1 ? x : INFINITY;
+    }
+    bool open = doubt && more;
+    int have = (int)run_sum<LN>((float)__popc(taken));
+    for (int i = 0; i < a.k && __any(open); ++i) {
+      float low = INFINITY;
 #pragma unroll
-    for (int j = 0; j < PL; ++j) next = larger(next, c[j] < level ? c[j] : -INFINITY);
-    level = run_max<LN>(next);
-    int equal = 0;
+      for (int j = 0; j < PL; ++j) low = c[j] < low ? c[j] : low;
+      low = run_min<LN>(low);
+      int equal = 0;
 #pragma unroll
-    for (int j = 0; j < PL; ++j) equal += c[j] == level;
-    if (left > 0) last = level;
-    left -= (int)run_sum<LN>((float)equal);
+      for (int j = 0; j < PL; ++j) {
+        equal += c[j] == low;
+        c[j] = c[j] == low ? INFINITY : c[j];
+      }
+      have -= (int)run_sum<LN>((float)equal);
+      last = open ? low : last;
+      open = open && have >= a.k;
+    }
   }
   const float tol = tol_of(last);
-  uint32_t near = 0, sure = 0;
+  uint32_t near = 0, sure = taken;
 #pragma unroll
-  for (int j = 0; j < PL; ++j) {
-    const float x = larger(c[j], v[j]);  // v is -inf where taken
-    near |= x > -INFINITY && x >= last - tol && x <= last + tol ? 1u << j : 0u;
-    sure |= x > last + tol ? 1u << j : 0u;
+  for (int j = 0; j < PL; ++j) near |= v[j] > -INFINITY && v[j] >= last - tol ? 1u << j : 0u;  // v is -inf where taken
+  for (uint32_t left = taken; doubt && left; left &= left - 1) {
+    const uint32_t bit = left & -left;
+    const float c = choice(p.e0 + __ffs((int)left) - 1);
+    if (c <= last + tol) {
+      sure &= ~bit;
+      near |= c >= last - tol ? bit : 0u;
+    }
   }
   const int counts = (int)run_sum<LN>((float)(__popc(sure) + 1024 * __popc(near)));  // at most 1024 experts of either
   int need = a.k - counts % 1024;

@@ -223,3 +223,15 @@ def test_gradients_are_rounded_once(T, E, k, score, renormalize, size):
     # of what is added and may cancel 2^-44 as well
     off = (got.cpu().double() - want).abs() - ONE_ROUNDING * want.abs() - 2.0 ** -44 * added - SMALLEST
     assert (off <= 0).all(), "%d, one %s" % ((off > 0).sum(), (got.cpu()[off > 0][0].item(), want[off > 0][0].item()))
+
+
+@pytest.mark.parametrize("T", [500, 2300])
+@pytest.mark.parametrize("E,k", [(24, 3), (64, 6), (256, 8), (300, 16), (768, 6)])
+def test_many_equal_choices(T, E, k):
+    """Logits of few values and a bias of one or two: equal choices at the border, above it, and at several values above it."""
+    g = torch.Generator().manual_seed(E + T)
+    for step, biases in ((0.25, (0.0, 0.0)), (0.5, (0.0, 0.125)), (0.015625, (0.0, 0.0))):
+        logits = (torch.randn(T, E, generator=g) / step).round() * step
+        bias = torch.tensor(biases)[torch.randint(0, 2, (E,), generator=g)]
+        idx, _ = gate(logits, bias, k, N.make_gate("sigmoid"))
+        assert torch.equal(idx, by_choices(logits, bias, k)), (step, biases)
