@@ -850,8 +850,8 @@ hipError_t launch_gate(const GateArgs& args, hipStream_t st) {
     return hipGetLastError();
   }
   // Lanes of a token. A wave a token is the shortest way for few tokens; for many, 8 to 16 experts a lane. 256 experts in 8
-  // groups: 2048 tokens 7.5 us by 64 lanes each, 8.5 by 16; 16384 tokens 29.6 by 64, 20.7 by 32, 17.2 by 16, 21.4 by 8. 64
-  // experts, 16384 tokens: 6.1 us by 8 lanes, 9.4 by 16.
+  // groups: 2048 tokens 12.3 us by 64 lanes each, 13.2 by 16 (7.0 by 64 without a doubtful token among them); 16384 tokens 33.5
+  // by 64, 31.4 by 32, 18.0 by 16, 19.1 by 8. 64 experts, 16384 tokens: 5.8 us by 8 lanes, 9.2 by 16; 512 experts: 22 by 32, 31 by 64.
   int ln = a.T <= 2048 ? 64 : a.E <= 128 ? 8 : a.E <= 256 ? 16 : a.E <= 512 ? 32 : 64;
   if (ln < a.groups) ln = a.groups;
   const int lanes = ln / a.groups, per = (a.E / a.groups + lanes - 1) / lanes;  // lanes of a group, experts of a lane

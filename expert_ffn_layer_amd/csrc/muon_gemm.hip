@@ -16,7 +16,8 @@
 // rounding would be most of the error. C's diagonal, which holds a too, multiplies the whole of X: what rounding adds to
 // directions that X lacks would grow by a = 3.4 in every step. The last step has none after it: it takes x alone, and C's
 // diagonal as the fp16 that stands in C, so that it has X to read in the product only (with SPLIT every step does: the pairs
-// hold all of both).
+// hold all of both). That adds to what five steps are off, before the result is rounded to bf16 (1.7e-3): 512 x 256 of full rank
+// 6.7e-4 for 6.2e-4, of rank 16 1.7e-3 for 1.4e-3.
 #include <algorithm>
 #include <type_traits>
 

@@ -516,9 +516,9 @@ moe_status moe_adamw(const moe_adamw_config* config, const moe_adamw_tensor* ten
  *   weights  w = scale s, divided by the sum of the chosen s with renormalize. The bias is not in them.
  * An expert whose logit or bias is -inf is never chosen: where fewer than k can be, the rest of the row is expert -1
  * with weight 0, which moe_permute skips and moe_combine leaves out (as in moe_route_hash). Equal choices, and equal
- * groups, go to the lower index. Choices are formed and compared in 64 bits, so they count as equal only where they
- * differ by less than about 2^-50; weights are rounded once, to fp32. NaN is the largest choice, and reaches the weights
- * as the formulas say.
+ * groups, go to the lower index. The order is that of the choices in 64 bits, so that they count as equal only where they
+ * differ by less than about 2^-50 of the largest of 1 and the biases that are added; weights are formed in 64 bits and
+ * rounded once, to fp32. NaN is the largest choice, and reaches the weights as the formulas say.
  */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 
@@ -550,7 +550,7 @@ moe_status moe_gate(const moe_shape* shape, const moe_gate_rule* rule, const flo
  *   logits, topk_idx  moe_gate's; an entry outside [0, E) or with a logit of -inf takes no part, equal ones add up
  *   dtopk_w  float[T][k] (moe_combine_backward's); not read where the entry takes no part
  *   dlogits  float[T][E] out, every element written; may be logits' memory
- * The bits of a token's result depend on that token alone. Other rules as moe_gate.
+ * Formed in 64 bits and rounded once. The bits of a token's result depend on that token alone. Other rules as moe_gate.
  */
 moe_status moe_gate_backward(const moe_shape* shape, const moe_gate_rule* rule, const float* logits,
                              const int32_t* topk_idx, const float* dtopk_w, float* dlogits, moe_stream_t stream);
@@ -578,10 +578,13 @@ moe_status moe_layer_forward_gated(const moe_shape* shape, const moe_gate_rule* 
  *   X_{i+1} = a X_i + (b A + c A^2) X_i with A = X_i X_i^T, on the side of fewer rows or columns
  * so that each step takes a singular value s to a s + b s^3 + c s^5. Every matrix of a stack is on its own: one with an
  * element that is not finite becomes NaN, the others do not change.
- * Precision by type: MOE_F32 forms the products of pairs of 16-bit numbers with fp32 sums (about 22 bits); MOE_BF16 those
- * of fp16 numbers with fp32 sums, X itself (but in the last step) and the diagonals of A and its polynomial wider: off by
- * about 0.0007 of its norm before it is rounded to bf16, which is 0.0017, up to 0.003 where the rank is a few. A shorter side
- * of up to 32 (64 where the longer exceeds 256) is worked on in 64 bits. The same bits on every run: no atomics.
+ * Precision by type: MOE_F32 forms the products of pairs of 16-bit numbers with fp32 sums (about 22 bits) and is off by 0.3
+ * to 1.5 times as much as fp32 products; MOE_BF16 those of fp16 numbers with fp32 sums, X itself and the diagonals of A and
+ * its polynomial wider but in the last step: five steps are off by about 0.0007 of O's norm before it is rounded to bf16,
+ * which is 0.0017, and by up to 0.004 where the rank is a few (0.005 for an fp32 gradient). What rounding adds in directions
+ * that X lacks is enlarged by a in every further step: eight usual steps are off by 0.001 at full rank, by up to 0.015 where a
+ * bf16 gradient's rank is a few and by 0.1 where an fp32 gradient's is, ten by 0.0015, 0.015 and as much as O itself. A shorter
+ * side of up to 32 (64 where the longer exceeds 256) is worked on in 64 bits. The same bits on every run: no atomics.
  */
 typedef struct {
   int32_t steps;  /* 1..32 */
