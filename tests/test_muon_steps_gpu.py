@@ -7,7 +7,7 @@ import torch
 from expert_ffn_layer_amd import native as N
 
 from _gpu import say
-from _muon import NS, newton_schulz, off, step_errors
+from _muon import NS, newton_schulz, off, plain_steps, step_errors
 from test_muon_gpu import DEV, DT, Step, gen_of, matrices, orthogonalize, verify, workspace
 
 pytestmark = pytest.mark.gpu
@@ -189,3 +189,68 @@ def test_step_by_other_numbers_of_steps(steps, p, g, master, tall):
         want[i] = (old * (1 - 0.02 * 0.1) - size * o, size * e * o.square().sum((1, 2)).sqrt(), 2.0 ** -22 * (old.abs() + (size * o).abs()), *want[i][3:])
     s.run(0.02, 0.9, True, 0.1, steps=steps)
     s.verify(want)
+
+
+def pair_steps(g, steps=5, coef=NS, eps=1e-7):
+    """The steps with the operands of fp32 matrices' products as pairs of fp16, whose lower halves are not multiplied with each
+    other, and nothing else rounded."""
+    a, b, c = coef
+    S = 4096.0
+
+    def pair(t):
+        hi = t.half().double()
+        return hi, (t - hi).half().double()
+
+    def product(p, q):
+        (ph, pl), (qh, ql) = pair(p), pair(q)
+        return torch.bmm(ph + pl, qh + ql) - torch.bmm(pl, ql)
+    x = g.double()
+    x = x * (S / (x.square().sum((1, 2), keepdim=True).sqrt() + eps))
+    wide = x.shape[1] <= x.shape[2]
+    x = x if wide else x.transpose(1, 2).contiguous()
+    one = torch.eye(x.shape[1], dtype=torch.float64, device=x.device)
+    for _ in range(steps):
+        A = product(x, x.transpose(1, 2).contiguous()) / S
+        d = torch.diag_embed(torch.diagonal(A, dim1=1, dim2=2))
+        C = b * A + c * (product(A - d, A - d) + torch.bmm(d, A) + torch.bmm(A, d) - torch.bmm(d, d)) / S + a * S * one
+        x = product(C, x) / S
+    x = x / S
+    return x if wide else x.transpose(1, 2).contiguous()
+
+
+@pytest.mark.parametrize("rank", [0, 16, 1])
+@pytest.mark.parametrize("z", [z for z in KINDS if min(z[1:]) > 64])
+def test_error_of_fp32(z, rank):
+    """That of the operands, which pair_steps has, twice for single operands that go the other way, and that of fp32 sums, which
+    fp32 products have: three sums of the same length in place of one, sqrt(3) < 2 times."""
+    g = gen_of(rank)
+    x = torch.randn(z, generator=g, device=DEV) if rank == 0 else low_rank(*z, rank, "f32", rank) + (0.0 if rank == 1 else torch.randn(z, generator=g, device=DEV))
+    want = newton_schulz(x)
+    got, plain, pairs = off(orthogonalize(x, "f32"), want), off(plain_steps(x), want), off(pair_steps(x), want)
+    say(z, rank, "error", got.max().item(), "fp32 products", plain.max().item(), "pairs", pairs.max().item())
+    assert (got <= 2 * plain + 2 * pairs + 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_many_steps_in_graphs_and_in_bounds(kind):
+    """Thin matrices, whose X passes through the workspace: two graphs that share one, other bytes in it, and what lies behind."""
+    for z in ((3, 40, 700), (2, 900, 31), (5, 7, 9)):
+        g = matrices(*z, kind, seed=z[1])
+        n, need = g.numel(), N.moe_orthogonalize_workspace_size(kind, *z)
+        ws = torch.full((need + 4096,), 0xAB, dtype=torch.uint8, device=DEV)
+        outs = [torch.full((n + 64,), 5.0, dtype=DT[kind], device=DEV) for _ in range(2)]
+        orthogonalize(g, kind, steps=12)
+        torch.cuda.synchronize()
+        graphs = [torch.cuda.CUDAGraph() for _ in outs]
+        for graph, o in zip(graphs, outs):
+            with torch.cuda.graph(graph):
+                N.moe_orthogonalize(g, o[:n].reshape(z), ws[:need], steps=12)
+        for i in range(3):
+            g.copy_(torch.randn(z, device=DEV))
+            ws[:need].fill_(0x11 * i)
+            for graph in graphs:
+                graph.replay()
+            want = orthogonalize(g, kind, steps=12)
+            torch.cuda.synchronize()
+            assert all(torch.equal(o[:n].reshape(z), want) for o in outs), "replay %d" % i
+        assert all((o[n:] == 5.0).all() for o in outs) and (ws[need:] == 0xAB).all()
