@@ -763,7 +763,7 @@ __global__ void __launch_bounds__(64 * WAVES) gate_backward_kernel(const GateArg
   const double rest = score.rest;
   double d = dw;
   if (a.renormalize) {
-    r *= 1.0 / reduce64(r, LN, sum64);
+    r /= reduce64(r, LN, sum64);  // 1 of one alone, whose gradient is 0
     r = here ? r : 0.0;
     d = dw - reduce64(r * dw, LN, sum64);
   }

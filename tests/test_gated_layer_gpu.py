@@ -215,3 +215,55 @@ def test_router_step():
     assert torch.equal(m, grad)
     d = ((W.double() - before + 0.1 * o[0]).abs() - 2.0 ** -22 * (before.abs() + 0.1 * o[0].abs())).clamp(min=0)
     assert d.norm() <= 0.1 * e[0] * o.norm()
+
+
+@pytest.mark.parametrize("spec", LAYERS, ids=[s.name for s in LAYERS])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_training_with_experts_that_are_off(spec, score, renormalize):
+    """Fewer experts than k: pairs that are nobody's, in memory that held NaN, reach neither the outputs nor the gradients."""
+    say("experts off", spec.name, score, renormalize)
+    gen, dtype = gen_of(spec.seed + 1), DT[spec.act]
+    H, E, k, T = spec.H, spec.E, spec.k, spec.T
+    routed_, shared = matrices(gen, spec, E), matrices(gen, spec) if spec.shared else None
+    Wr = (torch.randn(H, E, generator=gen, device=DEV) * H ** -0.5).to(dtype)
+    lay = TrainableLayer(spec, Wr, routed_, shared, rule=N.make_gate(score, renormalize=renormalize))
+    x, dy = ((torch.randn(T, H, generator=gen, device=DEV)).to(dtype) for _ in range(2))
+    for on in (1, 0, k - 1):
+        bias = torch.zeros(E, device=DEV)
+        bias[torch.randperm(E, generator=gen, device=DEV)[:E - on]] = -math.inf
+        for t in (*lay.y, *lay.dx, lay.dy_perm, *[p for pair in lay.pre for p in pair]):
+            t.fill_(math.nan)
+        y = lay.forward(x, bias)
+        dx, dlogits = lay.backward(dy)
+        assert (lay.idx[:, on:] == -1).all() and (lay.idx[:, :on] >= 0).all()
+        l = (x.double() @ Wr.double()).requires_grad_()
+        leaves = {"x": x.double().requires_grad_()} | {"r" + n: t.double().requires_grad_() for n, t in routed_.items()}
+        if shared is not None:
+            leaves |= {"s" + n: t.double().requires_grad_() for n, t in shared.items()}
+        s = torch.sigmoid(l) if score == "sigmoid" else torch.softmax(l, 1)
+        w = s.gather(1, lay.idx[:, :on].long())
+        if renormalize and on:
+            w = w / w.sum(1, keepdim=True)
+
+        def ffn(tag, e):
+            g = leaves["x"] @ leaves[tag + "gate"][e]
+            return (g * torch.sigmoid(g) * (leaves["x"] @ leaves[tag + "up"][e])) @ leaves[tag + "down"][e]
+        rows = torch.stack([ffn("r", e) for e in range(E)], 1)
+        want = (rows.gather(1, lay.idx[:, :on].long()[:, :, None].expand(T, on, H)) * w[:, :, None]).sum(1)
+        if shared is not None:
+            want = want + ffn("s", ...)
+        want.backward(dy.double())
+        got = {"x": dx} | {"r" + n: t for n, t in lay.grads[0].items()} | ({"s" + n: t for n, t in lay.grads[1].items()} if shared is not None else {})
+        # up to 8 roundings of half a step on each path, in norm
+        tol = 8 * half_step(dtype) + 1e-5
+
+        def near(a, b):  # zeros have to be zeros
+            return (a.double() - b).norm() <= tol * b.norm()
+        assert near(y, want.detach())
+        for n, t in got.items():
+            assert near(t, leaves[n].grad), (on, n)
+        if on == 0 or (on == 1 and renormalize):  # no weight, or one that is the scale
+            assert (dlogits == 0).all()
+        else:
+            assert near(dlogits, l.grad)
